@@ -548,3 +548,12 @@ gemm_smallm_static = nvfp4_gemm_smallm_static
 workspace = nvfp4_workspace
 device_status = nvfp4_device_status
 read_probe = nvfp4_read_probe
+
+
+# ---- the paged key/value cache --------------------------------------------------
+
+from . import kv as _kv  # noqa: E402
+from .kv import *  # noqa: E402,F401,F403
+
+SIGNATURES.update(_kv.SIGNATURES)
+__all__ += _kv.__all__

@@ -1,0 +1,466 @@
+"""The paged NVFP4 cache on the GPU through the public entry points: block
+tables against a loop over requests, appended bytes against the oracle's
+quantiser, attention against its definition in 64 bits."""
+import itertools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from kv_helpers import attention, check_attention, page_values
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_w4a4_decode_gb300 as nvmod
+    from nvfp4_w4a4_decode_gb300 import build as nvbuild
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    nvbuild.build()
+    oracle.build()
+    nvmod.library()
+    nvmod.device_status(clear=True)
+    return nvmod
+
+
+def ints(v, dtype=torch.int32):
+    return torch.tensor(v, dtype=dtype, device="cuda")
+
+
+# ---- block tables ----------------------------------------------------------------
+
+def tables_by_hand(past, new, page, free, head, table, tokens):
+    """The header's definition, one request and one token at a time."""
+    table = [list(row) for row in table]
+    cap = len(table[0]) * page if table else 0
+    seq, start, slots, positions = [], [0], [], []
+    for r, (n, c) in enumerate(zip(past, new)):
+        n, c = max(n, 0), max(c, 0)
+        end = min(n + c, cap)
+        held = -(-min(n, cap) // page)
+        for b in range(held, -(-end // page)):
+            table[r][b] = free[head] if 0 <= head < len(free) else -1
+            head += 1
+        for pos in range(n, n + c):
+            p = table[r][pos // page] if pos < end else -1
+            positions.append(pos)
+            slots.append(p * page + pos % page if p >= 0 else -1)
+        seq.append(end)
+        start.append(start[-1] + c)
+    pad = tokens - len(slots)
+    return table, seq, start, (slots + [-1] * pad)[:tokens], (positions + [0] * pad)[:tokens], head
+
+
+def run_tables(nv, past, new, page, blocks, free, head, tokens=None, table=None):
+    tokens = sum(max(c, 0) for c in new) if tokens is None else tokens
+    if table is None:
+        table, nxt = [], 100000
+        for n in past:
+            held = -(-min(max(n, 0), blocks * page) // page)
+            table.append([nxt + i if i < held else -7 for i in range(blocks)])
+            nxt += held
+    want = tables_by_hand(past, new, page, free, head, table, tokens)
+    td = ints(table).reshape(len(past), blocks)
+    args = (ints(past), ints(new), ints(free), ints([head]), td)
+    for _ in range(2):  # the second call repeats the first
+        got = nv.kv_tables(*args, page_size=page, tokens=tokens)
+        assert td.tolist() == want[0]
+        assert got.seq_len.tolist() == want[1]
+        assert got.q_start.tolist() == want[2]
+        assert got.slots.tolist() == want[3]
+        assert got.positions.tolist() == want[4]
+        assert got.free_head.tolist() == [want[5]]
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("reqs,seed", [(1, 0), (7, 1), (513, 2), (1500, 3)])
+def test_tables(nv, page, reqs, seed):
+    rng = np.random.default_rng(seed + page)
+    past = rng.integers(0, 5 * page, reqs).tolist()
+    new = rng.integers(0, 2 * page if reqs < 100 else 9, reqs).tolist()
+    past[0], new[-1] = 2 * page, page + 1            # a full last page, more than one new page
+    nv.device_status(clear=True)
+    run_tables(nv, past, new, page, 8, list(range(5, 5 + 8 * reqs)), 3)
+    assert nv.device_status() == 0
+
+
+def test_tables_edges(nv):
+    nv.device_status(clear=True)
+    run_tables(nv, [0, 0], [0, 0], 16, 4, [1, 2, 3], 0, tokens=0)       # nothing new
+    run_tables(nv, [0, 0], [0, 0], 16, 4, [1, 2, 3], 0, tokens=5)       # only padding
+    run_tables(nv, [15, 16, 17], [1, 1, 1], 16, 2, [9, 8], 0, tokens=8)  # page ends, padding
+    run_tables(nv, [-3, 5], [2, -1], 16, 2, [9, 8], 0, tokens=4)        # negative counts as 0
+    run_tables(nv, [], [], 16, 0, [4], 0, tokens=3, table=[])           # no requests
+    assert nv.device_status() == 0
+
+
+def test_tables_too_short_are_reported(nv):
+    for past, new, blocks, free, head in (([0, 0], [40, 40], 4, [5, 6, 7, 8], 0),    # free list ends
+                                          ([0], [20], 4, [5, 6, 7], -1),             # head below 0
+                                          ([30, 100], [10, 4], 2, [5, 6, 7], 0)):    # table ends
+        nv.device_status(clear=True)
+        run_tables(nv, past, new, 16, blocks, free, head)
+        assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+    nv.device_status(clear=True)
+    run_tables(nv, [0, 3], [5, 5], 16, 2, [5, 6, 7], 0, tokens=7)  # fewer rows than new tokens
+    assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+
+
+def test_tables_largest(nv):
+    reqs = 16384
+    past = ints(np.arange(reqs) % 33)
+    new = torch.ones(reqs, dtype=torch.int32, device="cuda")
+    table = torch.full((reqs, 4), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.arange(reqs, device="cuda") + 50000
+    table[:, 1] = torch.arange(reqs, device="cuda") + 90000
+    free = torch.randperm(reqs, device="cuda").to(torch.int32)
+    got = nv.kv_tables(past, new, free, ints([0]), table, page_size=16, tokens=reqs)
+    page = table.gather(1, (past // 16)[:, None].long())[:, 0]
+    assert torch.equal(got.slots, page.long() * 16 + past % 16)
+    assert got.free_head.item() == (past % 16 == 0).sum().item()
+    assert torch.equal(got.q_start, torch.arange(reqs + 1, device="cuda", dtype=torch.int32))
+
+
+# ---- append ----------------------------------------------------------------------
+
+def make_cache(nv, pages, heads, dim, page, kg, vg, layers=1, layer=0, fill=None):
+    """A cache over one layer of a pool of `layers` (strided pages)."""
+    whole = nv.kv_pool(pages * layers, heads, dim, page)
+    if fill is None:
+        whole.random_(0, 256)
+    else:
+        whole.fill_(fill)
+    pool = whole.view(pages, layers, heads, -1)[:, layer]
+    return nv.KVCache(pool, kg, vg, page_size=page, head_dim=dim), whole
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("heads,dim,page,tokens,layers",
+                         [(8, 128, 16, 1, 1), (8, 128, 64, 200, 2), (1, 64, 16, 37, 1),
+                          (3, 64, 32, 65, 1), (5, 128, 128, 33, 3), (32, 128, 256, 40, 1)])
+def test_append_bytes(nv, dtype, heads, dim, page, tokens, layers):
+    gen = torch.Generator(device="cuda").manual_seed(heads * dim + page)
+    rows = torch.randn((tokens, 3 * heads + 1, dim), generator=gen, device="cuda")
+    # block scales from subnormal to saturated, blocks of zeros, signed zeros
+    rows *= torch.exp2(torch.randint(-14, 4, (tokens, 3 * heads + 1, 1), generator=gen, device="cuda"))
+    rows[::5, :, :16] = 0.0
+    rows[1::5, :, :16] = -0.0
+    rows = rows.to(dtype)
+    k, v = rows[:, :heads], rows[:, heads:2 * heads]
+    kg, vg = ints([0.0011], FP32), ints([0.0002], FP32)
+    pages = -(-tokens // page) + 5
+    cache, whole = make_cache(nv, pages, heads, dim, page, kg, vg, layers, layers - 1)
+    before = whole.clone()
+    slots = torch.randperm(pages * page, generator=gen, device="cuda")[:tokens].contiguous()
+    slots[::7] = -1
+    nv.device_status(clear=True)
+    nv.kv_append(cache, k, v, slots)
+    assert nv.device_status() == 0
+    want = before.clone()
+    mine = want.view(pages, layers, heads, -1)[:, layers - 1]
+    half, block = page * dim // 2, page * dim // 16
+    for part, (x, g) in enumerate(((k, kg), (v, vg))):
+        q, s = oracle.quantize(x.float().cpu().numpy().reshape(tokens * heads, dim), np.float32(g.item()))
+        q = torch.from_numpy(q).cuda().view(tokens, heads, -1)
+        s = torch.from_numpy(s).cuda().view(tokens, heads, -1)
+        for t in range(tokens):
+            if slots[t] < 0:
+                continue
+            p, o = divmod(slots[t].item(), page)
+            at = part * half + o * dim // 2
+            mine[p, :, at:at + dim // 2] = q[t]
+            at = 2 * half + part * block + o * dim // 16
+            mine[p, :, at:at + dim // 16] = s[t]
+    assert torch.equal(whole, want)
+
+
+def test_append_bad_slots_are_skipped_and_reported(nv):
+    kg = ints([0.01], FP32)
+    cache, whole = make_cache(nv, 4, 2, 64, 16, kg, kg)
+    before = whole.clone()
+    k = torch.randn((5, 2, 64), device="cuda")
+    nv.device_status(clear=True)
+    nv.kv_append(cache, k, k, ints([64, -2, 1 << 40, -(1 << 40), -1], torch.int64))
+    assert torch.equal(whole, before)
+    assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+    nv.kv_append(cache, k[:0], k[:0], ints([], torch.int64))
+    nv.kv_append(cache, k[:1], k[:1], ints([-1], torch.int64))
+    assert torch.equal(whole, before) and nv.device_status() == 0
+
+
+# ---- attention -------------------------------------------------------------------
+
+def filled(nv, seqs, heads, dim, page, seed=0, layers=1, stale=255, blocks=None, dtype=FP32,
+           gain=1.0):
+    """A cache holding `seqs` tokens a request on scattered pages (all else 0xFF:
+    NaN scales), and its block table (unused entries far outside the pool)."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-n // page) for n in seqs]
+    pages = sum(need) + 3
+    blocks = max(max(need, default=0), 1) + 2 if blocks is None else blocks
+    kg, vg = ints([gain * 5 / 2688], FP32), ints([4.5 / 2688], FP32)
+    cache, whole = make_cache(nv, pages, heads, dim, page, kg, vg, layers, layers - 1, fill=stale)
+    order = torch.randperm(pages, generator=gen, device="cuda").tolist()
+    table = torch.full((len(seqs), blocks), 1 << 30, dtype=torch.int32)
+    slots = []
+    for r, (n, m) in enumerate(zip(seqs, need)):
+        mine = [order.pop() for _ in range(m)]
+        table[r, :m] = torch.tensor(mine, dtype=torch.int32)
+        slots += [mine[i // page] * page + i % page for i in range(n)]
+    total = len(slots)
+    k = torch.randn((total, heads, dim), generator=gen, device="cuda") * gain
+    v = torch.randn((total, heads, dim), generator=gen, device="cuda")
+    nv.kv_append(cache, k.to(dtype), v.to(dtype), ints(slots, torch.int64))
+    return cache, table.cuda(), gen
+
+
+def starts(counts):
+    return ints(list(itertools.accumulate(counts, initial=0)))
+
+
+def run_attention(nv, seqs, counts, hq, hkv, dim, page, q_dtype=BF16, out_dtype=None, window=0,
+                  scale=None, seed=0, layers=1, uniform=False, max_q="known", gain=1.0, **more):
+    cache, table, gen = filled(nv, seqs, hkv, dim, page, seed, layers, gain=gain)
+    rows = torch.randn((sum(counts), hq + 2 * hkv, dim), generator=gen, device="cuda").to(q_dtype)
+    q = rows[:, :hq]
+    nv.device_status(clear=True)
+    out, lse = nv.kv_attention(cache, q, table, ints(seqs), None if uniform else starts(counts),
+                               max_q=max(counts, default=0) if max_q == "known" else max_q, scale=scale,
+                               window=window, out_dtype=out_dtype, return_lse=True, **more)
+    assert nv.device_status() == 0
+    assert out.dtype == (out_dtype or q_dtype)
+    ref = attention(cache, q, table, seqs, counts, scale, window)
+    check_attention(out, lse, ref, q_dtype)
+    return cache, q, table, out, lse
+
+
+@pytest.mark.parametrize("q_dtype,out_dtype", [(BF16, BF16), (FP32, FP32), (BF16, FP32), (FP32, BF16)])
+@pytest.mark.parametrize("dim,page", [(128, 16), (64, 64)])
+def test_single_tokens(nv, q_dtype, out_dtype, dim, page):
+    """One token a request, lengths around every boundary, an empty request."""
+    seqs = [1, 0, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 1000]
+    run_attention(nv, seqs, [1] * len(seqs), 8, 2, dim, page, q_dtype, out_dtype)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (10, 2), (7, 1), (8, 1), (9, 1), (16, 1), (34, 2),
+                                    (40, 1), (64, 1), (32, 32)])
+def test_head_groups(nv, hq, hkv):
+    run_attention(nv, [77, 300], [1, 1], hq, hkv, 128, 32, seed=hq)
+    run_attention(nv, [50], [1], hq, hkv, 64, 16, FP32, seed=hq)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_pages_and_layers(nv, page, dtype):
+    run_attention(nv, [page * 3 - 1, page, page + 1, 5], [1, 2, 3, 4], 8, 4, 128, page, dtype, layers=3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("counts", [[2, 1, 0, 5], [16, 9], [3, 40, 1], [130, 0, 33], [300]])
+@pytest.mark.parametrize("past", [0, 1, 95])
+def test_several_tokens(nv, dtype, dim, counts, past):
+    """Drafted tokens, chunks and whole prompts: the causal edge inside tiles."""
+    run_attention(nv, [c + past if c else 0 for c in counts], counts, 8, 2, dim, 16, dtype, seed=past)
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 5000])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_window(nv, window, dtype):
+    run_attention(nv, [400, 90, 1, 200], [1, 1, 1, 1], 8, 2, 128, 32, dtype, window=window)
+    run_attention(nv, [400, 90, 7], [37, 90, 7], 8, 2, 64, 16, dtype, window=window)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_long(nv, dtype):
+    """A request cut between many SMs, beside short ones and empty ones."""
+    run_attention(nv, [20011, 0, 3, 4096, 0], [1] * 5, 8, 2, 128, 64, dtype)
+    run_attention(nv, [9001, 10, 700], [5, 2, 1], 16, 2, 64, 16, dtype)
+
+
+def test_many_requests(nv):
+    rng = np.random.default_rng(5)
+    seqs = rng.integers(0, 60, 700).tolist()
+    run_attention(nv, seqs, [1] * 700, 4, 2, 64, 16)
+    counts = [int(min(n, c)) for n, c in zip(seqs, rng.integers(0, 4, 700))]
+    run_attention(nv, seqs, counts, 4, 2, 64, 16)
+
+
+def test_more_rows_than_tokens(nv):
+    """Rows at positions below 0 (and requests whose cache is empty) see nothing."""
+    run_attention(nv, [3, 0, 20], [8, 4, 40], 8, 2, 64, 16)
+    run_attention(nv, [3, 0, 20], [8, 4, 200], 8, 2, 128, 16, FP32)
+
+
+def test_scale_and_hints(nv):
+    for max_q in (0, 1, 1000, None):
+        run_attention(nv, [60, 500], [20, 3], 8, 2, 128, 16, scale=0.3, max_q=max_q)
+    run_attention(nv, [60, 500, 8], [4, 4, 4], 8, 2, 128, 16, FP32, scale=-0.1, uniform=True)
+    run_attention(nv, [60, 500], [1, 1], 8, 2, 64, 16, scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_peaked_and_growing_scores(nv, dtype):
+    """Scores of hundreds that keep rising along the request: the reference is raised many times."""
+    cache, table, gen = filled(nv, [600, 600], 1, 64, 16, gain=1.0)
+    q = torch.randn((2, 4, 64), generator=gen, device="cuda")
+    k = torch.arange(600, device="cuda")[:, None, None] * (q[0, :1] / 100)
+    k = torch.cat([k, k.flip(0)])
+    v = torch.randn((1200, 1, 64), generator=gen, device="cuda")
+    cache.k_g.copy_(nv.global_scale(k.contiguous()))
+    slots = torch.cat([table[r, :38].long().repeat_interleave(16)[:600] * 16
+                       + torch.arange(600, device="cuda") % 16 for r in range(2)])
+    nv.kv_append(cache, k, v, slots)
+    q = (q[:1] * 10).expand(2, 4, 64).contiguous().to(dtype)
+    out, lse = nv.kv_attention(cache, q, table, ints([600, 600]), return_lse=True)
+    check_attention(out, lse, attention(cache, q, table, [600, 600], [1, 1]), dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_query_magnitudes(nv, dtype):
+    """Query rows of very large, very small, zero and mixed elements."""
+    cache, table, gen = filled(nv, [100], 1, 128, 16)
+    q = torch.randn((1, 6, 128), generator=gen, device="cuda")
+    q[0, 0] *= 2.0 ** 90
+    q[0, 1] *= 2.0 ** -90
+    q[0, 2] = 0.0
+    q[0, 3, ::2] *= 2.0 ** -12
+    q[0, 4] *= 2.0 ** -126
+    q = q.to(dtype)
+    for scale, rows in ((2.0 ** -90, [0]), (2.0 ** 90, [1]), (0.1, [2, 3, 4, 5])):
+        out, lse = nv.kv_attention(cache, q, table, ints([100]), scale=scale, return_lse=True)
+        ref = attention(cache, q, table, [100], [1], scale)
+        check_attention(out[:, rows], lse[:, rows], [x[:, rows] for x in ref], dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_nonfinite_query_stays_in_its_row(nv, dtype, bad):
+    cache, table, gen = filled(nv, [40, 90], 2, 64, 16)
+    q = torch.randn((4, 8, 64), generator=gen, device="cuda")
+    clean = q.clone()
+    q[2, 3, 7] = bad
+    out, lse = nv.kv_attention(cache, q.to(dtype), table, ints([40, 90]), starts([1, 3]), return_lse=True)
+    ref = attention(cache, clean.to(dtype), table, [40, 90], [1, 3])
+    keep = torch.ones((4, 8), dtype=torch.bool, device="cuda")
+    keep[2, 3] = False
+    assert not torch.isfinite(out[2, 3]).any()
+    check_attention(out[keep][None], lse[keep][None], [x[keep][None] for x in ref], dtype)
+
+
+def test_zero_tensor_scales(nv):
+    cache, table, gen = filled(nv, [50], 2, 128, 16)
+    cache.k_g.zero_()
+    q = torch.randn((1, 8, 128), generator=gen, device="cuda")
+    out, lse = nv.kv_attention(cache, q, table, ints([50]), return_lse=True)
+    check_attention(out, lse, attention(cache, q, table, [50], [1]), FP32)
+    cache.v_g.zero_()
+    assert not nv.kv_attention(cache, q, table, ints([50])).any()
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [7, 1, 30], [200, 1, 150]])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_workspace_and_repeats(nv, counts, dtype):
+    """The same bits every time; the workspace is zero again after each call as
+    far as its counters go, can be shared by calls of any shape, and may be left out."""
+    seqs = [9000, 300, 5000]
+    ws = nv.kv_attention_workspace(128)
+    cache, q, table, out, lse = run_attention(nv, seqs, counts, 8, 2, 128, 64, dtype, workspace=ws)
+    for _ in range(3):
+        o2, l2 = nv.kv_attention(cache, q, table, ints(seqs), starts(counts), max_q=max(counts),
+                                 return_lse=True, workspace=ws)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+        run_attention(nv, [3000, 5], [1, 1], 8, 2, 128, 64, dtype, workspace=ws)
+    run_attention(nv, seqs, counts, 8, 2, 128, 64, dtype, workspace=False)
+    run_attention(nv, seqs, counts, 8, 2, 128, 64, dtype, workspace=ws[:64])
+
+
+def test_output_tensors_and_strides(nv):
+    cache, table, gen = filled(nv, [70, 9], 2, 64, 16)
+    q = torch.randn((2, 8, 64), generator=gen, device="cuda").to(BF16)
+    want = nv.kv_attention(cache, q, table, ints([70, 9]))
+    wide = torch.full((2, 20, 64), 7.0, dtype=BF16, device="cuda")
+    got = nv.kv_attention(cache, q, table[:, :6], ints([70, 9]), out=wide[:, 4:12])
+    assert torch.equal(got, want) and (wide[:, :4] == 7).all() and (wide[:, 12:] == 7).all()
+    # rows that belong to no request are left alone
+    out = torch.full((4, 8, 64), 7.0, dtype=BF16, device="cuda")
+    nv.kv_attention(cache, torch.cat([q, q]), table, ints([70, 9]), ints([1, 2, 3]), out=out)
+    assert (out[[0, 3]] == 7).all() and torch.equal(out[1], nv.kv_attention(
+        cache, q[1:], table[:1], ints([70]))[0])
+
+
+def test_bad_entries_are_reported(nv):
+    """Page ids outside the pool (within the pages a request needs), lengths past the table."""
+    cache, table, gen = filled(nv, [70, 40], 2, 64, 16)
+    q = torch.randn((2, 8, 64), generator=gen, device="cuda")
+    good = nv.kv_attention(cache, q, table, ints([70, 40]))
+    for value in (-1, cache.num_pages, 1 << 30):
+        broken = table.clone()
+        broken[0, 2] = value
+        nv.device_status(clear=True)
+        out = nv.kv_attention(cache, q, broken, ints([70, 40]))
+        assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+        assert torch.equal(out[1], good[1])
+    nv.device_status(clear=True)
+    nv.kv_attention(cache, q, table[:, :3], ints([70, 40]))
+    assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+    nv.kv_attention(cache, q, table, ints([70, 40]), ints([-5, 1, 99]))
+    nv.device_status(clear=True)
+
+
+def test_offsets_past_32_bits(nv):
+    """A pool of over 8 GB whose last pages are used."""
+    page, heads, dim = 256, 8, 128
+    pages = (9 << 30) // nv.kv_page_bytes(page, heads, dim)
+    kg = ints([5 / 2688], FP32)
+    cache, whole = make_cache(nv, pages, heads, dim, page, kg, kg, fill=0)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn((300, heads, dim), generator=gen, device="cuda")
+    slots = torch.arange(300, device="cuda") + (pages - 2) * page
+    nv.kv_append(cache, k, k, slots)
+    table = ints([[pages - 2, pages - 1]])
+    q = torch.randn((1, 32, dim), generator=gen, device="cuda").to(BF16)
+    out, lse = nv.kv_attention(cache, q, table, ints([300]), return_lse=True)
+    check_attention(out, lse, attention(cache, q, table, [300], [1]), BF16)
+    kk, _ = page_values(cache.pool[-2:], page, dim)
+    assert (kk[0].transpose(0, 1) * kg.double() - k[:256].double()).abs().max() < 1.0
+
+
+def test_streams_and_graphs(nv):
+    """A step on a side stream and in a captured graph gives the eager bits."""
+    seqs, page = [100, 3000, 15], 16
+    cache, table, gen = filled(nv, seqs, 2, 64, page, blocks=200)
+    k = torch.randn((3, 2, 64), generator=gen, device="cuda").to(BF16)
+    q = torch.randn((3, 8, 64), generator=gen, device="cuda").to(BF16)
+    free = ints([cache.num_pages - 1 - i for i in range(3)])
+    new, head = ints([1, 1, 1]), ints([0])
+
+    def step(lens, pdl):
+        t = nv.kv_tables(lens, new, free, head, table, page_size=page, tokens=3, pdl=pdl)
+        nv.kv_append(cache, k, k, t.slots, pdl=pdl)
+        return nv.kv_attention(cache, q, table, t.seq_len, t.q_start, max_q=1, pdl=pdl), t.seq_len
+
+    lens = ints(seqs)
+    want, seq = step(lens, False)
+    want = want.clone()
+    assert seq.tolist() == [101, 3001, 16]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got, _ = step(lens, True)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, _ = step(lens, True)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert torch.equal(step(lens, False)[0], want)
