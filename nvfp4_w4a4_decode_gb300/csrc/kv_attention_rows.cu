@@ -16,18 +16,24 @@
 // Layout.  The query rows (token, head of the group) are the narrow side of
 // m16n8k16 tiles, 8 NT of them: S^T = K Q^T and O^T = V^T P^T, so a single
 // token of a group of 4 to 8 heads fills the tile and the 4-bit cache is
-// decoded once for all of them.  A warp takes 16 tokens at a time: lane
+// decoded once for all of them.  A warp takes 16 tokens a tile, two tiles at a time: lane
 // (g, t) = (lane / 4, lane % 4) reads K of token rows g, g + 8 -- its quarter
 // of the head dim, one vector -- and V of four tokens -- its eighth -- so that
 // every load is one contiguous vector and a lane meets one or two block scales
 // a token.  V's codes of two tokens are interleaved as nibbles before they are
 // converted, which gives the f16 pairs along the tokens that the MMA wants.
 //
-// Work.  One list of 16-token units for all requests (kv.cuh), equal shares a
-// CTA, the units of an item dealt to the CTA's warps in turn; each warp feeds
-// itself through its own ring of cp.async copies, no barrier in the loop.
-// Warps join through shared memory at an item's end; items cut between CTAs
-// are joined by the last of them to arrive, in CTA order.
+// Work.  One list of 64-token groups for all requests (kv.cuh), equal shares a
+// CTA; the 32-token units of an item's groups are dealt to the CTA's seven
+// compute warps in turn.  An eighth warp runs ahead through the list, across
+// items: it looks up the pages and fills a ring of groups with bulk copies --
+// a page of up to 64 tokens holds all four pieces of a kv head in one run of
+// bytes, so a group is one to four copies.  Compute warps join through shared
+// memory at an item's end; items cut between CTAs are joined by the last of
+// them to arrive, in CTA order.  Each item counts kItemCost groups more than it
+// has: its start and join cost about that, so that shares of many short
+// requests take equal time.  Every wait has a clock budget: one that runs out
+// sets NVFP4_DEVICE_WAIT_TIMEOUT and all waits after it are passed over.
 //
 // Bound by the cache's bytes for one token a request.
 #include "../../include/nvfp4_kv.h"
@@ -40,33 +46,79 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kUnit = 16;       // tokens a unit
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;
+constexpr int kUnit = 32;       // tokens a unit
+constexpr int kGroup = 64;      // tokens a group
+constexpr int kSub = kGroup / kUnit;
+constexpr int kWarps = 7;       // compute warps: with the copying warp eight, two
+                                // for each of the SM's four register files
+constexpr int kCompute = 32 * kWarps;
+constexpr int kThreads = kCompute + 32;
+constexpr int kItemCost = 2;    // groups that an item's start and end cost
 constexpr int kMaxCtas = 512;   // workspace extent
 constexpr int kMaxRows = 32;
 constexpr float kRaise = 8.0f;  // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;   // p = 2^(s - m + kLift)
+constexpr long long kWaitBudget = 2000000000LL;  // clock cycles a wait may take
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p)
 {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes)
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void cp_commit()
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 {
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
 }
-template <int N>
-__device__ __forceinline__ void cp_wait()
+// Wait for phase `parity`; false when the budget (or another wait's) ran out.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            unsigned* status)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    const long long t0 = clock64();
+    while (!mbar_test(bar, parity)) {
+        if (*abort_flag)
+            return false;
+        if (clock64() - t0 > kWaitBudget) {
+            *abort_flag = 1;
+            atomicOr(status, (unsigned)NVFP4_DEVICE_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned* status)
+{
+    return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// Barrier of the compute warps.
+__device__ __forceinline__ void compute_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -97,7 +149,7 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t h)
     return pack_f16(lo - f.x, hi - f.y);
 }
 
-// MMA row k of a unit holds this token: rows 2j are tokens 0..3, rows 2j + 1
+// MMA row k of 16 tokens holds this token: rows 2j are tokens 0..3, rows 2j + 1
 // tokens 4..7 (paired j with j ^ 1), and the same eight further on; so the
 // four lanes of a V load and the two rows of a K load phase fall on different
 // banks as far as 64-byte rows allow.
@@ -113,21 +165,28 @@ struct Item {
     KvReq q;
     int rows;       // query rows of the request (tokens * group)
     int row0, row1;
-    int64_t begin;  // first unit in the list
+    int64_t begin;  // its place in the list: kItemCost, then its groups
     int32_t first, n;
+    int32_t u0, u1;  // the groups of this CTA's share
+};
+
+// A CTA's share of the list, and whether items may be cut between shares.
+struct Share {
+    int64_t lo, hi;
+    bool cut;
 };
 
 template <int R>
-__device__ __forceinline__ void item_units(const KvAttnArgs& a, Item& it)
+__device__ __forceinline__ void item_units(const KvAttnArgs& a, const Share& s, Item& it)
 {
     it.row0 = it.tile * R;
     it.row1 = min(it.row0 + R, it.rows);
-    kv_tile_units<kUnit>(a, it.q, it.row0, it.row1, it.first, it.n);
+    kv_tile_units<kGroup>(a, it.q, it.row0, it.row1, it.first, it.n);
 }
 
 // The first item of the first request at or after r that has rows.
 template <int R>
-__device__ __forceinline__ bool item_request(const KvAttnArgs& a, Item& it, int r)
+__device__ __forceinline__ bool item_request(const KvAttnArgs& a, const Share& s, Item& it, int r)
 {
     for (; r < a.reqs; ++r) {
         it.q = kv_req(a, r);
@@ -139,37 +198,68 @@ __device__ __forceinline__ bool item_request(const KvAttnArgs& a, Item& it, int 
     if (r >= a.reqs)
         return false;
     it.rows = it.q.nq * a.group;
-    item_units<R>(a, it);
+    item_units<R>(a, s, it);
     return true;
 }
 
 template <int R>
-__device__ __forceinline__ bool item_next(const KvAttnArgs& a, Item& it)
+__device__ __forceinline__ bool item_after(const KvAttnArgs& a, const Share& s, Item& it)
 {
-    it.begin += it.n;
+    it.begin += kItemCost + it.n;
     if ((it.tile + 1) * R < it.rows) {
         ++it.tile;
-        item_units<R>(a, it);
+        item_units<R>(a, s, it);
         return true;
     }
     it.tile = 0;
     if (++it.h < a.c.heads) {
-        item_units<R>(a, it);
+        item_units<R>(a, s, it);
         return true;
     }
-    return item_request<R>(a, it, it.r + 1);
+    return item_request<R>(a, s, it, it.r + 1);
 }
 
-// Units of one kv head of a request.
+// Steps on, from an item that may have no group in the share, to one that has.
 template <int R>
-__device__ __forceinline__ int64_t head_units(const KvAttnArgs& a, const KvReq& q)
+__device__ __forceinline__ bool item_settle(const KvAttnArgs& a, const Share& s, Item& it, bool more)
+{
+    for (; more; more = item_after<R>(a, s, it)) {
+        const int64_t at = it.begin + kItemCost;  // place of group 0
+        if (s.cut) {
+            if (at >= s.hi)
+                return false;
+            it.u0 = (int32_t)max((int64_t)0, s.lo - at);
+            it.u1 = (int32_t)min((int64_t)it.n, s.hi - at);
+            if (it.u0 < it.u1)
+                return true;
+        } else {  // an uncut item belongs to the share that holds its group 0
+            if (at >= s.hi)
+                return false;
+            it.u0 = 0;
+            it.u1 = it.n;
+            if (at >= s.lo)
+                return true;
+        }
+    }
+    return false;
+}
+
+template <int R>
+__device__ __forceinline__ bool item_next(const KvAttnArgs& a, const Share& s, Item& it)
+{
+    return item_settle<R>(a, s, it, item_after<R>(a, s, it));
+}
+
+// Places of one kv head of a request.
+template <int R>
+__device__ __forceinline__ int64_t head_places(const KvAttnArgs& a, const KvReq& q)
 {
     int64_t s = 0;
     const int rows = q.nq * a.group;
     for (int row0 = 0; row0 < rows; row0 += R) {
         int32_t first, n;
-        kv_tile_units<kUnit>(a, q, row0, min(row0 + R, rows), first, n);
-        s += n;
+        kv_tile_units<kGroup>(a, q, row0, min(row0 + R, rows), first, n);
+        s += kItemCost + n;
     }
     return s;
 }
@@ -178,43 +268,55 @@ template <int D, int NT, bool SPLIT>
 struct Cfg {
     static constexpr int R = 8 * NT;             // query rows a tile
     static constexpr int KS = D / 16;            // k16 steps of Q K, m16 tiles of V
-    static constexpr int kCode = kUnit * D / 2;  // bytes of a unit's K (or V) codes
-    static constexpr int kScale = kUnit * D / 16;
-    static constexpr int kStageBytes = 2 * kCode + 2 * kScale;
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStageBytes = kGroup * D * 9 / 8;
+    // two CTAs an SM where the registers allow it: the joins and starts of one
+    // overlap the other's stream
+    static constexpr int kCtas = NT == 1 && !SPLIT ? 2 : 1;
+    static constexpr int kStages = 8;
     static constexpr int kQTerms = SPLIT ? 2 : 1;
     static constexpr int kQBytes = kQTerms * NT * KS * 32 * 8;
-    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kRedBytes = kWarps * KS * 32 * 16;
-    static constexpr int kMain = kRingBytes > kRedBytes ? kRingBytes : kRedBytes;
-    static constexpr int kSmem = kMain + kQBytes;
+    static constexpr int kSmem = kRingBytes + kRedBytes + kQBytes;
     static constexpr bool kQRegs = NT * kQTerms <= 2;  // queries held in registers
+    static_assert((kStages & (kStages - 1)) == 0, "the ring's parity");
 };
 
 template <int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     kv_rows_kernel(const KvAttnArgs a)
 {
     using C = Cfg<D, NT, SPLIT>;
-    constexpr int R = C::R, KS = C::KS;
+    constexpr int R = C::R, KS = C::KS, ST = C::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t warp_sum[kWarps];
+    __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
+    __shared__ int64_t warp_sum[kThreads / 32];
     __shared__ int64_t found_rem;
     __shared__ int found_r;
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_f[R];
     __shared__ int32_t sm_pos[R];
-    __shared__ int last_s;
-    uint2* sq = reinterpret_cast<uint2*>(smem + C::kMain);
+    __shared__ int last_s, abort_s;
+    float4* red = reinterpret_cast<float4*>(smem + C::kRingBytes);
+    uint2* sq = reinterpret_cast<uint2*>(smem + C::kRingBytes + C::kRedBytes);
+    volatile int* abort_flag = &abort_s;
 
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(smem_u32(&full_bar[i]), 1);
+            mbar_init(smem_u32(&empty_bar[i]), kSub);
+        }
+        abort_s = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     kv_pdl_begin();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
     // ---- this CTA's share of the list ------------------------------------------------
     const int per = (a.reqs + kThreads - 1) / kThreads;
     const int ra = min(tid * per, a.reqs), rb = min(ra + per, a.reqs);
     int64_t mine = 0;
     for (int r = ra; r < rb; ++r) {
-        mine += a.c.heads * head_units<R>(a, kv_req(a, r));
+        mine += a.c.heads * head_places<R>(a, kv_req(a, r));
         if (blockIdx.x == 0 && kv_too_long(a, r))
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
     }
@@ -230,24 +332,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
     __syncthreads();
     int64_t before = inc - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp)
             before += warp_sum[w];
         total += warp_sum[w];
     }
-    // at least a unit a warp
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < kWarps ? kWarps : share;
-    const int64_t lo = share * blockIdx.x, hi = min(lo + share, total);
-    if (lo >= total)
+    // at least an item's cost and a unit a warp
+    const int64_t share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kItemCost + 2));
+    Share sh;
+    sh.lo = share * blockIdx.x;
+    sh.hi = min(sh.lo + share, total);
+    sh.cut = a.part != nullptr;
+    if (sh.lo >= total)
         return;
-    if (lo >= before && lo < before + mine) {
+    if (sh.lo >= before && sh.lo < before + mine) {
         int64_t at = before;
         for (int r = ra; r < rb; ++r) {
-            const int64_t n = a.c.heads * head_units<R>(a, kv_req(a, r));
-            if (lo < at + n) {
+            const int64_t n = a.c.heads * head_places<R>(a, kv_req(a, r));
+            if (sh.lo < at + n) {
                 found_r = r;
-                found_rem = lo - at;
+                found_rem = sh.lo - at;
                 break;
             }
             at += n;
@@ -255,98 +359,178 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
     }
     __syncthreads();
     Item it;
-    it.begin = lo - found_rem;
-    bool more = item_request<R>(a, it, found_r);
+    it.begin = sh.lo - found_rem;
+    bool more = item_request<R>(a, sh, it, found_r);
     if (more) {
-        const int64_t hu = head_units<R>(a, it.q);
+        const int64_t hu = head_places<R>(a, it.q);
         it.h = (int)(found_rem / hu);
         it.begin += it.h * hu;
-        while (it.begin + it.n <= lo) {
-            it.begin += it.n;
+        while (it.begin + kItemCost + it.n <= sh.lo) {
+            it.begin += kItemCost + it.n;
             ++it.tile;
-            item_units<R>(a, it);
+            item_units<R>(a, sh, it);
         }
     }
-    // without a workspace an item belongs to the CTA whose share it begins in
-    const bool cut = a.part != nullptr;
-    if (!cut && it.begin < lo)
-        more = item_next<R>(a, it);
+    more = item_settle<R>(a, sh, it, more);
 
     const int64_t head_bytes = kv_head_bytes(a.c.page_shift, D);
-    const float vg = a.c.v_g[0], qk = a.scale_log2 * a.c.k_g[0];
-    const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
-    const uint8_t* ring_gen = smem + warp * C::kStages * C::kStageBytes;
-    const int code_part = (D / 2) << a.c.page_shift, scale_part = (D / 16) << a.c.page_shift;
-    bool bad = false;
+    const uint32_t ring = smem_u32(smem);
 
-    while (more && it.begin < hi) {
-        const int32_t u0 = cut ? (int32_t)max((int64_t)0, lo - it.begin) : 0;
-        const int32_t u1 = cut ? (int32_t)min((int64_t)it.n, hi - it.begin) : it.n;
-        const int32_t* row_table = a.table + it.r * a.table_stride;
-        const int my_n = u1 - u0 > warp ? (u1 - u0 - warp + kWarps - 1) / kWarps : 0;
-        const int32_t c0 = it.first + u0 + warp;  // this warp's units: c0, c0 + kWarps ..
-
-        // copies of one unit into a ring slot; the page id was looked up one unit before
-        auto page_of = [&](int i) {
-            const int32_t b = ((c0 + i * kWarps) * kUnit) >> a.c.page_shift;
-            return i < my_n && b < a.max_blocks ? row_table[b] : -1;
+    if (warp == kWarps) {
+        // ---- the copying warp: a lane a piece of a group ------------------------------------
+        // pages of up to 64 tokens: a piece is a page; longer ones: K codes, V
+        // codes, K scales, V scales of the group's part of the page
+        const bool by_page = a.c.page_shift <= 6;
+        const int pieces = by_page ? kGroup >> a.c.page_shift : 4;
+        const int row_bytes = by_page ? D * 9 / 8 : lane < 2 ? D / 2 : D / 16;
+        const uint32_t bytes = by_page ? (uint32_t)row_bytes << a.c.page_shift
+                                       : (uint32_t)row_bytes * kGroup;
+        const int before_me = lane < 2 ? lane * (D / 2) : D + (lane - 2) * (D / 16);
+        const uint32_t dst0 = ring + (by_page ? lane * bytes : before_me * kGroup);
+        const int64_t piece_at = by_page ? 0 : (int64_t)before_me << a.c.page_shift;
+        bool bad = false;
+        uint32_t sent = 0;  // groups so far
+        // a lane holds one of 32 entries of the block table, the next 32 (of this
+        // item, or the first of the next) are on their way
+        const int P = a.c.page_shift;
+        auto entries = [&](const Item& x, int32_t base) {
+            const int32_t b = base + lane;
+            return b < a.max_blocks && (int64_t)b << P < x.q.seq
+                       ? a.table[x.r * a.table_stride + b]
+                       : -2;  // nothing of the request there
         };
-        int32_t next_page = page_of(0);
-        auto issue = [&](int i) {
-            if (i < my_n) {
-                const int32_t tok = (c0 + i * kWarps) * kUnit;
-                bool ok = next_page >= 0 && next_page < a.c.num_pages;
-                if (!ok && tok < it.q.seq)
-                    bad = true;
-                const int32_t off = tok & ((1 << a.c.page_shift) - 1);
-                const uint8_t* src = a.c.pool + (ok ? next_page : 0) * a.c.page_stride +
-                                     it.h * head_bytes;
-                const uint32_t bytes = ok ? 16u : 0u;
-                const uint32_t dst = ring + (i % C::kStages) * C::kStageBytes;
-#pragma unroll
-                for (int j = lane; j < C::kCode / 16; j += 32) {
-                    cp16(dst + 16 * j, src + off * (D / 2) + 16 * j, bytes);
-                    cp16(dst + C::kCode + 16 * j, src + code_part + off * (D / 2) + 16 * j, bytes);
+        auto first_entry = [&](const Item& x) { return ((x.first + x.u0) * kGroup) >> P; };
+        int32_t base = 0, ids = -2;
+        if (more) {
+            base = first_entry(it);
+            ids = entries(it, base);
+        }
+        bool go = true;
+        while (more && go) {
+            Item nx = it;
+            const bool nmore = item_next<R>(a, sh, nx);
+            const int32_t end = ((it.first + it.u1) * kGroup + (1 << P) - 1) >> P;
+            auto following = [&]() {
+                return base + 32 < end ? entries(it, base + 32)
+                                       : nmore ? entries(nx, first_entry(nx)) : -2;
+            };
+            int32_t nids = following();
+            for (int32_t u = it.u0; u < it.u1; ++u) {
+                const int32_t entry = ((it.first + u) * kGroup) >> P;
+                if (entry >= base + 32) {
+                    base += 32;
+                    ids = nids;
+                    nids = following();
                 }
-                if (lane < 2 * C::kScale / 16) {
-                    const int v = lane >= C::kScale / 16, j = lane - v * (C::kScale / 16);
-                    cp16(dst + 2 * C::kCode + 16 * lane,
-                         src + 2 * code_part + v * scale_part + off * (D / 16) + 16 * j, bytes);
+                int32_t page = __shfl_sync(0xFFFFFFFFu, ids, entry - base + (by_page ? lane : 0));
+                page = lane < pieces ? page : -2;
+                const uint32_t slot = sent % ST;
+                const uint32_t fb = smem_u32(&full_bar[slot]);
+                go = __all_sync(0xFFFFFFFFu,
+                                sent < ST || mbar_wait(smem_u32(&empty_bar[slot]),
+                                                       (sent / ST - 1) & 1, abort_flag, a.status));
+                if (!go)
+                    break;
+                const bool ok = page >= 0 && page < a.c.num_pages;
+                bad |= !ok && page != -2;
+                // a piece without a page is left out: its place holds old bytes
+                const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
+                if (lane == 0) {
+                    const uint32_t all =
+                        by_page ? __popc(there) * bytes : there ? C::kStageBytes : 0;
+                    if (all)
+                        mbar_expect_tx(fb, all);
+                    else
+                        mbar_arrive(fb);
                 }
-                next_page = page_of(i + 1);
+                __syncwarp();
+                if (ok) {
+                    const int32_t off = by_page ? 0 : ((it.first + u) * kGroup) & ((1 << P) - 1);
+                    bulk_copy(dst0 + slot * C::kStageBytes,
+                              a.c.pool + page * a.c.page_stride + it.h * head_bytes + piece_at +
+                                  off * row_bytes,
+                              bytes, fb);
+                }
+                ++sent;
             }
-            cp_commit();
-        };
+            it = nx;
+            base = nmore ? first_entry(nx) : 0;
+            ids = nids;
+            more = nmore;
+        }
+        if (*abort_flag)  // copies still in flight must land before the CTA ends
+            for (uint32_t k = sent > ST ? sent - ST : 0; k < sent; ++k) {
+                const long long t0 = clock64();
+                while (!mbar_test(smem_u32(&full_bar[k % ST]), (k / ST) & 1) &&
+                       clock64() - t0 < kWaitBudget) {
+                }
+            }
+        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
+            atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
+        return;
+    }
+
+    const int g = lane >> 2, t = lane & 3;
+    const float vg = a.c.v_g[0], qk = a.scale_log2 * a.c.k_g[0];
+    const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
+    uint32_t taken = 0;  // groups of the items before
+    // a group is blocks of 2^bs tokens: K codes, V codes, K scales, V scales each
+    const int bs = min(a.c.page_shift, 6);
+    const int v_part = (D / 2) << bs, s_part = (D / 16) << bs, whole_block = (D * 9 / 8) << bs;
+    // from 16 tokens to the next 16, and from unit to unit, of codes and of scales
+    const int code_half = bs == 4 ? whole_block : 16 * (D / 2);
+    const int scale_half = bs == 4 ? whole_block : 16 * (D / 16);
+    const int code_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 2);
+    const int scale_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 16);
+    const int ka = token_of_row(g), v_tok = token_of_row(2 * t), v_odd = token_of_row(2 * t + 1) - v_tok;
+    constexpr int HB = NT == 1 ? kUnit / 16 : 1;  // 16-token halves in flight at once
+
+    // four consecutive elements of row c of an item's query tile
+    auto query = [&](const Item& x, int c) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int row = x.row0 + c;
+        if (c < R && row < x.row1 && 4 * lane < D) {
+            const int tok = row / a.group;
+            const int64_t at = (x.q.base + tok) * a.q_stride +
+                               (int64_t)(x.h * a.group + row - tok * a.group) * D + 4 * lane;
+            if (a.q_bf16) {
+                const uint2 w =
+                    *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at);
+                v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+            } else {
+                v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+            }
+        }
+        return v;
+    };
+    constexpr int QR = (R + kWarps - 1) / kWarps;
+    float4 qv[QR];  // the next item's rows warp, warp + kWarps ..
+    if (more) {
 #pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i)
-            issue(i);
+        for (int j = 0; j < QR; ++j)
+            qv[j] = query(it, warp + j * kWarps);
+    }
+
+    while (more) {
+        const int32_t u0 = it.u0, u1 = it.u1;
+        const int units = (u1 - u0) * kSub;
+        const int32_t first_tok = (it.first + u0) * kGroup;
 
         // queries of this item as B fragments, in f16 terms, rows scaled by powers of two
-        for (int c = warp; c < R; c += kWarps) {
-            const int row = it.row0 + c;
-            const bool live = row < it.row1;
-            const int tok = live ? row / a.group : 0;
-            const int head = it.h * a.group + (live ? row - tok * a.group : 0);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            const bool has = 4 * lane < D;
-            if (live && has) {
-                const int64_t at = (it.q.base + tok) * a.q_stride + (int64_t)head * D + 4 * lane;
-                if (a.q_bf16) {
-                    const uint2 w =
-                        *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at);
-                    v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-                } else {
-                    v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-                }
-            }
+#pragma unroll
+        for (int j = 0; j < QR; ++j) {
+            const int c = warp + j * kWarps;
+            if (c >= R)
+                break;
+            float4 v = qv[j];
             const float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
             const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
             // 2^(14 - exponent of the largest), kept a normal number
             const int e = min(max(14 - ((int)(bits >> 23) - 127), -100), 100);
             const float up = bits ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
             const float down = bits ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
-            if (has) {
+            if (4 * lane < D) {
                 v.x *= up, v.y *= up, v.z *= up, v.w *= up;
                 const int at = ((c >> 3) * KS + lane % KS) * 32 + (c & 7) * 4 + lane / KS;
                 const uint2 h = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
@@ -356,11 +540,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
                         make_uint2(pack_rest(v.x, v.y, h.x), pack_rest(v.z, v.w, h.y));
             }
             if (lane == 0) {
+                const int row = it.row0 + c;
                 sm_f[c] = qk * down;
-                sm_pos[c] = live ? it.q.seq - it.q.nq + tok : -1;
+                sm_pos[c] = row < it.row1 ? it.q.seq - it.q.nq + row / a.group : -1;
             }
         }
-        __syncthreads();
+        compute_sync();
 
         uint2 qf[C::kQRegs ? C::kQTerms * NT * KS : 1];
         if constexpr (C::kQRegs) {
@@ -388,194 +573,221 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
         const int32_t p1 = it.q.seq - it.q.nq + (it.row1 - 1) / a.group;
         const int32_t all_hi = p0, all_lo = a.window > 0 ? p1 - a.window + 1 : 0;
 
-        for (int i = 0; i < my_n; ++i) {
-            cp_wait<C::kStages - 2>();
-            __syncwarp();
-            const uint8_t* st = ring_gen + (i % C::kStages) * C::kStageBytes;
-            const int32_t tok0 = (c0 + i * kWarps) * kUnit;
+        for (int i = warp; i < units; i += kWarps) {
+            const uint32_t group = taken + i / kSub, slot = group % ST;
+            const int32_t unit0 = first_tok + i * kUnit;
+            mbar_wait(full0 + 8 * slot, (group / ST) & 1, abort_flag, a.status);
+            if (unit0 < it.q.seq) {  // else past the end: nothing to do in this unit
+                const uint8_t* st = smem + slot * C::kStageBytes + (i % kSub) * code_step;
+                const uint8_t* sk = smem + slot * C::kStageBytes + 2 * v_part + (i % kSub) * scale_step;
+#pragma unroll HB
+                for (int h0 = 0; h0 < kUnit / 16; h0 += HB) {
+                    const int32_t tok0 = unit0 + 16 * h0;
 
-            // ---- S^T = K Q^T: 16 tokens x 8 NT rows ----------------------------------------
-            float s[NT][4];
+                    // ---- S^T = K Q^T: HB times 16 tokens x 8 NT rows ---------------------------
+                    float s[HB][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                    for (int h = 0; h < HB; ++h) {
+                        const uint8_t* kc = st + (h0 + h) * code_half;
+                        const uint8_t* ks = sk + (h0 + h) * scale_half;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[nt][e] = 0.f;
-            const int ka = token_of_row(g), kb = ka + 8;
-            uint32_t wa[D / 32], wb[D / 32];
-            if constexpr (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4*>(st + ka * 64 + 16 * t);
-                const uint4 y = *reinterpret_cast<const uint4*>(st + kb * 64 + 16 * t);
-                wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
-                wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(st + ka * 32 + 8 * t);
-                const uint2 y = *reinterpret_cast<const uint2*>(st + kb * 32 + 8 * t);
-                wa[0] = x.x, wa[1] = x.y;
-                wb[0] = y.x, wb[1] = y.y;
-            }
-            const uint8_t* sk = st + 2 * C::kCode;
-            uint32_t sa[D / 64], sb[D / 64];  // this lane's block scales of the two rows, doubled
-            if constexpr (D == 128) {
-                const uint32_t x = e4m3x2_to_f16x2_bits(
-                    *reinterpret_cast<const uint16_t*>(sk + ka * 8 + 2 * t));
-                const uint32_t y = e4m3x2_to_f16x2_bits(
-                    *reinterpret_cast<const uint16_t*>(sk + kb * 8 + 2 * t));
-                sa[0] = f16x2_dup_lo(x), sa[1] = f16x2_dup_hi(x);
-                sb[0] = f16x2_dup_lo(y), sb[1] = f16x2_dup_hi(y);
-            } else {
-                const uint32_t two = e4m3x2_to_f16x2_bits(sk[ka * 4 + t] | (sk[kb * 4 + t] << 8));
-                sa[0] = f16x2_dup_lo(two);
-                sb[0] = f16x2_dup_hi(two);
-            }
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t ha[4], hb[4];
-                e2m1x8_to_f16(wa[w], ha);
-                e2m1x8_to_f16(wb[w], hb);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    ha[e] = f16x2_mul(ha[e], sa[w / 2]);
-                    hb[e] = f16x2_mul(hb[e], sb[w / 2]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < C::kQTerms; ++x)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = (x * NT + nt) * KS + 2 * w + e;
-                            const uint2 b = C::kQRegs ? qf[C::kQRegs ? j : 0] : sq[j * 32 + lane];
-                            mma_m16n8k16(s[nt], ha[2 * e], hb[2 * e], ha[2 * e + 1], hb[2 * e + 1],
-                                         b.x, b.y);
+                            for (int e = 0; e < 4; ++e)
+                                s[h][nt][e] = 0.f;
+                        uint32_t wa[D / 32], wb[D / 32];
+                        uint32_t sa[D / 64], sb[D / 64];  // block scales of the two rows, doubled
+                        if constexpr (D == 128) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(kc + ka * 64 + 16 * t);
+                            const uint4 y =
+                                *reinterpret_cast<const uint4*>(kc + (ka + 8) * 64 + 16 * t);
+                            wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
+                            wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
+                            const uint32_t u = e4m3x2_to_f16x2_bits(
+                                *reinterpret_cast<const uint16_t*>(ks + ka * 8 + 2 * t));
+                            const uint32_t v = e4m3x2_to_f16x2_bits(
+                                *reinterpret_cast<const uint16_t*>(ks + (ka + 8) * 8 + 2 * t));
+                            sa[0] = f16x2_dup_lo(u), sa[1] = f16x2_dup_hi(u);
+                            sb[0] = f16x2_dup_lo(v), sb[1] = f16x2_dup_hi(v);
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(kc + ka * 32 + 8 * t);
+                            const uint2 y =
+                                *reinterpret_cast<const uint2*>(kc + (ka + 8) * 32 + 8 * t);
+                            wa[0] = x.x, wa[1] = x.y;
+                            wb[0] = y.x, wb[1] = y.y;
+                            const uint32_t two = e4m3x2_to_f16x2_bits(
+                                ks[ka * 4 + t] | (ks[(ka + 8) * 4 + t] << 8));
+                            sa[0] = f16x2_dup_lo(two);
+                            sb[0] = f16x2_dup_hi(two);
                         }
-            }
-
-            // ---- softmax: rows of S^T are tokens ka, kb; columns 2t, 2t + 1 -----------------
-            const bool edge = tok0 < all_lo || tok0 + kUnit - 1 > all_hi;
-            bool raise = false;
-            float x[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                        for (int w = 0; w < D / 32; ++w) {
+                            uint32_t ha[4], hb[4];
+                            e2m1x8_to_f16(wa[w], ha);
+                            e2m1x8_to_f16(wb[w], hb);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[nt][e] = fmaf(s[nt][e], f[nt][e & 1], -m[nt][e & 1]);
-            if (edge) {
+                            for (int e = 0; e < 4; ++e) {
+                                ha[e] = f16x2_mul(ha[e], sa[w / 2]);
+                                hb[e] = f16x2_mul(hb[e], sb[w / 2]);
+                            }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int32_t pos = sm_pos[nt * 8 + 2 * t + (e & 1)];
-                        const int32_t tok = tok0 + (e < 2 ? ka : kb);
-                        if (tok > pos || (a.window > 0 && tok <= pos - a.window)) {
-                            x[nt][e] = -INFINITY;
-                            s[nt][e] = -INFINITY;
+                                for (int x = 0; x < C::kQTerms; ++x)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int j = (x * NT + nt) * KS + 2 * w + e;
+                                        const uint2 b =
+                                            C::kQRegs ? qf[C::kQRegs ? j : 0] : sq[j * 32 + lane];
+                                        mma_m16n8k16(s[h][nt], ha[2 * e], hb[2 * e], ha[2 * e + 1],
+                                                     hb[2 * e + 1], b.x, b.y);
+                                    }
                         }
                     }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    raise |= x[nt][e] > kLift + kRaise;
-            if (__any_sync(0xFFFFFFFFu, raise)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // a masked score stays at -inf whatever the factor
-                        const float s0 = s[nt][e] == -INFINITY ? -INFINITY : s[nt][e] * f[nt][e];
-                        const float s1 =
-                            s[nt][e + 2] == -INFINITY ? -INFINITY : s[nt][e + 2] * f[nt][e];
-                        float top = fmaxf(s0, s1);
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-                        const float now = fmaxf(m[nt][e], top - kLift);
-                        const float by = m[nt][e] == now ? 1.f : ex2(m[nt][e] - now);
-                        m[nt][e] = now;
-                        l[nt][e] *= by;
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            acc[nt][k][e] *= by;
-                            acc[nt][k][e + 2] *= by;
-                        }
-                        x[nt][e] = s0 == -INFINITY ? -INFINITY : fmaf(s[nt][e], f[nt][e], -now);
-                        x[nt][e + 2] =
-                            s1 == -INFINITY ? -INFINITY : fmaf(s[nt][e + 2], f[nt][e], -now);
-                    }
-            }
-            uint32_t pb[C::kQTerms][NT][2];  // P^T as B fragments
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    p[e] = ex2(x[nt][e]);
-                l[nt][0] += p[0] + p[2];
-                l[nt][1] += p[1] + p[3];
-                const uint32_t h0 = pack_f16(p[0], p[1]), h1 = pack_f16(p[2], p[3]);
-                pb[0][nt][0] = movm_trans(h0);
-                pb[0][nt][1] = movm_trans(h1);
-                if constexpr (SPLIT) {
-                    pb[1][nt][0] = movm_trans(pack_rest(p[0], p[1], h0));
-                    pb[1][nt][1] = movm_trans(pack_rest(p[2], p[3], h1));
-                }
-            }
 
-            // ---- O^T += V^T P^T: this lane's eighth of the head dim, tokens of rows 2t ..----
-            const uint8_t* sv = st + C::kCode;
-            const uint8_t* ss = sk + C::kScale;
-            int vt[4];
-            uint32_t vw[4][D / 64], vs[4];
+                    // ---- softmax: rows of S^T are tokens ka, ka + 8; columns 2t, 2t + 1 ----------
+                    float x[HB][NT][4];
+                    float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                vt[k] = token_of_row((k >> 1) * 8 + 2 * t + (k & 1));
-                if constexpr (D == 128) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(sv + vt[k] * 64 + 8 * g);
-                    vw[k][0] = v.x, vw[k][1] = v.y;
-                    vs[k] = ss[vt[k] * 8 + g];
-                } else {
-                    vw[k][0] = *reinterpret_cast<const uint32_t*>(sv + vt[k] * 32 + 4 * g);
-                    vs[k] = ss[vt[k] * 4 + (g >> 1)];
-                }
-            }
-            if (tok0 + kUnit > it.q.seq) {  // what lies past the end may be anything
+                    for (int h = 0; h < HB; ++h)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (tok0 + vt[k] >= it.q.seq) {
-                        vs[k] = 0;
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int w = 0; w < D / 64; ++w)
-                            vw[k][w] = 0;
+                            for (int e = 0; e < 4; ++e)
+                                x[h][nt][e] = fmaf(s[h][nt][e], f[nt][e & 1], -m[nt][e & 1]);
+                    if (tok0 < all_lo || tok0 + 16 * HB - 1 > all_hi) {
+#pragma unroll
+                        for (int h = 0; h < HB; ++h)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int32_t pos = sm_pos[nt * 8 + 2 * t + (e & 1)];
+                                    const int32_t tok = tok0 + 16 * h + ka + (e < 2 ? 0 : 8);
+                                    if (tok > pos || (a.window > 0 && tok <= pos - a.window)) {
+                                        x[h][nt][e] = -INFINITY;
+                                        s[h][nt][e] = -INFINITY;
+                                    }
+                                }
                     }
-            }
-            const uint32_t s01 = e4m3x2_to_f16x2_bits(vs[0] | (vs[1] << 8));
-            const uint32_t s23 = e4m3x2_to_f16x2_bits(vs[2] | (vs[3] << 8));
 #pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-                constexpr uint32_t kLow = 0x0F0F0F0Fu;
-                uint32_t e0[4], e1[4], o0[4], o1[4];  // even / odd elements of both token pairs
-                e2m1x8_to_f16((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), e0);
-                e2m1x8_to_f16(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), o0);
-                e2m1x8_to_f16((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), e1);
-                e2m1x8_to_f16(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), o1);
+                    for (int h = 0; h < HB; ++h)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t a0 = f16x2_mul(e0[k], s01), a1 = f16x2_mul(o0[k], s01);
-                    const uint32_t a2 = f16x2_mul(e1[k], s23), a3 = f16x2_mul(o1[k], s23);
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                            for (int e = 0; e < 4; ++e)
+                                top = fmaxf(top, x[h][nt][e]);
+                    if (__any_sync(0xFFFFFFFFu, top > kLift + kRaise)) {
 #pragma unroll
-                        for (int y = 0; y < C::kQTerms; ++y)
-                            mma_m16n8k16(acc[nt][4 * w + k], a0, a1, a2, a3, pb[y][nt][0],
-                                         pb[y][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                // a masked score stays at -inf whatever the factor
+                                float most = -INFINITY;
+#pragma unroll
+                                for (int h = 0; h < HB; ++h)
+#pragma unroll
+                                    for (int y = e; y < 4; y += 2)
+                                        if (s[h][nt][y] != -INFINITY)
+                                            most = fmaxf(most, s[h][nt][y] * f[nt][e]);
+                                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 4));
+                                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
+                                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+                                const float now = fmaxf(m[nt][e], most - kLift);
+                                const float by = m[nt][e] == now ? 1.f : ex2(m[nt][e] - now);
+                                m[nt][e] = now;
+                                l[nt][e] *= by;
+#pragma unroll
+                                for (int k = 0; k < KS; ++k) {
+                                    acc[nt][k][e] *= by;
+                                    acc[nt][k][e + 2] *= by;
+                                }
+#pragma unroll
+                                for (int h = 0; h < HB; ++h)
+#pragma unroll
+                                    for (int y = e; y < 4; y += 2)
+                                        x[h][nt][y] = s[h][nt][y] == -INFINITY
+                                                          ? -INFINITY
+                                                          : fmaf(s[h][nt][y], f[nt][e], -now);
+                            }
+                    }
+                    uint32_t pb[HB][C::kQTerms][NT][2];  // P^T as B fragments
+#pragma unroll
+                    for (int h = 0; h < HB; ++h)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float p[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                p[e] = ex2(x[h][nt][e]);
+                            l[nt][0] += p[0] + p[2];
+                            l[nt][1] += p[1] + p[3];
+                            const uint32_t h0_ = pack_f16(p[0], p[1]), h1_ = pack_f16(p[2], p[3]);
+                            pb[h][0][nt][0] = movm_trans(h0_);
+                            pb[h][0][nt][1] = movm_trans(h1_);
+                            if constexpr (SPLIT) {
+                                pb[h][1][nt][0] = movm_trans(pack_rest(p[0], p[1], h0_));
+                                pb[h][1][nt][1] = movm_trans(pack_rest(p[2], p[3], h1_));
+                            }
+                        }
+
+                    // ---- O^T += V^T P^T: this lane's eighth of the head dim, tokens of rows 2t .. --
+#pragma unroll
+                    for (int h = 0; h < HB; ++h) {
+                        const uint8_t* sv = st + (h0 + h) * code_half + v_part;
+                        const uint8_t* ss = sk + (h0 + h) * scale_half + s_part;
+                        uint32_t vw[4][D / 64], vs[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int vt = v_tok + (k >> 1) * 8 + (k & 1) * v_odd;
+                            if constexpr (D == 128) {
+                                const uint2 v = *reinterpret_cast<const uint2*>(sv + vt * 64 + 8 * g);
+                                vw[k][0] = v.x, vw[k][1] = v.y;
+                                vs[k] = ss[vt * 8 + g];
+                            } else {
+                                vw[k][0] = *reinterpret_cast<const uint32_t*>(sv + vt * 32 + 4 * g);
+                                vs[k] = ss[vt * 4 + (g >> 1)];
+                            }
+                        }
+                        if (tok0 + 16 * h + 16 > it.q.seq) {  // past the end may be anything
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (tok0 + 16 * h + v_tok + (k >> 1) * 8 + (k & 1) * v_odd >= it.q.seq) {
+                                    vs[k] = 0;
+#pragma unroll
+                                    for (int w = 0; w < D / 64; ++w)
+                                        vw[k][w] = 0;
+                                }
+                        }
+                        const uint32_t s01 = e4m3x2_to_f16x2_bits(vs[0] | (vs[1] << 8));
+                        const uint32_t s23 = e4m3x2_to_f16x2_bits(vs[2] | (vs[3] << 8));
+#pragma unroll
+                        for (int w = 0; w < D / 64; ++w) {
+                            constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                            uint32_t e0[4], e1[4], o0[4], o1[4];  // even / odd elements, token pairs
+                            e2m1x8_to_f16((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), e0);
+                            e2m1x8_to_f16(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), o0);
+                            e2m1x8_to_f16((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), e1);
+                            e2m1x8_to_f16(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), o1);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t a0 = f16x2_mul(e0[k], s01), a1 = f16x2_mul(o0[k], s01);
+                                const uint32_t a2 = f16x2_mul(e1[k], s23), a3 = f16x2_mul(o1[k], s23);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int y = 0; y < C::kQTerms; ++y)
+                                        mma_m16n8k16(acc[nt][4 * w + k], a0, a1, a2, a3,
+                                                     pb[h][y][nt][0], pb[h][y][nt][1]);
+                            }
+                        }
+                    }
                 }
+                __syncwarp();  // every lane has read the slot
             }
-            __syncwarp();  // every lane has read the slot that the next copies overwrite
-            issue(i + C::kStages - 1);
+            if (lane == 0)
+                mbar_arrive(empty0 + 8 * slot);
         }
-        cp_wait<0>();
 
         // ---- join the warps ---------------------------------------------------------------
 #pragma unroll
@@ -591,13 +803,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
                     sm_l[warp][nt * 8 + 2 * t + e] = v;
                 }
             }
-        __syncthreads();
+        compute_sync();
+
+        taken += u1 - u0;
+        // the next item's queries are on their way during the join
+        Item nx = it;
+        more = item_next<R>(a, sh, nx);
+        if (more) {
+#pragma unroll
+            for (int j = 0; j < QR; ++j)
+                qv[j] = query(nx, warp + j * kWarps);
+        }
 
         const bool whole = u0 == 0 && u1 == it.n;
         const int32_t slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
         constexpr int kFrag = KS * 32;  // float4 fragments of 8 rows
         constexpr int64_t kPart = (int64_t)NT * kFrag * 4 + 2 * R;  // floats of a partial result
-        float4* red = reinterpret_cast<float4*>(smem);
 
         // (row, two elements) of a fragment entry to the output
         auto store2 = [&](int col, int fi, int fl, float v0, float v1, float ltot) {
@@ -651,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
                 red[(warp * KS + i) * 32 + lane] =
                     make_float4(acc[nt][i][0] * by[0], acc[nt][i][1] * by[1],
                                 acc[nt][i][2] * by[0], acc[nt][i][3] * by[1]);
-            __syncthreads();
-            for (int e = tid; e < kFrag; e += kThreads) {
+            compute_sync();
+            for (int e = tid; e < kFrag; e += kCompute) {
                 float4 v = red[e];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) {
@@ -666,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
                     reinterpret_cast<float4*>(a.part + slot * kPart)[nt * kFrag + e] = v;
                 }
             }
-            __syncthreads();
+            compute_sync();
         }
         if (tid < R) {
             float mt, lt;
@@ -681,9 +902,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
         }
         if (!whole) {
             // ---- join the CTAs: the last to arrive sums all parts in CTA order ----------------
-            const int ca = (int)(it.begin / share), cb = (int)((it.begin + it.n - 1) / share);
+            const int ca = (int)((it.begin + kItemCost) / share);
+            const int cb = (int)((it.begin + kItemCost + it.n - 1) / share);
             __threadfence();
-            __syncthreads();
+            compute_sync();
             if (tid == 0) {
                 const unsigned seen = atomicAdd(a.count + ca, 1u);
                 last_s = seen == (unsigned)(cb - ca);
@@ -691,10 +913,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
                     a.count[ca] = 0u;
                 __threadfence();
             }
-            __syncthreads();
+            compute_sync();
             if (last_s) {
                 for (int nt = 0; nt < NT; ++nt)
-                    for (int e = tid; e < kFrag; e += kThreads) {
+                    for (int e = tid; e < kFrag; e += kCompute) {
                         const int col = nt * 8 + 2 * (e & 3);
                         float mt[2] = {-INFINITY, -INFINITY}, lt[2] = {0.f, 0.f};
                         for (int c = ca; c <= cb; ++c) {
@@ -726,11 +948,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 1)
                     }
             }
         }
-        __syncthreads();  // shared memory is free for the next item
-        more = item_next<R>(a, it);
+        compute_sync();  // shared memory is free for the next item
+        it = nx;
     }
-    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
-        atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
 }
 
 template <int D, int NT, bool SPLIT>
@@ -742,7 +962,7 @@ cudaError_t launch(const KvAttnArgs& a, cudaStream_t stream, bool pdl)
     const cudaError_t e = ensure_smem_limit(kern, C::kSmem, dev);
     if (e != cudaSuccess)
         return e;
-    const int grid = device_sm_count(dev) * (NT == 1 ? kCtasPerSm : 1);
+    const int grid = device_sm_count(dev) * C::kCtas;
     return kv_launch(kern, grid > kMaxCtas ? kMaxCtas : grid, kThreads, C::kSmem, stream, pdl, a);
 }
 

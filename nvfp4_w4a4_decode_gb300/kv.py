@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes
+import struct
 from collections import namedtuple
 
 import torch
@@ -29,66 +30,57 @@ SIGNATURES = {
 }
 
 
-class _CacheDesc(ctypes.Structure):
-    """``nvfp4_kv_cache``."""
-    _fields_ = [("pool", _p), ("k_g", _p), ("v_g", _p), ("num_pages", _i64), ("page_stride", _i64),
-                ("page_size", _i32), ("num_kv_heads", _i32), ("head_dim", _i32)]
-
-
-class _AttentionArgs(ctypes.Structure):
-    """``nvfp4_kv_attention_args``."""
-    _fields_ = [("q", _p), ("q_stride", _i64), ("num_q_heads", _i64), ("block_table", _p),
-                ("table_stride", _i64), ("max_blocks", _i64), ("seq_len", _p), ("q_start", _p),
-                ("reqs", _i64), ("tokens", _i64), ("max_q", _i64), ("scale", ctypes.c_float),
-                ("window", _i64), ("out", _p), ("out_stride", _i64), ("lse", _p)]
+# nvfp4_kv_cache and nvfp4_kv_attention_args as native struct layouts
+_CACHE = struct.Struct("@PPPqqiii4x")
+_ATTENTION = struct.Struct("@PqqPqqPPqqqfqPqP")
 
 
 from . import (FLAG_PDL, FLAG_X_BF16, FLAG_Y_BF16, KERNEL_AUTO, Nvfp4Error,  # noqa: E402
                library)
 
 
-def _raise(name, status):
-    if status != 0:
-        raise Nvfp4Error(name, status)
+# The checks run before every call of a decode step, so they read each tensor's
+# properties once and in their cheapest form (get_device() is -1 on the host).
 
-
-def _on_device(t, dtype, name, device=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+def _vector(t, dtype, name, dev, n=-1):
+    """Checks a contiguous vector (of n elements) on CUDA device index dev; its address."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (device {dev})")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 1 or not t.is_contiguous() or (n >= 0 and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous vector" + (f" of {n}" if n >= 0 else ""))
+    return t.data_ptr()
 
 
-def _vector(t, dtype, name, device, n=None):
-    _on_device(t, dtype, name, device)
-    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous vector" + ("" if n is None else f" of {n}"))
-
-
-def _table(t, rows, device):
-    """(pointer, row stride, entries a row) of a block table whose rows are contiguous."""
-    _on_device(t, torch.int32, "block_table", device)
-    if t.dim() != 2 or t.shape[0] != rows or (t.shape[1] > 1 and t.stride(1) != 1) or \
-            (rows > 1 and t.stride(0) < t.shape[1]):
+def _table(t, rows, dev):
+    """(address, row stride, entries a row) of a block table whose rows are contiguous."""
+    if t.get_device() != dev or t.dtype is not torch.int32:
+        raise ValueError(f"block_table must be an int32 tensor on device {dev}")
+    if t.dim() != 2:
+        raise ValueError(f"block_table must be [{rows}, blocks]")
+    n, blocks = t.shape
+    step, one = t.stride()
+    if n != rows or (blocks > 1 and one != 1) or (rows > 1 and step < blocks):
         raise ValueError(f"block_table must be [{rows}, blocks] with contiguous rows")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else t.shape[1]), t.shape[1]
+    return t.data_ptr(), (step if rows > 1 else blocks), blocks
 
 
-def _heads(t, name, device, dim, dtype=None):
-    """Token stride of [tokens, heads, dim] whose token rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype not in ((torch.float32, torch.bfloat16) if dtype is None else (dtype,)):
-        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim:
+def _heads(t, name, dev, dim):
+    """(tokens, heads, token stride) of [tokens, heads, dim] with contiguous token rows."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (device {dev})")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, {dim}]")
-    tokens, heads, _ = t.shape
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != dim) or (tokens > 1 and s[0] < heads * dim):
+    tokens, heads, d = t.shape
+    step, head, one = t.stride()
+    if d != dim:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}]")
+    if one != 1 or (heads > 1 and head != dim) or (tokens > 1 and step < heads * dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if tokens > 1 else heads * dim
+    return tokens, heads, (step if tokens > 1 else heads * dim)
 
 
 def nvfp4_kv_page_bytes(page_size: int, num_kv_heads: int, head_dim: int) -> int:
@@ -120,11 +112,8 @@ class KVCache:
     at the first of them (one per stream)."""
 
     def __init__(self, pool, k_g, v_g, page_size: int, head_dim: int):
-        _on_device(pool, torch.uint8, "pool")
-        _vector(k_g, torch.float32, "k_g", pool.device, 1)
-        _vector(v_g, torch.float32, "v_g", pool.device, 1)
-        if pool.dim() != 3:
-            raise ValueError("pool must be [num_pages, num_kv_heads, bytes]")
+        if pool.get_device() < 0 or pool.dtype is not torch.uint8 or pool.dim() != 3:
+            raise ValueError("pool must be a uint8 CUDA tensor [num_pages, num_kv_heads, bytes]")
         pages, heads, size = pool.shape
         want = nvfp4_kv_page_bytes(page_size, heads, head_dim)
         if size * heads != want:
@@ -135,16 +124,19 @@ class KVCache:
         self.pool, self.k_g, self.v_g = pool, k_g, v_g
         self.num_pages, self.num_kv_heads = pages, heads
         self.page_size, self.head_dim = int(page_size), int(head_dim)
-        self.device = pool.device
-        self._desc = _CacheDesc(pool.data_ptr(), k_g.data_ptr(), v_g.data_ptr(), pages,
-                                pool.stride(0) if pages > 1 else want, page_size, heads, head_dim)
-        self._ref = ctypes.addressof(self._desc)
+        self.device, self._dev = pool.device, pool.get_device()
+        self._desc = _CACHE.pack(
+            pool.data_ptr(), _vector(k_g, torch.float32, "k_g", self._dev, 1),
+            _vector(v_g, torch.float32, "v_g", self._dev, 1), pages,
+            pool.stride(0) if pages > 1 else want, page_size, heads, head_dim)
         self._workspaces = {}
 
-    def _workspace(self, stream: int) -> torch.Tensor:
+    def _workspace(self, stream: int):
+        """(address, bytes) of this stream's workspace."""
         ws = self._workspaces.get(stream)
         if ws is None:
-            ws = kv_attention_workspace(self.head_dim, self.device)
+            t = kv_attention_workspace(self.head_dim, self.device)
+            ws = (t.data_ptr(), t.numel(), t)
             # one made while a graph is captured is zeroed by that graph only
             if not torch.cuda.is_current_stream_capturing():
                 self._workspaces[stream] = ws
@@ -160,8 +152,12 @@ def kv_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
                        device=device if device is not None else torch.cuda.current_device())
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same handle without building a Stream object, where torch offers it
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 KVTables = namedtuple("KVTables", "seq_len q_start slots positions free_head")
@@ -179,28 +175,33 @@ def nvfp4_kv_tables(kv_len, q_len, free_pages, free_head, block_table, page_size
     [reqs + 1], slots [tokens] int64, positions [tokens], free_head [1])``,
     the last being the free list's next head.  A free list or table that is
     too short sets DEVICE_KV_RANGE in ``device_status()``."""
-    dev = kv_len.device
-    _vector(kv_len, torch.int32, "kv_len", None)
-    reqs = kv_len.shape[0]
-    _vector(q_len, torch.int32, "q_len", dev, reqs)
-    _vector(free_pages, torch.int32, "free_pages", dev)
-    _vector(free_head, torch.int32, "free_head", dev, 1)
+    dev, reqs = kv_len.get_device(), kv_len.numel()
+    p_len = _vector(kv_len, torch.int32, "kv_len", dev)
+    p_new = _vector(q_len, torch.int32, "q_len", dev, reqs)
+    p_free = _vector(free_pages, torch.int32, "free_pages", dev)
+    p_head = _vector(free_head, torch.int32, "free_head", dev, 1)
     tp, ts, blocks = _table(block_table, reqs, dev)
     if out is None:
-        # one allocation: slots first (8 bytes each), then the int32 vectors
-        buf = torch.empty(3 * tokens + 2 * reqs + 2, dtype=torch.int32, device=dev)
-        slots, positions, seq, start, head = buf.split((2 * tokens, tokens, reqs, reqs + 1, 1))
-        out = KVTables(seq, start, slots.view(torch.int64), positions, head)
+        at = kv_len.device
+        seq = torch.empty(reqs, dtype=torch.int32, device=at)
+        start = torch.empty(reqs + 1, dtype=torch.int32, device=at)
+        slots = torch.empty(tokens, dtype=torch.int64, device=at)
+        positions = torch.empty(tokens, dtype=torch.int32, device=at)
+        head = torch.empty(1, dtype=torch.int32, device=at)
+        out = KVTables(seq, start, slots, positions, head)
+        outs = (seq.data_ptr(), start.data_ptr(), slots.data_ptr(), positions.data_ptr(), tokens,
+                head.data_ptr())
     else:
-        for t, name, n in ((out.seq_len, "seq_len", reqs), (out.q_start, "q_start", reqs + 1),
-                           (out.positions, "positions", tokens), (out.free_head, "free_head", 1)):
-            _vector(t, torch.int32, name, dev, n)
-        _vector(out.slots, torch.int64, "slots", dev, tokens)
-    _raise("nvfp4_kv_tables", library().nvfp4_kv_tables(
-        kv_len.data_ptr(), q_len.data_ptr(), reqs, page_size, free_pages.data_ptr(),
-        free_pages.shape[0], free_head.data_ptr(), tp, ts, blocks, out.seq_len.data_ptr(),
-        out.q_start.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(), tokens,
-        out.free_head.data_ptr(), FLAG_PDL if pdl else 0, _stream(dev)))
+        outs = (_vector(out.seq_len, torch.int32, "seq_len", dev, reqs),
+                _vector(out.q_start, torch.int32, "q_start", dev, reqs + 1),
+                _vector(out.slots, torch.int64, "slots", dev, tokens),
+                _vector(out.positions, torch.int32, "positions", dev, tokens), tokens,
+                _vector(out.free_head, torch.int32, "free_head", dev, 1))
+    status = library().nvfp4_kv_tables(p_len, p_new, reqs, page_size, p_free, free_pages.numel(),
+                                       p_head, tp, ts, blocks, *outs, FLAG_PDL if pdl else 0,
+                                       _stream(dev))
+    if status:
+        raise Nvfp4Error("nvfp4_kv_tables", status)
     return out
 
 
@@ -208,15 +209,17 @@ def nvfp4_kv_append(cache: KVCache, k, v, slots, pdl: bool = False) -> None:
     """Quantise keys and values [tokens, num_kv_heads, head_dim] (float32 or
     bfloat16; slices of a projection's rows need no copy) into the cache at
     ``slots`` int64 [tokens] (-1: skipped)."""
-    ks = _heads(k, "k", cache.device, cache.head_dim)
-    vs = _heads(v, "v", cache.device, cache.head_dim, k.dtype)
-    if k.shape != v.shape or k.shape[1] != cache.num_kv_heads:
-        raise ValueError(f"k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}]")
-    _vector(slots, torch.int64, "slots", cache.device, k.shape[0])
-    _raise("nvfp4_kv_append", library().nvfp4_kv_append(
-        cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], slots.data_ptr(),
-        (FLAG_PDL if pdl else 0) | (FLAG_X_BF16 if k.dtype == torch.bfloat16 else 0),
-        _stream(cache.device)))
+    dev = cache._dev
+    tokens, heads, ks = _heads(k, "k", dev, cache.head_dim)
+    vtokens, vheads, vs = _heads(v, "v", dev, cache.head_dim)
+    if heads != cache.num_kv_heads or vheads != heads or vtokens != tokens or k.dtype is not v.dtype:
+        raise ValueError(f"k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}] of one dtype")
+    status = library().nvfp4_kv_append(
+        cache._desc, k.data_ptr(), ks, v.data_ptr(), vs, tokens,
+        _vector(slots, torch.int64, "slots", dev, tokens),
+        (FLAG_PDL if pdl else 0) | (FLAG_X_BF16 if k.dtype is torch.bfloat16 else 0), _stream(dev))
+    if status:
+        raise Nvfp4Error("nvfp4_kv_append", status)
 
 
 def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
@@ -235,42 +238,48 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     for this stream; False: none, long requests are then not cut).  Output
     float32 or bfloat16 (``out_dtype``, by default q's); with ``return_lse``
     also the natural-log sums [tokens, num_q_heads] float32."""
-    dev = cache.device
-    qs = _heads(q, "q", dev, cache.head_dim)
-    tokens, heads, dim = q.shape
-    _vector(seq_len, torch.int32, "seq_len", dev)
-    reqs = seq_len.shape[0]
+    dev, dim = cache._dev, cache.head_dim
+    tokens, heads, qs = _heads(q, "q", dev, dim)
+    reqs = seq_len.numel()
+    p_seq = _vector(seq_len, torch.int32, "seq_len", dev)
     if q_start is not None:
-        _vector(q_start, torch.int32, "q_start", dev, reqs + 1)
-    elif reqs and tokens % reqs:
-        raise ValueError("without q_start every request has the same number of rows")
+        p_start = _vector(q_start, torch.int32, "q_start", dev, reqs + 1)
+    else:
+        p_start = 0
+        if reqs and tokens % reqs:
+            raise ValueError("without q_start every request has the same number of rows")
     if heads % cache.num_kv_heads:
         raise ValueError(f"{heads} query heads do not share {cache.num_kv_heads} kv heads")
     tp, ts, blocks = _table(block_table, reqs, dev)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=out_dtype or q.dtype, device=dev)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    os_ = _heads(out, "out", dev, dim)
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
+        out = torch.empty((tokens, heads, dim), dtype=out_dtype or q.dtype, device=cache.device)
+        os_ = heads * dim
+        if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+            raise ValueError(f"the output must be float32 or bfloat16, got {out.dtype}")
+    else:
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        os_ = _heads(out, "out", dev, dim)[2]
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device) if return_lse else None
     stream = _stream(dev)
     if workspace is None:
-        workspace = cache._workspace(stream)
-    wp = wn = 0
-    if workspace is not False:
-        _vector(workspace, torch.uint8, "workspace", dev)
-        wp, wn = workspace.data_ptr(), workspace.numel()
+        wp, wn, _keep = cache._workspace(stream)
+    elif workspace is False:
+        wp = wn = 0
+    else:
+        wp, wn = _vector(workspace, torch.uint8, "workspace", dev), workspace.numel()
     if max_q is None:
         max_q = tokens if q_start is not None else (tokens // reqs if reqs else 0)
-    args = _AttentionArgs(
-        q.data_ptr(), qs, heads, tp, ts, blocks, seq_len.data_ptr(),
-        None if q_start is None else q_start.data_ptr(), reqs, tokens, max_q,
+    args = _ATTENTION.pack(
+        q.data_ptr(), qs, heads, tp, ts, blocks, p_seq, p_start, reqs, tokens, max_q,
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(), os_,
-        None if lse is None else lse.data_ptr())
-    _raise("nvfp4_kv_attention", library().nvfp4_kv_attention(
-        cache._ref, ctypes.addressof(args),
-        int(kernel) | (FLAG_PDL if pdl else 0) | (FLAG_X_BF16 if q.dtype == torch.bfloat16 else 0)
-        | (FLAG_Y_BF16 if out.dtype == torch.bfloat16 else 0), wp, wn, stream))
+        lse.data_ptr() if return_lse else 0)
+    status = library().nvfp4_kv_attention(
+        cache._desc, args,
+        kernel | (FLAG_PDL if pdl else 0) | (FLAG_X_BF16 if q.dtype is torch.bfloat16 else 0)
+        | (FLAG_Y_BF16 if out.dtype is torch.bfloat16 else 0), wp, wn, stream)
+    if status:
+        raise Nvfp4Error("nvfp4_kv_attention", status)
     return (out, lse) if return_lse else out
 
 

@@ -389,7 +389,7 @@ def test_output_tensors_and_strides(nv):
     assert torch.equal(got, want) and (wide[:, :4] == 7).all() and (wide[:, 12:] == 7).all()
     # rows that belong to no request are left alone
     out = torch.full((4, 8, 64), 7.0, dtype=BF16, device="cuda")
-    nv.kv_attention(cache, torch.cat([q, q]), table, ints([70, 9]), ints([1, 2, 3]), out=out)
+    nv.kv_attention(cache, torch.cat([q, q]), table, ints([70, 9]), ints([1, 2, 3]), max_q=1, out=out)
     assert (out[[0, 3]] == 7).all() and torch.equal(out[1], nv.kv_attention(
         cache, q[1:], table[:1], ints([70]))[0])
 

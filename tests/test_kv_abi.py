@@ -1,13 +1,11 @@
 """The paged NVFP4 cache's entry points refuse what they cannot take, on the
 host, before any launch.  CPU only: the calls below never reach a kernel."""
-import ctypes
-
 import pytest
 import torch
 
 import nvfp4_w4a4_decode_gb300 as nv
 from nvfp4_w4a4_decode_gb300 import build as nvbuild
-from nvfp4_w4a4_decode_gb300.kv import _AttentionArgs, _CacheDesc
+from nvfp4_w4a4_decode_gb300.kv import _ATTENTION, _CACHE
 
 FAKE = 1 << 20  # a non-null, aligned value never dereferenced
 OK, INVALID, UNSUPPORTED = 0, 1, 2
@@ -57,7 +55,7 @@ def cache(**change):
     d = dict(pool=FAKE, k_g=FAKE, v_g=FAKE, num_pages=10, page_stride=8 * 16 * 144, page_size=16,
              num_kv_heads=8, head_dim=128)
     d.update(change)
-    return _CacheDesc(*d.values())
+    return _CACHE.pack(*(v or 0 for v in d.values()))
 
 
 BAD_CACHES = [(dict(page_size=20), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED),
@@ -70,14 +68,14 @@ BAD_CACHES = [(dict(page_size=20), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED
 @pytest.mark.parametrize("change,status", BAD_CACHES)
 def test_cache_refusals(lib, change, status):
     c = cache(**change)
-    assert lib.nvfp4_kv_append(ctypes.addressof(c), FAKE, 1024, FAKE, 1024, 1, FAKE, 0, None) == status
+    assert lib.nvfp4_kv_append(c, FAKE, 1024, FAKE, 1024, 1, FAKE, 0, None) == status
     a = attention()
-    assert lib.nvfp4_kv_attention(ctypes.addressof(c), ctypes.addressof(a), 0, None, 0, None) == status
+    assert lib.nvfp4_kv_attention(c, a, 0, None, 0, None) == status
 
 
 def test_append_refusals(lib):
     c = cache()
-    ref = ctypes.addressof(c)
+    ref = c
     f = lib.nvfp4_kv_append
     assert f(None, FAKE, 1024, FAKE, 1024, 1, FAKE, 0, None) == INVALID
     assert f(ref, FAKE, 1024, FAKE, 1024, -1, FAKE, 0, None) == INVALID
@@ -97,7 +95,7 @@ def attention(**change):
              seq_len=FAKE, q_start=FAKE, reqs=2, tokens=2, max_q=1, scale=0.1, window=0, out=FAKE,
              out_stride=4096, lse=None)
     d.update(change)
-    return _AttentionArgs(*d.values())
+    return _ATTENTION.pack(*(v or 0 for v in d.values()))
 
 
 @pytest.mark.parametrize("change,status", [
@@ -113,12 +111,12 @@ def attention(**change):
     (dict(tokens=0), OK), (dict(reqs=0), OK)])
 def test_attention_refusals(lib, change, status):
     c, a = cache(), attention(**change)
-    assert lib.nvfp4_kv_attention(ctypes.addressof(c), ctypes.addressof(a), 0, None, 0, None) == status
+    assert lib.nvfp4_kv_attention(c, a, 0, None, 0, None) == status
 
 
 def test_attention_options_and_workspace(lib):
     c, a = cache(), attention()
-    f, cr, ar = lib.nvfp4_kv_attention, ctypes.addressof(c), ctypes.addressof(a)
+    f, cr, ar = lib.nvfp4_kv_attention, c, a
     assert f(cr, None, 0, None, 0, None) == INVALID
     assert f(cr, ar, 0x1000, None, 0, None) == INVALID     # a flag of other calls
     assert f(cr, ar, 0x77, None, 0, None) == UNSUPPORTED   # no such kernel
