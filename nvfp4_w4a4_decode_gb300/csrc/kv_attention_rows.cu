@@ -49,7 +49,17 @@ namespace {
 constexpr int kUnit = 32;       // tokens a unit
 constexpr int kGroup = 64;      // tokens a group
 constexpr int kSub = kGroup / kUnit;
-constexpr int kWarps = 7;       // compute warps: with the copying warp eight, two
+#ifndef KV_BATCH
+#define KV_BATCH 2
+#endif
+constexpr int kBatch = KV_BATCH;
+#ifndef KV_WARPS
+#define KV_WARPS 7
+#endif
+#ifndef KV_CTAS
+#define KV_CTAS 2
+#endif
+constexpr int kWarps = KV_WARPS;       // compute warps: with the copying warp eight, two
                                 // for each of the SM's four register files
 constexpr int kCompute = 32 * kWarps;
 constexpr int kThreads = kCompute + 32;
@@ -271,15 +281,21 @@ struct Cfg {
     static constexpr int kStageBytes = kGroup * D * 9 / 8;
     // two CTAs an SM where the registers allow it: the joins and starts of one
     // overlap the other's stream
-    static constexpr int kCtas = NT == 1 && !SPLIT ? 2 : 1;
-    static constexpr int kStages = 8;
+    static constexpr int kCtas = NT == 1 && !SPLIT ? KV_CTAS : 1;
+    #ifndef KV_ST
+#define KV_ST 7
+#endif
+    static constexpr int kStages = KV_ST;
     static constexpr int kQTerms = SPLIT ? 2 : 1;
     static constexpr int kQBytes = kQTerms * NT * KS * 32 * 8;
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kRedBytes = kWarps * KS * 32 * 16;
     static constexpr int kSmem = kRingBytes + kRedBytes + kQBytes;
     static constexpr bool kQRegs = NT * kQTerms <= 2;  // queries held in registers
-    static_assert((kStages & (kStages - 1)) == 0, "the ring's parity");
+    // A parity tells a phase from its neighbours only: a warp must see every
+    // phase of the slots it reads.  Units are dealt by their number in the CTA's
+    // whole sequence, so a unit's place in the ring always has the same warp.
+    static_assert(kStages * kSub % kWarps == 0, "a ring holds whole rounds of the warps");
 };
 
 template <int D, int NT, bool SPLIT>
@@ -377,85 +393,72 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     const uint32_t ring = smem_u32(smem);
 
     if (warp == kWarps) {
-        // ---- the copying warp: a lane a piece of a group ------------------------------------
+        // ---- the copying warp: four groups at a time, four lanes a group -----------------
         // pages of up to 64 tokens: a piece is a page; longer ones: K codes, V
-        // codes, K scales, V scales of the group's part of the page
-        const bool by_page = a.c.page_shift <= 6;
-        const int pieces = by_page ? kGroup >> a.c.page_shift : 4;
-        const int row_bytes = by_page ? D * 9 / 8 : lane < 2 ? D / 2 : D / 16;
-        const uint32_t bytes = by_page ? (uint32_t)row_bytes << a.c.page_shift
-                                       : (uint32_t)row_bytes * kGroup;
-        const int before_me = lane < 2 ? lane * (D / 2) : D + (lane - 2) * (D / 16);
-        const uint32_t dst0 = ring + (by_page ? lane * bytes : before_me * kGroup);
-        const int64_t piece_at = by_page ? 0 : (int64_t)before_me << a.c.page_shift;
+        // codes, K scales, V scales of the group's part of the page.  (One group
+        // at a time took this warp about 800 cycles each, the SM's whole time
+        // for two groups.)
+        const int P = a.c.page_shift, sub = lane >> 2, piece = lane & 3;
+        const bool by_page = P <= 6;
+        const int pieces = by_page ? kGroup >> P : 4;
+        const bool mine_to_copy = sub < kBatch && piece < pieces;
+        const int row_bytes = by_page ? D * 9 / 8 : piece < 2 ? D / 2 : D / 16;
+        const uint32_t bytes = by_page ? (uint32_t)row_bytes << P : (uint32_t)row_bytes * kGroup;
+        const int before_me = piece < 2 ? piece * (D / 2) : D + (piece - 2) * (D / 16);
+        const uint32_t dst0 = ring + (by_page ? piece * bytes : before_me * kGroup);
+        const uint8_t* src0 = a.c.pool + (by_page ? 0 : (int64_t)before_me << P);
         bool bad = false;
         uint32_t sent = 0;  // groups so far
-        // a lane holds one of 32 entries of the block table, the next 32 (of this
-        // item, or the first of the next) are on their way
-        const int P = a.c.page_shift;
-        auto entries = [&](const Item& x, int32_t base) {
-            const int32_t b = base + lane;
-            return b < a.max_blocks && (int64_t)b << P < x.q.seq
+        // the page of this lane's piece of groups u .. of an item
+        auto page_of = [&](const Item& x, int32_t u) {
+            const int32_t tok = (x.first + u + sub) * kGroup + (by_page ? piece << P : 0);
+            const int32_t b = tok >> P;
+            return mine_to_copy && u + sub < x.u1 && tok < x.q.seq && b < a.max_blocks
                        ? a.table[x.r * a.table_stride + b]
                        : -2;  // nothing of the request there
         };
-        auto first_entry = [&](const Item& x) { return ((x.first + x.u0) * kGroup) >> P; };
-        int32_t base = 0, ids = -2;
-        if (more) {
-            base = first_entry(it);
-            ids = entries(it, base);
-        }
-        bool go = true;
-        while (more && go) {
+        int32_t u = more ? it.u0 : 0;
+        int32_t page = more ? page_of(it, u) : -2;
+        while (more) {
             Item nx = it;
-            const bool nmore = item_next<R>(a, sh, nx);
-            const int32_t end = ((it.first + it.u1) * kGroup + (1 << P) - 1) >> P;
-            auto following = [&]() {
-                return base + 32 < end ? entries(it, base + 32)
-                                       : nmore ? entries(nx, first_entry(nx)) : -2;
-            };
-            int32_t nids = following();
-            for (int32_t u = it.u0; u < it.u1; ++u) {
-                const int32_t entry = ((it.first + u) * kGroup) >> P;
-                if (entry >= base + 32) {
-                    base += 32;
-                    ids = nids;
-                    nids = following();
-                }
-                int32_t page = __shfl_sync(0xFFFFFFFFu, ids, entry - base + (by_page ? lane : 0));
-                page = lane < pieces ? page : -2;
-                const uint32_t slot = sent % ST;
-                const uint32_t fb = smem_u32(&full_bar[slot]);
-                go = __all_sync(0xFFFFFFFFu,
-                                sent < ST || mbar_wait(smem_u32(&empty_bar[slot]),
-                                                       (sent / ST - 1) & 1, abort_flag, a.status));
-                if (!go)
-                    break;
-                const bool ok = page >= 0 && page < a.c.num_pages;
-                bad |= !ok && page != -2;
-                // a piece without a page is left out: its place holds old bytes
-                const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
-                if (lane == 0) {
-                    const uint32_t all =
-                        by_page ? __popc(there) * bytes : there ? C::kStageBytes : 0;
-                    if (all)
-                        mbar_expect_tx(fb, all);
-                    else
-                        mbar_arrive(fb);
-                }
-                __syncwarp();
-                if (ok) {
-                    const int32_t off = by_page ? 0 : ((it.first + u) * kGroup) & ((1 << P) - 1);
-                    bulk_copy(dst0 + slot * C::kStageBytes,
-                              a.c.pool + page * a.c.page_stride + it.h * head_bytes + piece_at +
-                                  off * row_bytes,
-                              bytes, fb);
-                }
-                ++sent;
+            int32_t nu = u + kBatch;
+            bool nmore = true;
+            if (nu >= it.u1) {
+                nmore = item_next<R>(a, sh, nx);
+                nu = nx.u0;
             }
+            const int32_t npage = nmore ? page_of(nx, nu) : -2;
+            const int n = min(kBatch, it.u1 - u);
+            const uint32_t k = sent + sub, slot = k % ST;
+            const uint32_t fb = smem_u32(&full_bar[slot]);
+            const bool free_slot =
+                sub >= n || k < ST ||
+                mbar_wait(smem_u32(&empty_bar[slot]), (k / ST - 1) & 1, abort_flag, a.status);
+            if (!__all_sync(0xFFFFFFFFu, free_slot))
+                break;
+            const bool ok = page >= 0 && page < a.c.num_pages;
+            bad |= !ok && page != -2;
+            // a piece without a page is left out: its place holds old bytes
+            const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok) >> (4 * sub) & 0xFu;
+            if (piece == 0 && sub < n) {
+                const uint32_t all = by_page ? __popc(there) * bytes : there ? C::kStageBytes : 0;
+                if (all)
+                    mbar_expect_tx(fb, all);
+                else
+                    mbar_arrive(fb);
+            }
+            __syncwarp();
+            if (ok) {
+                const int32_t off =
+                    by_page ? 0 : ((it.first + u + sub) * kGroup) & ((1 << P) - 1);
+                bulk_copy(dst0 + slot * C::kStageBytes,
+                          src0 + page * a.c.page_stride + it.h * head_bytes + off * row_bytes,
+                          bytes, fb);
+            }
+            sent += n;
             it = nx;
-            base = nmore ? first_entry(nx) : 0;
-            ids = nids;
+            u = nu;
+            page = npage;
             more = nmore;
         }
         if (*abort_flag)  // copies still in flight must land before the CTA ends
@@ -483,7 +486,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     const int code_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 2);
     const int scale_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 16);
     const int ka = token_of_row(g), v_tok = token_of_row(2 * t), v_odd = token_of_row(2 * t + 1) - v_tok;
-    constexpr int HB = NT == 1 ? kUnit / 16 : 1;  // 16-token halves in flight at once
+    #ifndef KV_HB
+#define KV_HB 2
+#endif
+    constexpr int HB = NT == 1 ? KV_HB : 1;  // 16-token halves in flight at once
 
     // four consecutive elements of row c of an item's query tile
     auto query = [&](const Item& x, int c) {
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         const int32_t p1 = it.q.seq - it.q.nq + (it.row1 - 1) / a.group;
         const int32_t all_hi = p0, all_lo = a.window > 0 ? p1 - a.window + 1 : 0;
 
-        for (int i = warp; i < units; i += kWarps) {
+        for (int i = (warp + kWarps - taken * kSub % kWarps) % kWarps; i < units; i += kWarps) {
             const uint32_t group = taken + i / kSub, slot = group % ST;
             const int32_t unit0 = first_tok + i * kUnit;
             mbar_wait(full0 + 8 * slot, (group / ST) & 1, abort_flag, a.status);
