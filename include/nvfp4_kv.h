@@ -141,7 +141,11 @@ typedef struct {
 /*
  * options: a kernel choice in the low byte --
  *   NVFP4_KERNEL_AUTO          the library's choice
- *   NVFP4_KERNEL_KV_ROWS       query rows as the narrow side of mma.sync tiles
+ *   NVFP4_KERNEL_KV_ROWS       query rows as the narrow side of mma.sync tiles:
+ *                              few rows a request; any dtype
+ *   NVFP4_KERNEL_KV_TILE       tcgen05 tiles of 128 query rows: many rows a
+ *                              request; BF16 queries and outputs only
+ *                              (NVFP4_ERR_UNSUPPORTED otherwise)
  * -- OR-ed with NVFP4_FLAG_X_BF16, NVFP4_FLAG_Y_BF16, NVFP4_FLAG_PDL.
  * The keys of all requests are one list of work that the SMs share equally:
  * a request cut between SMs is joined through the workspace in a fixed order
@@ -155,6 +159,7 @@ typedef struct {
  * max_blocks * page_size below 2^30 (else NVFP4_ERR_UNSUPPORTED).  One kernel.
  */
 #define NVFP4_KERNEL_KV_ROWS 1u
+#define NVFP4_KERNEL_KV_TILE 2u
 
 int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
                        uint32_t options, void* workspace, size_t workspace_bytes, void* stream);

@@ -90,8 +90,18 @@ struct KvAttnArgs {
     unsigned* status;
 };
 
+// The workspace's arrival counters (zero between calls; both kernels' lie
+// here), then partial results.
+constexpr int64_t kKvCountBytes = 4096;
+
+// Few query rows a request, any dtype.
 int64_t kv_rows_workspace_bytes(int dim);
 cudaError_t launch_kv_rows(const KvAttnArgs& a, void* workspace, int64_t workspace_bytes,
+                           cudaStream_t stream, bool pdl);
+
+// Many query rows a request (tcgen05); BF16 queries and outputs only.
+int64_t kv_tile_workspace_bytes(int dim);
+cudaError_t launch_kv_tile(const KvAttnArgs& a, void* workspace, int64_t workspace_bytes,
                            cudaStream_t stream, bool pdl);
 
 // Launch with or without programmatic dependent launch (every kernel of the
@@ -117,63 +127,6 @@ __device__ __forceinline__ void kv_pdl_begin()
 {
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// ---- the attention kernels' work list ------------------------------------------
-// An item is (request, kv head, tile of query rows): rows token * group + head,
-// tiles of `R` of them.  Its units are the blocks of UT tokens that any of its
-// rows sees (one unit when it sees none, so that its rows are written).  Items
-// are ordered request, head, tile; the units of all items form one list, cut
-// into equal shares, one a CTA.
-
-struct KvReq {
-    int32_t seq;   // tokens in the cache
-    int32_t base;  // first query row
-    int32_t nq;    // query rows (tokens)
-};
-
-__device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
-{
-    KvReq q;
-    int32_t b, e;
-    if (a.q_start) {
-        b = a.q_start[r];
-        e = a.q_start[r + 1];
-    } else {
-        b = r * a.q_per_req;
-        e = b + a.q_per_req;
-    }
-    b = min(max(b, 0), a.tokens);
-    e = min(max(e, b), a.tokens);
-    q.base = b;
-    q.nq = e - b;
-    const int64_t cap = (int64_t)a.max_blocks << a.c.page_shift;
-    q.seq = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
-    return q;
-}
-
-// Whether a request is longer than its table (its end is then cut off).
-__device__ __forceinline__ bool kv_too_long(const KvAttnArgs& a, int r)
-{
-    return (int64_t)a.seq_len[r] > (int64_t)a.max_blocks << a.c.page_shift;
-}
-
-// Units [first, first + n) of a tile of rows [row0, row0 + rows).
-template <int UT>
-__device__ __forceinline__ void kv_tile_units(const KvAttnArgs& a, const KvReq& q, int row0,
-                                              int row1, int32_t& first, int32_t& n)
-{
-    const int32_t i0 = row0 / a.group, i1 = (row1 - 1) / a.group;
-    const int32_t p0 = q.seq - q.nq;
-    const int32_t hi = p0 + i1 + 1;  // keys [lo, hi)
-    const int32_t lo = a.window > 0 ? max(0, p0 + i0 - a.window + 1) : 0;
-    if (hi <= lo) {
-        first = 0;
-        n = 1;
-        return;
-    }
-    first = lo / UT;
-    n = (hi + UT - 1) / UT - first;
 }
 
 }  // namespace nvfp4

@@ -11,6 +11,10 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
+// Query rows a request (tokens * heads of a group) above which the tcgen05
+// kernel takes BF16 attention.
+constexpr int64_t kTileRows = 64;
+
 bool aligned(const void* p, uintptr_t a)
 {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
@@ -136,7 +140,9 @@ int64_t nvfp4_kv_attention_workspace_size(int64_t head_dim)
         return -NVFP4_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128)
         return -NVFP4_ERR_UNSUPPORTED;
-    return nvfp4::kv_rows_workspace_bytes((int)head_dim);
+    const int64_t rows = nvfp4::kv_rows_workspace_bytes((int)head_dim);
+    const int64_t tile = nvfp4::kv_tile_workspace_bytes((int)head_dim);
+    return rows > tile ? rows : tile;
 }
 
 int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
@@ -161,7 +167,9 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
         r.max_blocks >= (kMaxTokens >> a.c.page_shift))
         return NVFP4_ERR_UNSUPPORTED;
     const uint32_t kern = options & NVFP4_KERNEL_MASK;
-    if (kern != NVFP4_KERNEL_AUTO && kern != NVFP4_KERNEL_KV_ROWS)
+    const bool all_bf16 = (options & NVFP4_FLAG_X_BF16) && (options & NVFP4_FLAG_Y_BF16);
+    if (kern != NVFP4_KERNEL_AUTO && kern != NVFP4_KERNEL_KV_ROWS &&
+        !(kern == NVFP4_KERNEL_KV_TILE && all_bf16))
         return NVFP4_ERR_UNSUPPORTED;
     if (r.tokens == 0 || r.reqs == 0)
         return NVFP4_OK;
@@ -197,9 +205,11 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     a.lse = r.lse;
     a.q_bf16 = q_bf16;
     a.out_bf16 = out_bf16;
-    return from_cuda(nvfp4::launch_kv_rows(a, workspace, (int64_t)workspace_bytes,
-                                           static_cast<cudaStream_t>(stream),
-                                           (options & NVFP4_FLAG_PDL) != 0));
+    const bool tile = kern == NVFP4_KERNEL_KV_TILE ||
+                      (kern == NVFP4_KERNEL_AUTO && all_bf16 && (int64_t)a.max_q * a.group > kTileRows);
+    const auto launch = tile ? nvfp4::launch_kv_tile : nvfp4::launch_kv_rows;
+    return from_cuda(launch(a, workspace, (int64_t)workspace_bytes,
+                            static_cast<cudaStream_t>(stream), (options & NVFP4_FLAG_PDL) != 0));
 }
 
 }  // extern "C"

@@ -36,9 +36,8 @@
 // sets NVFP4_DEVICE_WAIT_TIMEOUT and all waits after it are passed over.
 //
 // Bound by the cache's bytes for one token a request.
-#include "../../include/nvfp4_kv.h"
 #include "formats.cuh"
-#include "kv.cuh"
+#include "kv_work.cuh"
 #include "launch_cache.cuh"
 #include "mma_frag.cuh"
 
@@ -68,87 +67,17 @@ constexpr int kMaxCtas = 512;   // workspace extent
 constexpr int kMaxRows = 32;
 constexpr float kRaise = 8.0f;  // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;   // p = 2^(s - m + kLift)
-constexpr long long kWaitBudget = 2000000000LL;  // clock cycles a wait may take
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p)
-{
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(done)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return done != 0;
-}
-// Wait for phase `parity`; false when the budget (or another wait's) ran out.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                            unsigned* status)
-{
-    const long long t0 = clock64();
-    while (!mbar_test(bar, parity)) {
-        if (*abort_flag)
-            return false;
-        if (clock64() - t0 > kWaitBudget) {
-            *abort_flag = 1;
-            atomicOr(status, (unsigned)NVFP4_DEVICE_WAIT_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned* status)
-{
-    return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, status);
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-                 "[%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 // Barrier of the compute warps.
 __device__ __forceinline__ void compute_sync()
 {
     asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t movm_trans(uint32_t v)
 {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
 
@@ -167,111 +96,6 @@ __device__ __forceinline__ int token_of_row(int k)
 {
     const int j = (k & 7) >> 1;
     return (k & 8) | ((k & 1) ? 4 + (j ^ 1) : j);
-}
-
-// The place of an item in the work list.
-struct Item {
-    int r, h, tile;
-    KvReq q;
-    int rows;       // query rows of the request (tokens * group)
-    int row0, row1;
-    int64_t begin;  // its place in the list: kItemCost, then its groups
-    int32_t first, n;
-    int32_t u0, u1;  // the groups of this CTA's share
-};
-
-// A CTA's share of the list, and whether items may be cut between shares.
-struct Share {
-    int64_t lo, hi;
-    bool cut;
-};
-
-template <int R>
-__device__ __forceinline__ void item_units(const KvAttnArgs& a, const Share& s, Item& it)
-{
-    it.row0 = it.tile * R;
-    it.row1 = min(it.row0 + R, it.rows);
-    kv_tile_units<kGroup>(a, it.q, it.row0, it.row1, it.first, it.n);
-}
-
-// The first item of the first request at or after r that has rows.
-template <int R>
-__device__ __forceinline__ bool item_request(const KvAttnArgs& a, const Share& s, Item& it, int r)
-{
-    for (; r < a.reqs; ++r) {
-        it.q = kv_req(a, r);
-        if (it.q.nq > 0)
-            break;
-    }
-    it.r = r;
-    it.h = it.tile = 0;
-    if (r >= a.reqs)
-        return false;
-    it.rows = it.q.nq * a.group;
-    item_units<R>(a, s, it);
-    return true;
-}
-
-template <int R>
-__device__ __forceinline__ bool item_after(const KvAttnArgs& a, const Share& s, Item& it)
-{
-    it.begin += kItemCost + it.n;
-    if ((it.tile + 1) * R < it.rows) {
-        ++it.tile;
-        item_units<R>(a, s, it);
-        return true;
-    }
-    it.tile = 0;
-    if (++it.h < a.c.heads) {
-        item_units<R>(a, s, it);
-        return true;
-    }
-    return item_request<R>(a, s, it, it.r + 1);
-}
-
-// Steps on, from an item that may have no group in the share, to one that has.
-template <int R>
-__device__ __forceinline__ bool item_settle(const KvAttnArgs& a, const Share& s, Item& it, bool more)
-{
-    for (; more; more = item_after<R>(a, s, it)) {
-        const int64_t at = it.begin + kItemCost;  // place of group 0
-        if (s.cut) {
-            if (at >= s.hi)
-                return false;
-            it.u0 = (int32_t)max((int64_t)0, s.lo - at);
-            it.u1 = (int32_t)min((int64_t)it.n, s.hi - at);
-            if (it.u0 < it.u1)
-                return true;
-        } else {  // an uncut item belongs to the share that holds its group 0
-            if (at >= s.hi)
-                return false;
-            it.u0 = 0;
-            it.u1 = it.n;
-            if (at >= s.lo)
-                return true;
-        }
-    }
-    return false;
-}
-
-template <int R>
-__device__ __forceinline__ bool item_next(const KvAttnArgs& a, const Share& s, Item& it)
-{
-    return item_settle<R>(a, s, it, item_after<R>(a, s, it));
-}
-
-// Places of one kv head of a request.
-template <int R>
-__device__ __forceinline__ int64_t head_places(const KvAttnArgs& a, const KvReq& q)
-{
-    int64_t s = 0;
-    const int rows = q.nq * a.group;
-    for (int row0 = 0; row0 < rows; row0 += R) {
-        int32_t first, n;
-        kv_tile_units<kGroup>(a, q, row0, min(row0 + R, rows), first, n);
-        s += kItemCost + n;
-    }
-    return s;
 }
 
 template <int D, int NT, bool SPLIT>
@@ -304,11 +128,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
 {
     using C = Cfg<D, NT, SPLIT>;
     constexpr int R = C::R, KS = C::KS, ST = C::kStages;
+    using Work = KvWork<R, kGroup, kItemCost>;
+    using Item = KvItem;
+    using Share = KvShare;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
-    __shared__ int64_t warp_sum[kThreads / 32];
-    __shared__ int64_t found_rem;
-    __shared__ int found_r;
+    __shared__ typename Work::Smem work_sm;
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_f[R];
     __shared__ int32_t sm_pos[R];
     __shared__ int last_s, abort_s;
@@ -327,67 +152,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     }
     kv_pdl_begin();
 
-    // ---- this CTA's share of the list ------------------------------------------------
-    const int per = (a.reqs + kThreads - 1) / kThreads;
-    const int ra = min(tid * per, a.reqs), rb = min(ra + per, a.reqs);
-    int64_t mine = 0;
-    for (int r = ra; r < rb; ++r) {
-        mine += a.c.heads * head_places<R>(a, kv_req(a, r));
-        if (blockIdx.x == 0 && kv_too_long(a, r))
-            atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
-    }
-    int64_t inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-        if (lane >= d)
-            inc += o;
-    }
-    if (lane == 31)
-        warp_sum[warp] = inc;
-    __syncthreads();
-    int64_t before = inc - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp)
-            before += warp_sum[w];
-        total += warp_sum[w];
-    }
-    // at least an item's cost and a unit a warp
-    const int64_t share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kItemCost + 2));
+    // at least an item's cost and a group for each pair of warps
     Share sh;
-    sh.lo = share * blockIdx.x;
-    sh.hi = min(sh.lo + share, total);
-    sh.cut = a.part != nullptr;
-    if (sh.lo >= total)
-        return;
-    if (sh.lo >= before && sh.lo < before + mine) {
-        int64_t at = before;
-        for (int r = ra; r < rb; ++r) {
-            const int64_t n = a.c.heads * head_places<R>(a, kv_req(a, r));
-            if (sh.lo < at + n) {
-                found_r = r;
-                found_rem = sh.lo - at;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
     Item it;
-    it.begin = sh.lo - found_rem;
-    bool more = item_request<R>(a, sh, it, found_r);
-    if (more) {
-        const int64_t hu = head_places<R>(a, it.q);
-        it.h = (int)(found_rem / hu);
-        it.begin += it.h * hu;
-        while (it.begin + kItemCost + it.n <= sh.lo) {
-            it.begin += kItemCost + it.n;
-            ++it.tile;
-            item_units<R>(a, sh, it);
-        }
-    }
-    more = item_settle<R>(a, sh, it, more);
+    bool more = Work::template start<kThreads>(a, work_sm, kItemCost + 2, sh, it);
+    if (sh.lo >= sh.hi)
+        return;
 
     const int64_t head_bytes = kv_head_bytes(a.c.page_shift, D);
     const uint32_t ring = smem_u32(smem);
@@ -424,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             int32_t nu = u + kBatch;
             bool nmore = true;
             if (nu >= it.u1) {
-                nmore = item_next<R>(a, sh, nx);
+                nmore = Work::next(a, sh, nx);
                 nu = nx.u0;
             }
             const int32_t npage = nmore ? page_of(nx, nu) : -2;
@@ -465,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             for (uint32_t k = sent > ST ? sent - ST : 0; k < sent; ++k) {
                 const long long t0 = clock64();
                 while (!mbar_test(smem_u32(&full_bar[k % ST]), (k / ST) & 1) &&
-                       clock64() - t0 < kWaitBudget) {
+                       clock64() - t0 < kKvWaitBudget) {
                 }
             }
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
@@ -814,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         taken += u1 - u0;
         // the next item's queries are on their way during the join
         Item nx = it;
-        more = item_next<R>(a, sh, nx);
+        more = Work::next(a, sh, nx);
         if (more) {
 #pragma unroll
             for (int j = 0; j < QR; ++j)
@@ -908,8 +678,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         }
         if (!whole) {
             // ---- join the CTAs: the last to arrive sums all parts in CTA order ----------------
-            const int ca = (int)((it.begin + kItemCost) / share);
-            const int cb = (int)((it.begin + kItemCost + it.n - 1) / share);
+            const int ca = Work::first_cta(sh, it), cb = Work::last_cta(sh, it);
             __threadfence();
             compute_sync();
             if (tid == 0) {
@@ -983,14 +752,12 @@ cudaError_t launch_rows(const KvAttnArgs& a, cudaStream_t stream, bool pdl)
     return launch<D, 4, SPLIT>(a, stream, pdl);
 }
 
-constexpr int64_t kCountBytes = kMaxCtas * sizeof(unsigned);
-
 }  // namespace
 
 // Counters, then two partial results a CTA.
 int64_t kv_rows_workspace_bytes(int dim)
 {
-    return kCountBytes + (int64_t)kMaxCtas * 2 * (kMaxRows * dim + 2 * kMaxRows) * sizeof(float);
+    return kKvCountBytes + (int64_t)kMaxCtas * 2 * (kMaxRows * dim + 2 * kMaxRows) * sizeof(float);
 }
 
 cudaError_t launch_kv_rows(const KvAttnArgs& args, void* workspace, int64_t workspace_bytes,
@@ -1001,7 +768,7 @@ cudaError_t launch_kv_rows(const KvAttnArgs& args, void* workspace, int64_t work
     a.part = nullptr;
     if (workspace_bytes >= kv_rows_workspace_bytes(a.c.dim)) {
         a.count = static_cast<unsigned*>(workspace);
-        a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCountBytes);
+        a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCountBytes);
     }
     const bool split = !a.q_bf16 || !a.out_bf16;
     if (a.c.dim == 128)

@@ -1,0 +1,371 @@
+// kv_work.cuh -- what the attention kernels over the paged cache share: bounded
+// mbarrier waits, and the list of work that is cut into equal shares on the
+// device (lengths are device data, and a captured graph replays with others).
+#pragma once
+
+#include "../../include/nvfp4_kv.h"
+#include "kv.cuh"
+
+namespace nvfp4 {
+
+constexpr long long kKvWaitBudget = 2000000000LL;  // clock cycles a wait may take
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// Wait for phase `parity`; false when the budget (or another wait's) ran out.
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            unsigned* status)
+{
+    const long long t0 = clock64();
+    while (!mbar_test(bar, parity)) {
+        if (*abort_flag)
+            return false;
+        if (clock64() - t0 > kKvWaitBudget) {
+            *abort_flag = 1;
+            atomicOr(status, (unsigned)NVFP4_DEVICE_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned* status)
+{
+    return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// ---- the work list ---------------------------------------------------------------
+// An item is (request, kv head, tile of R query rows), rows being token * group
+// + head of the group.  Its units are the blocks of UT tokens that any of its
+// rows sees (one when it sees none, so that its rows are written).  Items are
+// ordered request, head, tile; each takes COST places, which stand for its
+// start and its join, and one a unit.  The list is cut into equal shares, one a
+// CTA; an item whose units lie in several shares is cut between them.
+
+struct KvReq {
+    int32_t seq;   // tokens in the cache
+    int32_t base;  // first query row
+    int32_t nq;    // query rows (tokens)
+};
+
+__device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
+{
+    KvReq q;
+    int32_t b, e;
+    if (a.q_start) {
+        b = a.q_start[r];
+        e = a.q_start[r + 1];
+    } else {
+        b = r * a.q_per_req;
+        e = b + a.q_per_req;
+    }
+    b = min(max(b, 0), a.tokens);
+    e = min(max(e, b), a.tokens);
+    q.base = b;
+    q.nq = e - b;
+    const int64_t cap = (int64_t)a.max_blocks << a.c.page_shift;
+    q.seq = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
+    return q;
+}
+
+// Whether a request is longer than its table (its end is then cut off).
+__device__ __forceinline__ bool kv_too_long(const KvAttnArgs& a, int r)
+{
+    return (int64_t)a.seq_len[r] > (int64_t)a.max_blocks << a.c.page_shift;
+}
+
+struct KvItem {
+    int r, h, tile;
+    KvReq q;
+    int rows;       // query rows of the request (tokens * group)
+    int row0, row1;
+    int64_t begin;  // its place in the list: COST, then its units
+    int32_t first, n;
+    int32_t u0, u1;  // the units of this CTA's share
+};
+
+// A CTA's share of the list, and whether items may be cut between shares.
+struct KvShare {
+    int64_t lo, hi, size;
+    bool cut;
+};
+
+template <int R, int UT, int COST>
+struct KvWork {
+    // Units [first, first + n) of the rows [row0, row1) of a request.
+    static __device__ __forceinline__ void tile_units(const KvAttnArgs& a, const KvReq& q, int row0,
+                                                      int row1, int32_t& first, int32_t& n)
+    {
+        const int32_t i0 = row0 / a.group, i1 = (row1 - 1) / a.group;
+        const int32_t p0 = q.seq - q.nq;
+        const int32_t hi = p0 + i1 + 1;  // keys [lo, hi)
+        const int32_t lo = a.window > 0 ? max(0, p0 + i0 - a.window + 1) : 0;
+        if (hi <= lo) {
+            first = 0;
+            n = 1;
+            return;
+        }
+        first = lo / UT;
+        n = (hi + UT - 1) / UT - first;
+    }
+
+    static __device__ __forceinline__ void units(const KvAttnArgs& a, KvItem& it)
+    {
+        it.row0 = it.tile * R;
+        it.row1 = min(it.row0 + R, it.rows);
+        tile_units(a, it.q, it.row0, it.row1, it.first, it.n);
+    }
+
+    // The first item of the first request at or after r that has rows.
+    static __device__ __forceinline__ bool request(const KvAttnArgs& a, KvItem& it, int r)
+    {
+        for (; r < a.reqs; ++r) {
+            it.q = kv_req(a, r);
+            if (it.q.nq > 0)
+                break;
+        }
+        it.r = r;
+        it.h = it.tile = 0;
+        if (r >= a.reqs)
+            return false;
+        it.rows = it.q.nq * a.group;
+        units(a, it);
+        return true;
+    }
+
+    static __device__ __forceinline__ bool after(const KvAttnArgs& a, KvItem& it)
+    {
+        it.begin += COST + it.n;
+        if ((it.tile + 1) * R < it.rows) {
+            ++it.tile;
+            units(a, it);
+            return true;
+        }
+        it.tile = 0;
+        if (++it.h < a.c.heads) {
+            units(a, it);
+            return true;
+        }
+        return request(a, it, it.r + 1);
+    }
+
+    // Steps on, from an item that may have no unit in the share, to one that has.
+    static __device__ __forceinline__ bool settle(const KvAttnArgs& a, const KvShare& s, KvItem& it,
+                                                  bool more)
+    {
+        for (; more; more = after(a, it)) {
+            const int64_t at = it.begin + COST;  // place of unit 0
+            if (at >= s.hi)
+                return false;
+            if (s.cut) {
+                it.u0 = (int32_t)max((int64_t)0, s.lo - at);
+                it.u1 = (int32_t)min((int64_t)it.n, s.hi - at);
+                if (it.u0 < it.u1)
+                    return true;
+            } else {  // an uncut item belongs to the share that holds its unit 0
+                it.u0 = 0;
+                it.u1 = it.n;
+                if (at >= s.lo)
+                    return true;
+            }
+        }
+        return false;
+    }
+
+    static __device__ __forceinline__ bool next(const KvAttnArgs& a, const KvShare& s, KvItem& it)
+    {
+        return settle(a, s, it, after(a, it));
+    }
+
+    // The CTAs that hold the first and the last unit of an item.
+    static __device__ __forceinline__ int first_cta(const KvShare& s, const KvItem& it)
+    {
+        return (int)((it.begin + COST) / s.size);
+    }
+    static __device__ __forceinline__ int last_cta(const KvShare& s, const KvItem& it)
+    {
+        return (int)((it.begin + COST + it.n - 1) / s.size);
+    }
+
+    // Places of one kv head of a request, summed by one thread or by a warp.
+    static __device__ __forceinline__ int64_t head_places(const KvAttnArgs& a, const KvReq& q,
+                                                          int start, int step)
+    {
+        int64_t s = 0;
+        const int rows = q.nq * a.group;
+        for (int64_t row0 = (int64_t)start * R; row0 < rows; row0 += (int64_t)step * R) {
+            int32_t first, n;
+            tile_units(a, q, (int)row0, (int)min(row0 + R, (int64_t)rows), first, n);
+            s += COST + n;
+        }
+        return s;
+    }
+    static __device__ __forceinline__ int64_t head_places_warp(const KvAttnArgs& a, const KvReq& q)
+    {
+        int64_t s = head_places(a, q, threadIdx.x & 31, 32);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        return s;
+    }
+
+    struct Smem {
+        int64_t warp_sum[32];
+        int64_t req_sum[256];
+        int64_t rem;
+        int r;
+    };
+
+    // The whole CTA (THREADS threads) computes its share of the list and the
+    // first item with a unit in it; false when there is none.
+    template <int THREADS>
+    static __device__ bool start(const KvAttnArgs& a, Smem& sm, int64_t least, KvShare& sh,
+                                 KvItem& it)
+    {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        // few requests of many tiles: a warp sums a request; else a thread a run of them
+        const bool by_warp = a.reqs <= 256 && (int64_t)a.tokens * a.group > 2 * (int64_t)R * a.reqs;
+        int per = (a.reqs + THREADS - 1) / THREADS;
+        if (by_warp) {
+            for (int r = warp; r < a.reqs; r += THREADS / 32) {
+                const int64_t s = head_places_warp(a, kv_req(a, r));
+                if (lane == 0)
+                    sm.req_sum[r] = a.c.heads * s;
+            }
+            per = (a.reqs + THREADS - 1) / THREADS;
+            __syncthreads();
+        }
+        auto places = [&](int r) {
+            return by_warp ? sm.req_sum[r] : a.c.heads * head_places(a, kv_req(a, r), 0, 1);
+        };
+        const int ra = min(tid * per, a.reqs), rb = min(ra + per, a.reqs);
+        int64_t mine = 0;
+        for (int r = ra; r < rb; ++r) {
+            mine += places(r);
+            if (blockIdx.x == 0 && kv_too_long(a, r))
+                atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
+        }
+        int64_t inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            if (lane >= d)
+                inc += o;
+        }
+        if (lane == 31)
+            sm.warp_sum[warp] = inc;
+        __syncthreads();
+        int64_t before = inc - mine, total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp)
+                before += sm.warp_sum[w];
+            total += sm.warp_sum[w];
+        }
+        sh.size = max((total + gridDim.x - 1) / gridDim.x, least);
+        sh.lo = sh.size * blockIdx.x;
+        sh.hi = min(sh.lo + sh.size, total);
+        sh.cut = a.part != nullptr;
+        if (sh.lo >= total)
+            return false;
+        if (sh.lo >= before && sh.lo < before + mine) {
+            int64_t at = before;
+            for (int r = ra; r < rb; ++r) {
+                const int64_t n = places(r);
+                if (sh.lo < at + n) {
+                    sm.r = r;
+                    sm.rem = sh.lo - at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        it.begin = sh.lo - sm.rem;
+        if (!request(a, it, sm.r))
+            return false;
+        // the head, then the tile, that holds place sh.lo; 32 tiles at a time
+        const int64_t head = places_of_head(a, it.q);
+        it.h = (int)(sm.rem / head);
+        it.begin += it.h * head;
+        const int tiles = (it.rows + R - 1) / R;
+        for (int t0 = 0; t0 < tiles; t0 += 32) {
+            int32_t first, n = 0;
+            const int t = t0 + lane;
+            if (t < tiles) {
+                tile_units(a, it.q, t * R, min(t * R + R, it.rows), first, n);
+                n += COST;
+            }
+            int32_t sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d)
+                    sum += o;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, it.begin + sum <= sh.lo);
+            const int skip = __popc(past);  // whole tiles before sh.lo
+            if (skip < 32) {
+                it.tile = t0 + skip;
+                it.begin += skip ? __shfl_sync(0xFFFFFFFFu, sum, skip - 1) : 0;
+                break;
+            }
+            it.begin += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        units(a, it);
+        return settle(a, sh, it, true);
+    }
+
+private:
+    static __device__ __forceinline__ int64_t places_of_head(const KvAttnArgs& a, const KvReq& q)
+    {
+        return (int64_t)q.nq * a.group <= 4 * R ? head_places(a, q, 0, 1) : head_places_warp(a, q);
+    }
+};
+
+}  // namespace nvfp4

@@ -10,9 +10,11 @@ import torch
 
 __all__ = ["KVCache", "KVTables", "kv_page_bytes", "kv_pool", "kv_tables", "kv_append",
            "kv_attention", "kv_attention_workspace", "nvfp4_kv_tables", "nvfp4_kv_append",
-           "nvfp4_kv_attention", "nvfp4_kv_page_bytes", "KERNEL_KV_ROWS", "DEVICE_KV_RANGE"]
+           "nvfp4_kv_attention", "nvfp4_kv_page_bytes", "KERNEL_KV_ROWS", "KERNEL_KV_TILE",
+           "DEVICE_KV_RANGE"]
 
 KERNEL_KV_ROWS = 1
+KERNEL_KV_TILE = 2
 DEVICE_KV_RANGE = 2
 
 _p = ctypes.c_void_p
@@ -233,7 +235,8 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     query row (None: the same number each).  A request's query rows are its
     last tokens; a row sees its own and earlier positions, the last ``window``
     of them when that is not 0.  ``max_q``: the most rows a request has, if
-    known (a hint).  Rows that see nothing get zeros and lse = -inf.
+    known (a hint).  ``kernel`` forces KERNEL_KV_ROWS or KERNEL_KV_TILE
+    (bfloat16 q and output only).  Rows that see nothing get zeros and lse = -inf.
     ``workspace``: one of ``kv_attention_workspace`` (None: the cache's own
     for this stream; False: none, long requests are then not cut).  Output
     float32 or bfloat16 (``out_dtype``, by default q's); with ``return_lse``

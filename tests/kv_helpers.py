@@ -40,13 +40,14 @@ def request_values(cache, table_row, n):
 
 
 def attention(cache, q, table, seqs, counts, scale=None, window=0):
-    """float64 (out, lse, A, S): the definition, sum p |V| / l of each output
-    and the largest sum |q| |K| scale of each row (for the bounds)."""
+    """float64 (out, lse, A, S, B): the definition, sum p |V| / l of each output,
+    the largest sum |q| |K| scale of each row, and sum |V| over the keys that a
+    row sees (for the bounds)."""
     heads, dim = q.shape[1:]
     group = heads // cache.num_kv_heads
     scale = dim ** -0.5 if scale is None else scale
     q = q.double()
-    out, mag = torch.zeros_like(q), torch.zeros_like(q)
+    out, mag, reach = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q)
     lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device=q.device)
     big = torch.zeros_like(lse)
     t = 0
@@ -68,10 +69,11 @@ def attention(cache, q, table, seqs, counts, scale=None, window=0):
             safe = torch.where(l == 0, 1.0, l)
             out[t:t + c] = (p @ v / safe).transpose(0, 1)
             mag[t:t + c] = (p @ v.abs() / safe).transpose(0, 1)
+            reach[t:t + c] = ((~hide).double() @ v.abs()).transpose(0, 1)
             lse[t:t + c] = (m + l.log())[..., 0].T
             big[t:t + c] = (qr.abs() @ k.abs().transpose(1, 2) * abs(scale)).amax(-1).T
         t += c
-    return out, lse, mag, big
+    return out, lse, mag, big, reach
 
 
 def check_attention(out, lse, ref, in_dtype):
@@ -82,10 +84,12 @@ def check_attention(out, lse, ref, in_dtype):
     with 22 bits, 2^-22 S), one rounded product and difference (2^-23 of it
     each) and the exponential's 2^-22: 2^-19 (1 + S) holds all of it.  BF16
     outputs add the f16 rounding of the probabilities (2^-11) and their own
-    (2^-8 of the value), FP32 outputs 2^-22 and the FP32 sums (inside 2^-19)."""
-    want, want_lse, mag, big = ref
+    (2^-8 of the value), FP32 outputs 2^-22 and the FP32 sums (inside 2^-19).
+    f16 is also absolute below its normal range: a probability is stored to
+    2^-25, the largest being at least 2^7, so to 2^-32 of the row's largest."""
+    want, want_lse, mag, big, reach = ref
     score = 2.0 ** -19 * (1 + big)
-    tol = score[..., None] * mag
+    tol = score[..., None] * mag + 2.0 ** -32 * reach
     if out.dtype == torch.bfloat16:
         tol = tol + 2.0 ** -8 * want.abs() + 2.0 ** -11 * mag
     err = (out.double() - want).abs()

@@ -464,3 +464,111 @@ def test_streams_and_graphs(nv):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
     assert torch.equal(step(lens, False)[0], want)
+
+
+# ---- the tcgen05 kernel by name ----------------------------------------------------
+
+def run_tile(nv, seqs, counts, hq, hkv, dim, page, **more):
+    return run_attention(nv, seqs, counts, hq, hkv, dim, page, kernel=nv.KERNEL_KV_TILE, **more)
+
+
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("n", [1, 16, 100, 128, 129, 300])
+def test_tile_one_request(nv, dim, n):
+    run_tile(nv, [n], [1], 4, 1, dim, 16, seed=n)
+    run_tile(nv, [n], [n], 4, 1, dim, 16, seed=n)
+
+
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16), (128, 256)])
+@pytest.mark.parametrize("counts", [[2, 1, 0, 5], [16, 9], [64, 65, 1], [130, 0, 33], [300], [700, 3, 1, 90]])
+@pytest.mark.parametrize("past", [0, 1, 95, 1000])
+def test_tile_several_tokens(nv, dim, page, counts, past):
+    run_tile(nv, [c + past if c else 0 for c in counts], counts, 8, 2, dim, page, seed=past)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (10, 2), (7, 1), (16, 1), (40, 1), (64, 1), (32, 32)])
+def test_tile_head_groups(nv, hq, hkv):
+    run_tile(nv, [77, 300, 41], [5, 70, 41], hq, hkv, 128, 32, seed=hq)
+
+
+@pytest.mark.parametrize("window", [1, 2, 100, 127, 128, 129, 5000])
+def test_tile_window(nv, window):
+    run_tile(nv, [400, 90, 7, 1000], [37, 90, 7, 400], 8, 2, 128, 16, window=window)
+    run_tile(nv, [1500], [1], 8, 2, 64, 16, window=window)
+
+
+def test_tile_empty_and_early_rows(nv):
+    run_tile(nv, [0, 3, 0, 20], [1, 8, 4, 200], 8, 2, 128, 16)
+    run_tile(nv, [0, 0], [1, 1], 8, 2, 64, 16)
+
+
+def test_tile_scale(nv):
+    for scale in (0.3, -0.1, 0.0):
+        run_tile(nv, [260, 500], [20, 3], 8, 2, 128, 16, scale=scale)
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [300, 1], [900, 40]])
+def test_tile_workspace_and_repeats(nv, counts):
+    """Items cut between many SMs; the same bits each time; no workspace: no cuts."""
+    seqs = [9000, 3000]
+    cache, q, table, out, lse = run_tile(nv, seqs, counts, 8, 2, 128, 64)
+    for _ in range(3):
+        o2, l2 = nv.kv_attention(cache, q, table, ints(seqs), starts(counts), return_lse=True,
+                                 kernel=nv.KERNEL_KV_TILE)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+        run_attention(nv, [3000, 5], [1, 1], 8, 2, 128, 64)
+    run_tile(nv, seqs, counts, 8, 2, 128, 64, workspace=False)
+
+
+def test_tile_nonfinite_query_stays_in_its_row(nv):
+    cache, table, gen = filled(nv, [140, 290], 2, 64, 16)
+    for bad in (math.nan, math.inf):
+        q = torch.randn((103, 8, 64), generator=gen, device="cuda")
+        clean = q.to(BF16)
+        q[50, 3, 7] = bad
+        out, lse = nv.kv_attention(cache, q.to(BF16), table, ints([140, 290]), starts([100, 3]),
+                                   return_lse=True, kernel=nv.KERNEL_KV_TILE)
+        ref = attention(cache, clean, table, [140, 290], [100, 3])
+        keep = torch.ones((103, 8), dtype=torch.bool, device="cuda")
+        keep[50, 3] = False
+        assert not torch.isfinite(out[50, 3]).any()
+        check_attention(out[keep][None], lse[keep][None], [x[keep][None] for x in ref], BF16)
+
+
+def test_tile_zero_tensor_scale_and_bad_pages(nv):
+    cache, table, gen = filled(nv, [200, 40], 2, 128, 16)
+    q = torch.randn((60, 8, 128), generator=gen, device="cuda").to(BF16)
+    args = (ints([200, 40]), starts([40, 20]))
+    good = nv.kv_attention(cache, q, table, *args, kernel=nv.KERNEL_KV_TILE)
+    broken = table.clone()
+    broken[0, 2] = cache.num_pages
+    nv.device_status(clear=True)
+    out = nv.kv_attention(cache, q, broken, *args, kernel=nv.KERNEL_KV_TILE)
+    assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+    assert torch.equal(out[40:], good[40:])
+    cache.k_g.zero_()
+    out, lse = nv.kv_attention(cache, q, table, *args, return_lse=True, kernel=nv.KERNEL_KV_TILE)
+    check_attention(out, lse, attention(cache, q, table, [200, 40], [40, 20]), BF16)
+
+
+def test_tile_wants_bf16(nv):
+    cache, table, gen = filled(nv, [20], 1, 64, 16)
+    q = torch.randn((2, 4, 64), generator=gen, device="cuda")
+    for x, dtype in ((q, FP32), (q.to(BF16), FP32), (q, BF16)):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.kv_attention(cache, x, table, ints([20]), out_dtype=dtype, kernel=nv.KERNEL_KV_TILE)
+
+
+def test_growing_scores_in_tiles(nv):
+    """Scores that rise along the keys: outputs are rescaled in tensor memory again and again."""
+    cache, table, gen = filled(nv, [900], 1, 64, 16)
+    base = torch.randn((64,), generator=gen, device="cuda")
+    k = torch.arange(900, device="cuda")[:, None, None] * (base / 100)
+    v = torch.randn((900, 1, 64), generator=gen, device="cuda")
+    cache.k_g.copy_(nv.global_scale(k.contiguous()))
+    slots = table[0, :57].long().repeat_interleave(16)[:900] * 16 + torch.arange(900, device="cuda") % 16
+    nv.kv_append(cache, k.contiguous(), v, slots)
+    q = (base * 10 + torch.randn((300, 4, 64), generator=gen, device="cuda")).to(BF16)
+    for kernel in (nv.KERNEL_KV_ROWS, nv.KERNEL_KV_TILE):
+        out, lse = nv.kv_attention(cache, q, table, ints([900]), return_lse=True, kernel=kernel)
+        check_attention(out, lse, attention(cache, q, table, [900], [300]), BF16)
