@@ -79,6 +79,7 @@ struct KvAttnArgs {
     int32_t tokens;
     int32_t max_q;
     int32_t group;  // query heads per kv head
+    uint32_t group_magic;  // floor(2^32 / group) + 1
     float scale_log2;
     int32_t window;  // 0: none
     void* out;

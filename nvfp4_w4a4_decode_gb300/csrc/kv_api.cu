@@ -197,6 +197,7 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     a.tokens = (int32_t)r.tokens;
     a.max_q = (int32_t)(r.max_q < r.tokens ? r.max_q : r.tokens);
     a.group = (int32_t)(r.num_q_heads / a.c.heads);
+    a.group_magic = (uint32_t)(((uint64_t)1 << 32) / (uint64_t)a.group + 1);
     a.scale_log2 = r.scale * 1.4426950408889634f;
     // a window past every length is none
     a.window = r.window >= kMaxTokens ? 0 : (int32_t)r.window;

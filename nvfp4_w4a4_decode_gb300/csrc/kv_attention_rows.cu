@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         const int row = x.row0 + c;
         if (c < R && row < x.row1 && 4 * lane < D) {
-            const int tok = row / a.group;
+            const int tok = kv_token(a, row);
             const int64_t at = (x.q.base + tok) * a.q_stride +
                                (int64_t)(x.h * a.group + row - tok * a.group) * D + 4 * lane;
             if (a.q_bf16) {
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             if (lane == 0) {
                 const int row = it.row0 + c;
                 sm_f[c] = qk * down;
-                sm_pos[c] = row < it.row1 ? it.q.seq - it.q.nq + row / a.group : -1;
+                sm_pos[c] = row < it.row1 ? it.q.seq - it.q.nq + kv_token(a, row) : -1;
             }
         }
         compute_sync();
@@ -345,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                     acc[nt][i][e] = 0.f;
         }
         // positions every row of the tile sees: keys in [all_lo, all_hi]
-        const int32_t p0 = it.q.seq - it.q.nq + it.row0 / a.group;
-        const int32_t p1 = it.q.seq - it.q.nq + (it.row1 - 1) / a.group;
+        const int32_t p0 = it.q.seq - it.q.nq + kv_token(a, it.row0);
+        const int32_t p1 = it.q.seq - it.q.nq + kv_token(a, it.row1 - 1);
         const int32_t all_hi = p0, all_lo = a.window > 0 ? p1 - a.window + 1 : 0;
 
         for (int i = (warp + kWarps - taken * kSub % kWarps) % kWarps; i < units; i += kWarps) {
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             if (row >= it.row1)
                 return;
             const float inv = ltot == 0.f ? 0.f : vg / ltot;
-            const int tok = row / a.group;
+            const int tok = kv_token(a, row);
             const int64_t at = (it.q.base + tok) * a.out_stride +
                                (int64_t)(it.h * a.group + row - tok * a.group) * D +
                                (D / 8) * (fl >> 2) + 2 * fi;
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             const int row = it.row0 + col;
             if (a.lse == nullptr || row >= it.row1)
                 return;
-            const int tok = row / a.group;
+            const int tok = kv_token(a, row);
             a.lse[(int64_t)(it.q.base + tok) * (a.c.heads * a.group) + it.h * a.group + row -
                   tok * a.group] =
                 ltot == 0.f ? -INFINITY : 0.6931471805599453f * (mtot + log2f(ltot));

@@ -8,11 +8,15 @@
 // second product as f16 (scaled by 2^7), row sums are FP32.
 //
 // One CTA an SM, 256 query rows (token, head of the group) of one kv head as two
-// 128-row tiles, 128 keys at a time, warps in four groups:
+// 128-row tiles, 128 keys at a time:
 //   warps 0..3, 4..7   softmax of tile 0, 1, a thread a row: the queries into
 //                      shared memory, scores out of tensor memory, probabilities
-//                      back into it over the scores, at the end the output
-//   warps 8..11        decode the cache, a thread a token: codes and scales of
+//                      back into it over the scores, at the end the output.  The
+//                      exponentials of a block are taken against the reference at
+//                      hand, with the block's maximum as a by-product; only where
+//                      that passes the reference by 2^8 is it raised, the output
+//                      rescaled and the block done again
+//   warps 8..11        decode the cache, 32 tokens each: codes and scales of
 //                      the next block of keys are loaded while this block's are
 //                      converted to f16 and written as 128-byte-swizzled tiles
 //   warp 12            one thread issues the MMAs: S = Q K^T (both operands in
@@ -43,13 +47,11 @@ constexpr int kRowsTile = 128;             // query rows of an MMA tile
 constexpr int kRows = 2 * kRowsTile;       // of an item
 constexpr int kKeys = 128;                 // keys of a block
 constexpr int kItemCost = 2;               // blocks that an item's start and end cost
-constexpr int kThreads = 512;
+constexpr int kDecodeWarp = 8, kMmaWarp = 12;
+constexpr int kThreads = 416;
 constexpr float kRaise = 8.0f;             // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;              // p = 2^(s - m + kLift)
 constexpr uint32_t kColS = 0, kColO = 256;  // scores and outputs, 128 columns a tile
-// probabilities lie over the second half of the scores: that half is in
-// registers when they are written, the first is read once more
-constexpr uint32_t kColP = 64;
 
 using Work = KvWork<kRows, kKeys, kItemCost>;
 
@@ -80,24 +82,30 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major)
            ((uint32_t)(kRowsTile >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc)
+// The MMA warp runs its loop with all lanes, so that descriptors stay in uniform
+// registers (from a branch of one lane each MMA took 80 cycles to issue, more
+// than it takes to run); `one` is set in the lane that issues.
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       bool acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc), "r"(one)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc)
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       bool acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc), "r"(one)
                  : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar)
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+                     "r"(bar), "r"(one)
                  : "memory");
 }
 __device__ __forceinline__ void fence_after()
@@ -109,7 +117,7 @@ __device__ __forceinline__ void fence_before()
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 
-// 32 columns of this warp's 32 rows, a thread a row (call tmem_wait_ld before use).
+// 32 columns of this warp's 32 rows, a thread a row (tmem_wait_ld before use).
 __device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* v)
 {
     asm volatile(
@@ -122,44 +130,112 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* v)
           "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(t));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(t));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+        "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+        "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(t),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+        "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* v)
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
         "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+        "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld()
+// The loads are complete; the values are tied to the wait so that no use of
+// theirs can be scheduled before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* v)
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 64 columns of scores, those outside [first, last] as -inf.
-__device__ __forceinline__ void load_scores(uint32_t t, uint32_t (&s)[64], bool edge, int32_t first,
-                                            int32_t last)
+// Packed pairs of FP32 operations.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
 {
-    tmem_ld32(t, s);
-    tmem_ld32(t + 32, s + 32);
-    tmem_wait_ld();
-    if (edge) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-            if (i > last || i < first)
-                s[i] = 0xFF800000u;  // -inf
-    }
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(x), "l"(y), "l"(z));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+    return v;
+}
+
+// One arrival for the warp.
+__device__ __forceinline__ void warp_arrive(uint32_t bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+}
+
+// Barrier of a tile's softmax threads.
+__device__ __forceinline__ void tile_sync(int st)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + st), "n"(kRowsTile) : "memory");
+}
+
+// Byte of 16-byte piece `piece` (8 elements) of row r in a swizzled tile.
+__device__ __forceinline__ int piece_at(int r, int piece)
+{
+    return (piece >> 3) * (kKeys * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
 }
 
 struct Barriers {
-    uint64_t qfull[2];                // a tile's queries are in shared memory
+    uint64_t qfull[2];                // a tile's queries are in shared memory (an arrival a warp, here and below)
     uint64_t kfull[2], kempty[2];     // decoded K blocks
     uint64_t vfull[2], vempty[2];
     uint64_t sfull[2];                // a tile's scores are in tensor memory
@@ -169,65 +245,66 @@ struct Barriers {
 };
 
 // ---- warps 8..11: the cache to f16 ----------------------------------------------------
+// 32 tokens of a block a warp: a lane takes 32 elements (16 bytes of codes, two
+// scales) of every RPI-th row, neighbouring lanes neighbouring bytes.
 template <int D>
-struct RawToken {
-    uint4 k[D / 32], v[D / 32];
-    uint32_t ks[D / 64], vs[D / 64];
+struct Raw {
+    static constexpr int kLanes = D / 32;        // lanes a row
+    static constexpr int kRpi = 32 / kLanes;     // rows at a time
+    static constexpr int kIters = 32 / kRpi;
+    uint4 c[kIters];
+    uint32_t s[kIters];
 };
 
+// The K or V rows of a warp's 32 tokens; page[i] holds the i-th 16 of them (-1:
+// nothing there, the rows become zeros).
 template <int D>
-__device__ __forceinline__ void load_token(RawToken<D>& x, const KvAttnArgs& a, int32_t page,
-                                           int32_t tok, int h)
+__device__ __forceinline__ void load_rows(Raw<D>& x, const KvAttnArgs& a, const int32_t (&page)[2],
+                                          int32_t tok0, int32_t seq, int h, bool is_v)
 {
-    if (page < 0) {
+    using X = Raw<D>;
+    const int P = a.c.page_shift, lane = threadIdx.x & 31, t = lane % X::kLanes;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            x.k[i] = x.v[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-            x.ks[i] = x.vs[i] = 0u;
-        return;
-    }
-    const int P = a.c.page_shift;
-    const int32_t off = tok & ((1 << P) - 1);
-    const uint8_t* p = a.c.pool + page * a.c.page_stride + h * kv_head_bytes(P, D);
-    const uint4* k = reinterpret_cast<const uint4*>(p + off * (D / 2));
-    const uint4* v = reinterpret_cast<const uint4*>(p + ((D / 2) << P) + off * (D / 2));
-    const uint32_t* ks = reinterpret_cast<const uint32_t*>(p + (D << P) + off * (D / 16));
-    const uint32_t* vs =
-        reinterpret_cast<const uint32_t*>(p + (D << P) + ((D / 16) << P) + off * (D / 16));
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        x.k[i] = __ldg(k + i);
-        x.v[i] = __ldg(v + i);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        x.ks[i] = __ldg(ks + i);
-        x.vs[i] = __ldg(vs + i);
+    for (int i = 0; i < X::kIters; ++i) {
+        const int row = i * X::kRpi + lane / X::kLanes;
+        const int32_t pg = row < 16 ? page[0] : page[1], tok = tok0 + row;
+        x.c[i] = make_uint4(0u, 0u, 0u, 0u);
+        x.s[i] = 0u;
+        if (pg >= 0 && tok < seq) {
+            const int32_t off = tok & ((1 << P) - 1);
+            const uint8_t* p = a.c.pool + pg * a.c.page_stride + h * kv_head_bytes(P, D);
+            x.c[i] = __ldg(reinterpret_cast<const uint4*>(p + (is_v ? (D / 2) << P : 0) +
+                                                          off * (D / 2) + 16 * t));
+            x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(
+                p + (D << P) + (is_v ? (D / 16) << P : 0) + off * (D / 16) + 2 * t));
+        }
     }
 }
 
-// A token's row as f16 into a swizzled tile (row r of 128-byte rows, a half a
-// 64 elements): eight 16-byte pieces of a row, piece c at c XOR (r mod 8).
+// The same rows as f16 into a swizzled tile (rows row0 ..).  Lanes of the second
+// half of a row write their pieces in another order, so that a store's lanes fall
+// on different banks.
 template <int D>
-__device__ __forceinline__ void store_token(uint8_t* tile, int r, const uint4 (&c)[D / 32],
-                                            const uint32_t (&s)[D / 64])
+__device__ __forceinline__ void store_rows(uint8_t* tile, int row0, const Raw<D>& x)
 {
-    uint8_t* row = tile + r * 128;
+    using X = Raw<D>;
+    const int lane = threadIdx.x & 31, t = lane % X::kLanes;
+    const bool turn = t >= 2;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {  // 32 elements: two blocks, four pieces
-        const uint32_t two = e4m3x2_to_f16x2_bits(s[i / 2] >> (16 * (i % 2)));
-        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+    for (int i = 0; i < X::kIters; ++i) {
+        const int r = row0 + i * X::kRpi + lane / X::kLanes;
+        const uint32_t two = e4m3x2_to_f16x2_bits(x.s[i]);
+        const uint32_t lo = f16x2_dup_lo(two), hi = f16x2_dup_hi(two);
+        const uint32_t w[4] = {turn ? x.c[i].z : x.c[i].x, turn ? x.c[i].w : x.c[i].y,
+                               turn ? x.c[i].x : x.c[i].z, turn ? x.c[i].y : x.c[i].w};
+        const uint32_t sc[2] = {turn ? hi : lo, turn ? lo : hi};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t sc = j < 2 ? f16x2_dup_lo(two) : f16x2_dup_hi(two);
             uint32_t f[4];
             e2m1x8_to_f16(w[j], f);
-            const int piece = (i * 4 + j) & 7, half = (i * 4 + j) >> 3;
-            *reinterpret_cast<uint4*>(row + half * (kKeys * 128) + ((piece ^ (r & 7)) << 4)) =
-                make_uint4(f16x2_mul(f[0], sc), f16x2_mul(f[1], sc), f16x2_mul(f[2], sc),
-                           f16x2_mul(f[3], sc));
+            *reinterpret_cast<uint4*>(tile + piece_at(r, 4 * t + (turn ? j ^ 2 : j))) =
+                make_uint4(f16x2_mul(f[0], sc[j / 2]), f16x2_mul(f[1], sc[j / 2]),
+                           f16x2_mul(f[2], sc[j / 2]), f16x2_mul(f[3], sc[j / 2]));
         }
     }
 }
@@ -249,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars.qfull[i]), kRowsTile);
-            mbar_init(smem_u32(&bars.kfull[i]), kKeys);
+            mbar_init(smem_u32(&bars.qfull[i]), kRowsTile / 32);
+            mbar_init(smem_u32(&bars.kfull[i]), kKeys / 32);
             mbar_init(smem_u32(&bars.kempty[i]), 1);
-            mbar_init(smem_u32(&bars.vfull[i]), kKeys);
+            mbar_init(smem_u32(&bars.vfull[i]), kKeys / 32);
             mbar_init(smem_u32(&bars.vempty[i]), 1);
             mbar_init(smem_u32(&bars.sfull[i]), 1);
-            mbar_init(smem_u32(&bars.pfull[i]), kRowsTile);
+            mbar_init(smem_u32(&bars.pfull[i]), kRowsTile / 32);
             mbar_init(smem_u32(&bars.ofull[i]), 1);
         }
         mbar_init(smem_u32(&bars.drain), 1);
@@ -269,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     bool more = Work::start<kThreads>(a, work_sm, kItemCost + 1, sh, it);
     if (sh.lo >= sh.hi)
         return;
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_base_s)),
                      "r"(512u));
@@ -280,14 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     fence_after();
     const uint32_t tmem = tmem_base_s;
 
-    if (warp < 8) {
+    if (warp < kDecodeWarp) {
         // ---- softmax: thread = row of tile st -------------------------------------------------
-        const int st = warp >> 2, r = tid & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
+        const int st = warp >> 2, r = tid & 127, wrow = r & ~31;  // the warp's first row
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // its 32 lanes
         const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
         const uint32_t qfull = smem_u32(&bars.qfull[st]), sfull = smem_u32(&bars.sfull[st]),
                        pfull = smem_u32(&bars.pfull[st]), ofull = smem_u32(&bars.ofull[st]);
-        uint8_t* q_row = smem + st * C::kTile + r * 128;
+        uint8_t* tile = smem + st * C::kTile;  // the queries; at the end the outputs
+        constexpr int kRowLanes = D / 4, kRowsAtOnce = 32 / kRowLanes;  // 8 bytes a lane
+        const int my_part = lane % kRowLanes, my_row = lane / kRowLanes;
         // a negative factor goes into the queries' signs, so that larger scores are
         // larger throughout
         const float vg = a.c.v_g[0], signed_qk = a.scale_log2 * a.c.k_g[0], qk = fabsf(signed_qk);
@@ -295,80 +374,161 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         uint32_t blocks = 0, items = 0;  // this tile's so far
         for (; more; more = Work::next(a, sh, it)) {
             __syncwarp();
-            const int row = it.row0 + st * kRowsTile + r;
-            if (it.row0 + st * kRowsTile >= it.row1)
+            const int tile0 = it.row0 + st * kRowsTile;
+            if (tile0 >= it.row1)
                 continue;  // the item has no second tile
+            const int row = tile0 + r;
             const bool live = row < it.row1;
-            const int tok = live ? row / a.group : 0;
+            // this thread's row: token and head; the others' by shuffle
+            const int tok = live ? kv_token(a, row) : 0;
             const int head = it.h * a.group + (live ? row - tok * a.group : 0);
+            auto row_at = [&](int64_t stride) {
+                return (it.q.base + tok) * stride + (int64_t)head * D;
+            };
+            const int rows_here = min(it.row1 - tile0 - wrow, 32);  // of the warp's 32
 
-            // the row's queries, scaled by a power of two, as f16
+            // the warp's 32 rows of queries: as they are into the tile, a row's lanes
+            // reading neighbouring bytes; then a thread a row scales its own by a power of
+            // two and leaves it as f16
+            {
+                const int64_t at = row_at(a.q_stride);
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += 8 * kRowsAtOnce) {
+                    uint2 w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int x = i0 + i * kRowsAtOnce + my_row;
+                        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, x);
+                        w[i] = x < rows_here
+                                   ? __ldg(reinterpret_cast<const uint2*>(
+                                               static_cast<const __nv_bfloat16*>(a.q) + from) +
+                                           my_part)
+                                   : make_uint2(0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint2*>(
+                            tile + piece_at(wrow + i0 + i * kRowsAtOnce + my_row, my_part >> 1) +
+                            8 * (my_part & 1)) = w[i];
+                }
+            }
+            __syncwarp();
             float f;
             {
-                uint2 w[D / 4];
-                const uint2* src = reinterpret_cast<const uint2*>(
-                    static_cast<const __nv_bfloat16*>(a.q) +
-                    (int64_t)(it.q.base + tok) * a.q_stride + (int64_t)head * D);
                 uint32_t top = 0;  // BF16 magnitudes order like their bits
 #pragma unroll
-                for (int i = 0; i < D / 4; ++i) {
-                    w[i] = live ? __ldg(src + i) : make_uint2(0u, 0u);
-                    top = __vmaxu2(top, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu));
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(tile + piece_at(r, c));
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                                 __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
                 }
                 top = max(top & 0xFFFFu, top >> 16);
-                if (top > 0x7F80u)
-                    top = 0x7F80u;  // NaN: any finite factor keeps it
+                top = min(top, 0x7F80u);  // NaN: any finite factor keeps it
                 const int e = min(max(14 - ((int)(top >> 7) - 127), -100), 100);
                 const float up = top ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
                 f = qk * (top ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f);
-                // a factor of 0 (a zero scale) would make -inf of a masked score NaN
-                f = f == 0.f ? 1e-38f : f;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
+                    uint4* place = reinterpret_cast<uint4*>(tile + piece_at(r, c));
+                    const uint4 x = *place;
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t x = j & 1 ? w[2 * c + j / 2].y : w[2 * c + j / 2].x;
-                        o[j] = pack_f16(__uint_as_float(x << 16) * up,
-                                        __uint_as_float(x & 0xFFFF0000u) * up) ^
-                               flip;
-                    }
-                    *reinterpret_cast<uint4*>(q_row + (c >> 3) * (kKeys * 128) +
-                                              (((c & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = pack_f16(__uint_as_float(w[j] << 16) * up,
+                                        __uint_as_float(w[j] & 0xFFFF0000u) * up) ^ flip;
+                    *place = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
+            // a factor of 0 (a zero scale) would make -inf of a masked score NaN
+            f = f == 0.f ? 1e-38f : f;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             fence_before();  // the last item's reads of the output come before this item's products
-            mbar_arrive(qfull);
+            warp_arrive(qfull);
 
             const int32_t pos = live ? it.q.seq - it.q.nq + tok : -1;
             float m = -INFINITY, l = 0.f;  // reference minus kLift, and the sum
+            const uint64_t f2 = pair(f, f);
             for (int32_t u = it.u0; u < it.u1; ++u, ++blocks) {
-                mbar_wait(sfull, blocks & 1, abort_flag, a.status);
-                fence_after();
                 // columns [first, last] are seen
-                const int32_t k0 = (it.first + u) * kKeys;
-                const int32_t last = pos - k0;
+                const int32_t last = pos - (it.first + u) * kKeys;
                 const int32_t first = a.window > 0 ? last - a.window + 1 : 0;
                 const bool edge = last < kKeys - 1 || first > 0;
-                // scores 64 at a time: both halves for the maximum, then the second
-                // half (still in registers) and the first again for the exponentials
-                uint32_t s[64];
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                mbar_wait(sfull, blocks & 1, abort_flag, a.status);
+                fence_after();
+                // bit i: column c + i of a chunk of 16 is seen
+                auto seen16 = [&](int c) {
+                    const int lo = min(max(first - c, 0), 16), hi = min(max(last - c + 1, 0), 16);
+                    return (0xFFFFu >> (16 - hi)) & (0xFFFFu << lo);
+                };
+                auto load16 = [&](int c, uint32_t* s) { tmem_ld16(tS + c, s); };
+                auto hide = [&](int c, uint32_t* s) {
+                    const uint32_t seen = seen16(c);
 #pragma unroll
-                for (int h = 0; h < kKeys; h += 64) {
-                    load_scores(tS + h, s, edge, first - h, last - h);
+                    for (int i = 0; i < 16; ++i)
+                        s[i] = seen >> i & 1 ? s[i] : 0xFF800000u;  // -inf
+                };
+                if (u == it.u0) {  // the first reference: the block's largest score
+                    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8)
+                    for (int c = 0; c < kKeys; c += 16) {
+                        uint32_t s[16];
+                        load16(c, s);
+                        tmem_wait_ld16(s);
+                        if (edge)
+                            hide(c, s);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            top[j] = fmaxf(top[j], fmaxf(__uint_as_float(s[i + 2 * j]),
-                                                         __uint_as_float(s[i + 2 * j + 1])));
+                        for (int i = 0; i < 16; i += 4)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                top[j] = fmaxf(top[j], fmaxf(__uint_as_float(s[i + 2 * j]),
+                                                             __uint_as_float(s[i + 2 * j + 1])));
+                    }
+                    m = fmaxf(top[0], top[1]);
+                    m = m == -INFINITY ? m : m * f - kLift;
                 }
-                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
-                if (__any_sync(0xFFFFFFFFu, best > m + (kLift + kRaise))) {
-                    const float now = fmaxf(m, best - kLift);
+                uint32_t p16[kKeys / 2];
+                float sum;
+                // usually one pass; a second when the reference had to be raised
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
+                    // no key seen yet: every score is -inf, against any finite reference
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const uint64_t neg = pair(-ref, -ref);
+                    float top[2] = {-INFINITY, -INFINITY};
+                    uint64_t sums[2] = {0ull, 0ull};
+                    uint32_t s[2][16];  // a chunk, and the next on its way
+                    load16(0, s[0]);
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 16) {
+                        uint32_t* x16 = s[(c >> 4) & 1];
+                        tmem_wait_ld16(x16);
+                        if (c + 16 < kKeys)
+                            load16(c + 16, s[((c >> 4) + 1) & 1]);
+                        if (edge)
+                            hide(c, x16);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint64_t x = fma2(
+                                pair(__uint_as_float(x16[i]), __uint_as_float(x16[i + 1])), f2, neg);
+                            float p0, p1;
+                            unpair(x, p0, p1);
+                            top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(p0, p1));
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], pair(p0, p1));
+                            p16[(c + i) / 2] = pack_f16(p0, p1);
+                        }
+                    }
+                    float x0, x1;
+                    unpair(add2(sums[0], sums[1]), x0, x1);
+                    sum = x0 + x1;
+                    const float best = fmaxf(top[0], top[1]);  // against ref
+                    // (a row that has seen no key takes its first reference too)
+                    const bool raise = best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
+                    if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
+                        break;
+                    const float now = fmaxf(m, best + ref - kLift);
                     const float by = m == now ? 1.f : ex2(m - now);
                     m = now;
                     l *= by;
@@ -376,42 +536,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     // after them, and their commit covers both
                     if (u > it.u0) {
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + i, o);
-                            tmem_wait_ld();
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + i, o);
+                            tmem_wait_ld16(o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < 16; ++j)
                                 o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-                            tmem_st32(tO + i, o);
+                            tmem_st16(tO + i, o);
                         }
                     }
                 }
-                // no key seen yet: every score is -inf, against any finite reference
-                const float ref = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int h = kKeys - 64; h >= 0; h -= 64) {
-                    if (h == 0)
-                        load_scores(tS, s, edge, first, last);
-                    uint32_t p16[32];
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        float p[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            p[j] = ex2(fmaf(__uint_as_float(s[i + j]), f, -ref));
-                            sum[j] += p[j];
-                        }
-                        p16[i / 2] = pack_f16(p[0], p[1]);
-                        p16[i / 2 + 1] = pack_f16(p[2], p[3]);
-                    }
-                    tmem_st32(tS + kColP + h / 2, p16);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += sum;
+                tmem_st32(tS, p16);
+                tmem_st32(tS + 32, p16 + 32);
                 tmem_wait_st();
                 fence_before();
-                mbar_arrive(pfull);
+                warp_arrive(pfull);
             }
 
             // ---- the item's output ----------------------------------------------------------
@@ -419,44 +560,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             ++items;
             fence_after();
             const bool whole = it.u0 == 0 && it.u1 == it.n;
-            const int64_t out_at = (int64_t)(it.q.base + tok) * a.out_stride + (int64_t)head * D;
-            const int64_t lse_at = (int64_t)(it.q.base + tok) * (a.c.heads * a.group) + head;
-            auto write32 = [&](int i, const float* o, float scale) {
-                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_at + i);
+            auto write_lse = [&](float mt, float lt) {
+                if (a.lse != nullptr && live)
+                    a.lse[(int64_t)(it.q.base + tok) * (a.c.heads * a.group) + head] =
+                        lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
+            };
+            // 32 outputs of the row into the tile, which the products are done with
+            auto stage = [&](int i, const float* o, float scale) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(o[j] * scale, o[j + 1] * scale);
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(o[j + 2] * scale, o[j + 3] * scale);
-                    dst[j / 4] = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
-                                            *reinterpret_cast<const uint32_t*>(&y));
+                for (int j = 0; j < 32; j += 8) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(o[j + 2 * k] * scale,
+                                                                       o[j + 2 * k + 1] * scale);
+                        v[k] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+                    *reinterpret_cast<uint4*>(tile + piece_at(r, (i + j) / 8)) =
+                        make_uint4(v[0], v[1], v[2], v[3]);
                 }
             };
-            auto write_lse = [&](float mt, float lt) {
-                if (a.lse != nullptr)
-                    a.lse[lse_at] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
+            // the warp's staged rows to the output, a row's lanes neighbouring bytes
+            auto write_rows = [&]() {
+                const int64_t at = row_at(a.out_stride);
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < 32; i += kRowsAtOnce) {
+                    const int x = i + my_row;
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, at, x);
+                    if (x < rows_here)
+                        *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) + my_part) =
+                            *reinterpret_cast<const uint2*>(tile + piece_at(wrow + x, my_part >> 1) +
+                                                            8 * (my_part & 1));
+                }
             };
+            // a partial tile: [D] columns of 128 rows, then references, then sums
             float* part = a.part + (4 * blockIdx.x + 2 * (it.u0 == 0 ? 1 : 0) + st) * C::kPart + r;
             const float scale = l == 0.f ? 0.f : vg / l;
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + i, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
                 float x[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     x[j] = __uint_as_float(o[j]);
-                if (!whole) {
+                if (whole) {
+                    stage(i, x, scale);
+                } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         part[(i + j) * kRowsTile] = x[j];
-                } else if (live) {
-                    write32(i, x, scale);
                 }
             }
             if (whole) {
-                if (live)
-                    write_lse(m, l);
+                write_rows();
+                write_lse(m, l);
                 continue;
             }
             part[D * kRowsTile] = m;
@@ -464,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             // the last CTA of the item to arrive joins the parts in CTA order
             const int ca = Work::first_cta(sh, it), cb = Work::last_cta(sh, it);
             __threadfence();
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + st) : "memory");
+            tile_sync(st);
             if (r == 0) {
                 const unsigned seen = atomicAdd(a.count + 2 * ca + st, 1u);
                 last_s[st] = seen == (unsigned)(cb - ca);
@@ -472,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     a.count[2 * ca + st] = 0u;
                 __threadfence();
             }
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + st) : "memory");
-            if (!last_s[st] || !live)
+            tile_sync(st);
+            if (!last_s[st])
                 continue;
             auto part_of = [&](int c) {
                 return a.part + (4 * c + 2 * (c == ca ? 1 : 0) + st) * C::kPart + r;
@@ -500,150 +660,160 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     for (int j = 0; j < 32; ++j)
                         x[j] = fmaf(__ldcg(pc + (i + j) * kRowsTile), by, x[j]);
                 }
-                write32(i, x, all);
+                stage(i, x, all);
             }
+            write_rows();
             write_lse(mt, lt);
         }
-    } else if (warp < 12) {
-        // ---- decode: thread = token of a block -------------------------------------------------
-        const int r = tid & 127;
+    } else if (warp < kMmaWarp) {
+        // ---- decode: 32 tokens of a block a warp -------------------------------------------------
+        const int row0 = 32 * (warp - kDecodeWarp);
         bool bad = false;
-        auto page_of = [&](const KvItem& x, int32_t u) {
-            const int32_t tok = (x.first + u) * kKeys + r, b = tok >> a.c.page_shift;
-            if (tok >= x.q.seq || b >= a.max_blocks)
-                return -1;
-            const int32_t page = a.table[x.r * a.table_stride + b];
-            if (page >= 0 && page < a.c.num_pages)
-                return page;
-            bad = true;
-            return -1;
+        // a block's rows are loaded a block ahead, their pages (16 tokens each) two
+        Raw<D> k, v;
+        int32_t pages[2] = {-1, -1};
+        auto look_up = [&](const KvItem& y, int32_t u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int32_t tok = (y.first + u) * kKeys + row0 + 16 * i, b = tok >> a.c.page_shift;
+                int32_t page = -1;
+                if (tok < y.q.seq && b < a.max_blocks) {
+                    page = a.table[y.r * a.table_stride + b];
+                    if (page < 0 || page >= a.c.num_pages) {
+                        bad = true;
+                        page = -1;
+                    }
+                }
+                pages[i] = page;
+            }
         };
-        RawToken<D> x;
+        auto load = [&](const KvItem& y, int32_t u) {
+            const int32_t tok0 = (y.first + u) * kKeys + row0;
+            load_rows<D>(k, a, pages, tok0, y.q.seq, y.h, false);
+            load_rows<D>(v, a, pages, tok0, y.q.seq, y.h, true);
+        };
         int32_t u = 0;
-        KvItem nx = it;
-        int32_t npage = -1;
-        // the block after (it, u): its token is loaded a block ahead, its page two
-        auto advance = [&](KvItem& w, int32_t& v) {
-            if (v + 1 < w.u1) {
-                ++v;
+        auto advance = [&]() {  // to the block after u of `it`
+            if (u + 1 < it.u1) {
+                ++u;
                 return true;
             }
-            if (!Work::next(a, sh, w))
+            if (!Work::next(a, sh, it))
                 return false;
-            v = w.u0;
+            u = it.u0;
             return true;
         };
-        uint32_t n = 0;
         bool have_next = more;
-        int32_t nu = 0;
         if (more) {
             u = it.u0;
-            load_token<D>(x, a, page_of(it, u), (it.first + u) * kKeys + r, it.h);
-            nu = u;
-            have_next = advance(nx, nu);
-            npage = have_next ? page_of(nx, nu) : -1;
+            look_up(it, u);
+            load(it, u);
+            have_next = advance();
+            if (have_next)
+                look_up(it, u);
         }
-        while (more) {
+        for (uint32_t n = 0; more; ++n) {
             const uint32_t b = n & 1, turn = n >> 1;
             if (n >= 2)
                 mbar_wait(smem_u32(&bars.kempty[b]), (turn - 1) & 1, abort_flag, a.status);
-            store_token<D>(smem + (2 + b) * C::kTile, r, x.k, x.ks);
+            store_rows<D>(smem + (2 + b) * C::kTile, row0, k);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(smem_u32(&bars.kfull[b]));
+            warp_arrive(smem_u32(&bars.kfull[b]));
             if (n >= 2)
                 mbar_wait(smem_u32(&bars.vempty[b]), (turn - 1) & 1, abort_flag, a.status);
-            store_token<D>(smem + (4 + b) * C::kTile, r, x.v, x.vs);
+            store_rows<D>(smem + (4 + b) * C::kTile, row0, v);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(smem_u32(&bars.vfull[b]));
-            ++n;
+            warp_arrive(smem_u32(&bars.vfull[b]));
             more = have_next;
             if (more) {
-                load_token<D>(x, a, npage, (nx.first + nu) * kKeys + r, nx.h);
-                have_next = advance(nx, nu);
-                npage = have_next ? page_of(nx, nu) : -1;
+                load(it, u);
+                have_next = advance();
+                if (have_next)
+                    look_up(it, u);
             }
         }
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
     } else {
         // ---- warp 12: the MMAs --------------------------------------------------------------------
-        if (warp == 12 && lane == 0) {
-            constexpr uint32_t id_s = idesc(kKeys, false), id_o = idesc(D, true);
-            uint32_t n = 0, items = 0, items1 = 0, blocks1 = 0;  // blocks and items (tile 1: its own)
-            auto scores = [&](int st, uint32_t b) {
+        uint32_t one;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+        constexpr uint32_t id_s = idesc(kKeys, false), id_o = idesc(D, true);
+        const uint64_t q_desc = desc_k(sQ), k_desc = desc_k(sK), v_desc = desc_n(sV);
+        constexpr uint32_t kTileStep = C::kTile >> 4;  // of a descriptor's address
+        uint32_t n = 0, items = 0, items1 = 0, blocks1 = 0;  // blocks and items (tile 1: its own)
+        auto scores = [&](int st, uint32_t b) {
+            const uint64_t qd = q_desc + st * kTileStep, kd = k_desc + b * kTileStep;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
-                    mma_ss(tmem + kColS + st * 128, desc_k(sQ + st * C::kTile + at),
-                           desc_k(sK + b * C::kTile + at), id_s, k > 0);
-                }
-                commit(smem_u32(&bars.sfull[st]));
-            };
-            auto outputs = [&](int st, uint32_t b, bool acc) {
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                mma_ss(one, tmem + kColS + st * 128, qd + at, kd + at, id_s, k > 0);
+            }
+            commit(one, smem_u32(&bars.sfull[st]));
+        };
+        auto outputs = [&](int st, uint32_t b, bool acc) {
+            const uint64_t vd = v_desc + b * kTileStep;
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tmem + kColO + st * 128, tmem + kColS + kColP + st * 128 + k * 8,
-                           desc_n(sV + b * C::kTile + k * 2048), id_o, acc || k > 0);
-            };
-            bool ok = true;
-            for (; more && ok; more = Work::next(a, sh, it)) {
-                const int tiles = it.row1 - it.row0 > kRowsTile ? 2 : 1;
-                const int32_t count = it.u1 - it.u0;
-                for (int st = 0; st < tiles && ok; ++st)
-                    ok = mbar_wait(smem_u32(&bars.qfull[st]), (st ? items1 : items) & 1, abort_flag,
-                                   a.status);
-                ok = ok && mbar_wait(smem_u32(&bars.kfull[n & 1]), (n >> 1) & 1, abort_flag, a.status);
-                if (!ok)
+            for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts(one, tmem + kColO + st * 128, tmem + kColS + st * 128 + k * 8,
+                       vd + k * (2048 >> 4), id_o, acc || k > 0);
+        };
+        bool ok = true;
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar), parity & 1, abort_flag, a.status));
+            return ok;
+        };
+        for (; more && ok; more = Work::next(a, sh, it)) {
+            const int tiles = it.row1 - it.row0 > kRowsTile ? 2 : 1;
+            const int32_t count = it.u1 - it.u0;
+            if (!wait(bars.qfull[0], items) || (tiles == 2 && !wait(bars.qfull[1], items1)) ||
+                !wait(bars.kfull[n & 1], n >> 1))
+                break;
+            fence_after();
+            for (int st = 0; st < tiles; ++st)
+                scores(st, n & 1);
+            commit(one, smem_u32(&bars.kempty[n & 1]));
+            for (int32_t j = 0; j < count && ok; ++j, ++n) {
+                const uint32_t b = n & 1, nb = (n + 1) & 1;
+                if (!wait(bars.vfull[b], n >> 1))
                     break;
-                fence_after();
-                for (int st = 0; st < tiles; ++st)
-                    scores(st, n & 1);
-                commit(smem_u32(&bars.kempty[n & 1]));
-                for (int32_t j = 0; j < count && ok; ++j, ++n) {
-                    const uint32_t b = n & 1, nb = (n + 1) & 1;
-                    ok = mbar_wait(smem_u32(&bars.vfull[b]), (n >> 1) & 1, abort_flag, a.status);
-                    for (int st = 0; st < tiles && ok; ++st) {
-                        ok = mbar_wait(smem_u32(&bars.pfull[st]), (st ? blocks1 : n) & 1, abort_flag,
-                                       a.status);
-                        if (!ok)
+                for (int st = 0; st < tiles; ++st) {
+                    if (!wait(bars.pfull[st], st ? blocks1 : n))
+                        break;
+                    fence_after();
+                    outputs(st, b, j > 0);
+                    if (st == tiles - 1)
+                        commit(one, smem_u32(&bars.vempty[b]));
+                    if (j + 1 < count) {
+                        if (st == 0 && !wait(bars.kfull[nb], (n + 1) >> 1))
                             break;
                         fence_after();
-                        outputs(st, b, j > 0);
+                        scores(st, nb);
                         if (st == tiles - 1)
-                            commit(smem_u32(&bars.vempty[b]));
-                        if (j + 1 < count) {
-                            if (st == 0)
-                                ok = mbar_wait(smem_u32(&bars.kfull[nb]), ((n + 1) >> 1) & 1,
-                                               abort_flag, a.status);
-                            if (!ok)
-                                break;
-                            fence_after();
-                            scores(st, nb);
-                            if (st == tiles - 1)
-                                commit(smem_u32(&bars.kempty[nb]));
-                        } else {
-                            commit(smem_u32(&bars.ofull[st]));
-                        }
+                            commit(one, smem_u32(&bars.kempty[nb]));
+                    } else {
+                        commit(one, smem_u32(&bars.ofull[st]));
                     }
-                    if (tiles == 2)
-                        ++blocks1;
                 }
-                ++items;
                 if (tiles == 2)
-                    ++items1;
+                    ++blocks1;
             }
-            // what was issued must be complete before tensor memory is freed
-            commit(smem_u32(&bars.drain));
-            const long long t0 = clock64();
-            while (!mbar_test(smem_u32(&bars.drain), 0) && clock64() - t0 < kKvWaitBudget) {
-            }
+            ++items;
+            if (tiles == 2)
+                ++items1;
+        }
+        // what was issued must be complete before tensor memory is freed
+        commit(one, smem_u32(&bars.drain));
+        const long long t0 = clock64();
+        while (!mbar_test(smem_u32(&bars.drain), 0) && clock64() - t0 < kKvWaitBudget) {
         }
         __syncwarp();
     }
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 12)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 

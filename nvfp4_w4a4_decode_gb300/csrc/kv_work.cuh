@@ -119,6 +119,16 @@ __device__ __forceinline__ bool kv_too_long(const KvAttnArgs& a, int r)
     return (int64_t)a.seq_len[r] > (int64_t)a.max_blocks << a.c.page_shift;
 }
 
+// The token of a query row: row / group, by a multiplication (the group is a
+// launch's constant; a division took a tenth of an item's start).
+__device__ __forceinline__ int kv_token(const KvAttnArgs& a, int row)
+{
+    if (a.group == 1)
+        return row;
+    const uint32_t q = __umulhi((uint32_t)row, a.group_magic);  // one too large at most
+    return (int)(q - (q * (uint32_t)a.group > (uint32_t)row ? 1u : 0u));
+}
+
 struct KvItem {
     int r, h, tile;
     KvReq q;
@@ -141,7 +151,7 @@ struct KvWork {
     static __device__ __forceinline__ void tile_units(const KvAttnArgs& a, const KvReq& q, int row0,
                                                       int row1, int32_t& first, int32_t& n)
     {
-        const int32_t i0 = row0 / a.group, i1 = (row1 - 1) / a.group;
+        const int32_t i0 = kv_token(a, row0), i1 = kv_token(a, row1 - 1);
         const int32_t p0 = q.seq - q.nq;
         const int32_t hi = p0 + i1 + 1;  // keys [lo, hi)
         const int32_t lo = a.window > 0 ? max(0, p0 + i0 - a.window + 1) : 0;
