@@ -12,14 +12,14 @@
 //   warps 0..3, 4..7   softmax of tile 0, 1, a thread a row: the queries into
 //                      shared memory, scores out of tensor memory, probabilities
 //                      back into it over the scores, at the end the output.  The
-//                      exponentials of a block are taken against the reference at
-//                      hand, with the block's maximum as a by-product; only where
-//                      that passes the reference by 2^8 is it raised, the output
-//                      rescaled and the block done again
-//   warps 8..11        decode the cache, 32 tokens each: codes and scales of
+//                      exponentials of 32 scores are taken against the reference
+//                      at hand, with their maximum as a by-product; only where
+//                      that passes the reference by 2^8 is it raised, what was
+//                      accumulated rescaled and the 32 scores done again
+//   warps 8..15        decode the cache, 16 tokens each: codes and scales of
 //                      the next block of keys are loaded while this block's are
 //                      converted to f16 and written as 128-byte-swizzled tiles
-//   warp 12            one thread issues the MMAs: S = Q K^T (both operands in
+//   warp 16            one lane issues the MMAs: S = Q K^T (both operands in
 //                      shared memory) and O += P V (P in tensor memory, V in
 //                      shared memory with the head dim contiguous)
 // The two tiles alternate: while one's scores are in the softmax the other's
@@ -47,8 +47,9 @@ constexpr int kRowsTile = 128;             // query rows of an MMA tile
 constexpr int kRows = 2 * kRowsTile;       // of an item
 constexpr int kKeys = 128;                 // keys of a block
 constexpr int kItemCost = 2;               // blocks that an item's start and end cost
-constexpr int kDecodeWarp = 8, kMmaWarp = 12;
-constexpr int kThreads = 416;
+constexpr int kDecodeWarp = 8, kMmaWarp = 16;
+constexpr int kDecodeRows = 16;            // tokens of a block a decoding warp
+constexpr int kThreads = 544;
 constexpr float kRaise = 8.0f;             // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;              // p = 2^(s - m + kLift)
 constexpr uint32_t kColS = 0, kColO = 256;  // scores and outputs, 128 columns a tile
@@ -159,18 +160,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v)
         "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
-        "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
 // The loads are complete; the values are tied to the wait so that no use of
 // theirs can be scheduled before it.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t* v)
@@ -235,7 +224,8 @@ __device__ __forceinline__ int piece_at(int r, int piece)
 }
 
 struct Barriers {
-    uint64_t qfull[2];                // a tile's queries are in shared memory (an arrival a warp, here and below)
+    uint64_t qfull[2];                // a tile's queries are in shared memory (an arrival a
+                                      // warp, here and below)
     uint64_t kfull[2], kempty[2];     // decoded K blocks
     uint64_t vfull[2], vempty[2];
     uint64_t sfull[2];                // a tile's scores are in tensor memory
@@ -244,39 +234,40 @@ struct Barriers {
     uint64_t drain;
 };
 
-// ---- warps 8..11: the cache to f16 ----------------------------------------------------
-// 32 tokens of a block a warp: a lane takes 32 elements (16 bytes of codes, two
-// scales) of every RPI-th row, neighbouring lanes neighbouring bytes.
+// ---- warps 8..15: the cache to f16 ----------------------------------------------------
+// 16 tokens of a block a warp: a lane takes 32 elements (16 bytes of codes, two
+// scales) of every kRpi-th row, neighbouring lanes neighbouring bytes.
 template <int D>
 struct Raw {
     static constexpr int kLanes = D / 32;        // lanes a row
     static constexpr int kRpi = 32 / kLanes;     // rows at a time
-    static constexpr int kIters = 32 / kRpi;
+    static constexpr int kIters = kDecodeRows / kRpi;
     uint4 c[kIters];
     uint32_t s[kIters];
 };
 
-// The K or V rows of a warp's 32 tokens; page[i] holds the i-th 16 of them (-1:
-// nothing there, the rows become zeros).
+// The K or V rows of a warp's 16 tokens, which lie in one page (-1: nothing
+// there, the rows become zeros).
 template <int D>
-__device__ __forceinline__ void load_rows(Raw<D>& x, const KvAttnArgs& a, const int32_t (&page)[2],
-                                          int32_t tok0, int32_t seq, int h, bool is_v)
+__device__ __forceinline__ void load_rows(Raw<D>& x, const KvAttnArgs& a, int32_t page, int32_t tok0,
+                                          int32_t seq, int h, bool is_v)
 {
     using X = Raw<D>;
-    const int P = a.c.page_shift, lane = threadIdx.x & 31, t = lane % X::kLanes;
+    const int P = a.c.page_shift, lane = threadIdx.x & 31;
+    const int32_t off0 = tok0 & ((1 << P) - 1);
+    const uint8_t* p = a.c.pool + page * a.c.page_stride + h * kv_head_bytes(P, D);
+    const uint8_t* codes = p + (is_v ? (D / 2) << P : 0) + off0 * (D / 2) + lane * 16;
+    const uint8_t* scales =
+        p + (D << P) + (is_v ? (D / 16) << P : 0) + off0 * (D / 16) + lane * 2;
 #pragma unroll
     for (int i = 0; i < X::kIters; ++i) {
         const int row = i * X::kRpi + lane / X::kLanes;
-        const int32_t pg = row < 16 ? page[0] : page[1], tok = tok0 + row;
+        const bool there = page >= 0 && tok0 + row < seq;
         x.c[i] = make_uint4(0u, 0u, 0u, 0u);
         x.s[i] = 0u;
-        if (pg >= 0 && tok < seq) {
-            const int32_t off = tok & ((1 << P) - 1);
-            const uint8_t* p = a.c.pool + pg * a.c.page_stride + h * kv_head_bytes(P, D);
-            x.c[i] = __ldg(reinterpret_cast<const uint4*>(p + (is_v ? (D / 2) << P : 0) +
-                                                          off * (D / 2) + 16 * t));
-            x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(
-                p + (D << P) + (is_v ? (D / 16) << P : 0) + off * (D / 16) + 2 * t));
+        if (there) {
+            x.c[i] = __ldg(reinterpret_cast<const uint4*>(codes + i * 512));
+            x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + i * 64));
         }
     }
 }
@@ -327,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.qfull[i]), kRowsTile / 32);
-            mbar_init(smem_u32(&bars.kfull[i]), kKeys / 32);
+            mbar_init(smem_u32(&bars.kfull[i]), kKeys / kDecodeRows);
             mbar_init(smem_u32(&bars.kempty[i]), 1);
-            mbar_init(smem_u32(&bars.vfull[i]), kKeys / 32);
+            mbar_init(smem_u32(&bars.vfull[i]), kKeys / kDecodeRows);
             mbar_init(smem_u32(&bars.vempty[i]), 1);
             mbar_init(smem_u32(&bars.sfull[i]), 1);
             mbar_init(smem_u32(&bars.pfull[i]), kRowsTile / 32);
@@ -372,11 +363,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         const float vg = a.c.v_g[0], signed_qk = a.scale_log2 * a.c.k_g[0], qk = fabsf(signed_qk);
         const uint32_t flip = signed_qk < 0.f ? 0x80008000u : 0u;
         uint32_t blocks = 0, items = 0;  // this tile's so far
-        for (; more; more = Work::next(a, sh, it)) {
+        KvItem nx;
+        for (; more; it = nx) {
             __syncwarp();
             const int tile0 = it.row0 + st * kRowsTile;
-            if (tile0 >= it.row1)
-                continue;  // the item has no second tile
+            if (tile0 >= it.row1) {  // the item has no second tile
+                nx = it;
+                more = Work::next(a, sh, nx);
+                continue;
+            }
             const int row = tile0 + r;
             const bool live = row < it.row1;
             // this thread's row: token and head; the others' by shuffle
@@ -392,25 +387,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             // two and leaves it as f16
             {
                 const int64_t at = row_at(a.q_stride);
-#pragma unroll 1
-                for (int i0 = 0; i0 < 32; i0 += 8 * kRowsAtOnce) {
-                    uint2 w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int x = i0 + i * kRowsAtOnce + my_row;
-                        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, x);
-                        w[i] = x < rows_here
-                                   ? __ldg(reinterpret_cast<const uint2*>(
-                                               static_cast<const __nv_bfloat16*>(a.q) + from) +
-                                           my_part)
-                                   : make_uint2(0u, 0u);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint2*>(
-                            tile + piece_at(wrow + i0 + i * kRowsAtOnce + my_row, my_part >> 1) +
-                            8 * (my_part & 1)) = w[i];
+#pragma unroll 4
+                for (int i = 0; i < 32; i += kRowsAtOnce) {
+                    const int x = i + my_row;
+                    const int64_t from = __shfl_sync(0xFFFFFFFFu, at, x);
+                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + from +
+                                               4 * my_part;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
+                                     smem_u32(tile + piece_at(wrow + x, my_part >> 1)) +
+                                     8 * (my_part & 1)),
+                                 "l"(src), "r"(x < rows_here ? 8u : 0u)
+                                 : "memory");
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
             }
             __syncwarp();
             float f;
@@ -446,6 +435,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             fence_before();  // the last item's reads of the output come before this item's products
             warp_arrive(qfull);
 
+            // the next item, while this one's first scores are made: its query rows to L2
+            nx = it;
+            more = Work::next(a, sh, nx);
+            {
+                const int x = nx.row0 + st * kRowsTile + r;
+                if (more && x < nx.row1) {
+                    const int y = kv_token(a, x);
+                    const char* q = reinterpret_cast<const char*>(
+                        static_cast<const __nv_bfloat16*>(a.q) + (nx.q.base + y) * a.q_stride +
+                        (int64_t)(nx.h * a.group + x - y * a.group) * D);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                    if constexpr (D > 64)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128));
+                }
+            }
+
             const int32_t pos = live ? it.q.seq - it.q.nq + tok : -1;
             float m = -INFINITY, l = 0.f;  // reference minus kLift, and the sum
             const uint64_t f2 = pair(f, f);
@@ -456,29 +461,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 const bool edge = last < kKeys - 1 || first > 0;
                 mbar_wait(sfull, blocks & 1, abort_flag, a.status);
                 fence_after();
-                // bit i: column c + i of a chunk of 16 is seen
-                auto seen16 = [&](int c) {
-                    const int lo = min(max(first - c, 0), 16), hi = min(max(last - c + 1, 0), 16);
-                    return (0xFFFFu >> (16 - hi)) & (0xFFFFu << lo);
-                };
-                auto load16 = [&](int c, uint32_t* s) { tmem_ld16(tS + c, s); };
+                // scores outside [first, last] of the 32 from c on become -inf
                 auto hide = [&](int c, uint32_t* s) {
-                    const uint32_t seen = seen16(c);
+                    int lo = first - c, hi = last - c + 1;
+                    asm volatile("" : "+r"(lo), "+r"(hi));  // not computed where it is not needed
+                    lo = min(max(lo, 0), 32);
+                    hi = min(max(hi, 0), 32);
+                    const uint32_t seen = __funnelshift_lc(0u, 0xFFFFFFFFu, lo) &
+                                          ~__funnelshift_lc(0u, 0xFFFFFFFFu, hi);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[i] = seen >> i & 1 ? s[i] : 0xFF800000u;  // -inf
+                    for (int i = 0; i < 32; ++i)
+                        s[i] = seen >> i & 1 ? s[i] : 0xFF800000u;
                 };
                 if (u == it.u0) {  // the first reference: the block's largest score
                     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 16) {
-                        uint32_t s[16];
-                        load16(c, s);
-                        tmem_wait_ld16(s);
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(tS + c, s);
+                        tmem_wait_ld(s);
                         if (edge)
                             hide(c, s);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
+                        for (int i = 0; i < 32; i += 4)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
                                 top[j] = fmaxf(top[j], fmaxf(__uint_as_float(s[i + 2 * j]),
@@ -487,69 +492,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     m = fmaxf(top[0], top[1]);
                     m = m == -INFINITY ? m : m * f - kLift;
                 }
-                uint32_t p16[kKeys / 2];
-                float sum;
-                // usually one pass; a second when the reference had to be raised
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t p16[16];
+                    float sum;
+                    // usually once; a second time when the reference had to be raised
 #pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    // no key seen yet: every score is -inf, against any finite reference
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    const uint64_t neg = pair(-ref, -ref);
-                    float top[2] = {-INFINITY, -INFINITY};
-                    uint64_t sums[2] = {0ull, 0ull};
-                    uint32_t s[2][16];  // a chunk, and the next on its way
-                    load16(0, s[0]);
-#pragma unroll
-                    for (int c = 0; c < kKeys; c += 16) {
-                        uint32_t* x16 = s[(c >> 4) & 1];
-                        tmem_wait_ld16(x16);
-                        if (c + 16 < kKeys)
-                            load16(c + 16, s[((c >> 4) + 1) & 1]);
+                    for (int pass = 0;; ++pass) {
+                        // no key seen yet: every score is -inf, against any finite reference
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const uint64_t neg = pair(-ref, -ref);
+                        float top[2] = {-INFINITY, -INFINITY};
+                        uint64_t sums[2] = {0ull, 0ull};
+                        uint32_t s[32];
+                        tmem_ld32(tS + c, s);
+                        tmem_wait_ld(s);
                         if (edge)
-                            hide(c, x16);
+                            hide(c, s);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
+                        for (int i = 0; i < 32; i += 2) {
                             const uint64_t x = fma2(
-                                pair(__uint_as_float(x16[i]), __uint_as_float(x16[i + 1])), f2, neg);
+                                pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2, neg);
                             float p0, p1;
                             unpair(x, p0, p1);
                             top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(p0, p1));
                             p0 = ex2(p0);
                             p1 = ex2(p1);
                             sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], pair(p0, p1));
-                            p16[(c + i) / 2] = pack_f16(p0, p1);
+                            p16[i / 2] = pack_f16(p0, p1);
                         }
-                    }
-                    float x0, x1;
-                    unpair(add2(sums[0], sums[1]), x0, x1);
-                    sum = x0 + x1;
-                    const float best = fmaxf(top[0], top[1]);  // against ref
-                    // (a row that has seen no key takes its first reference too)
-                    const bool raise = best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
-                    if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
-                        break;
-                    const float now = fmaxf(m, best + ref - kLift);
-                    const float by = m == now ? 1.f : ex2(m - now);
-                    m = now;
-                    l *= by;
-                    // earlier products are complete: this block's scores were issued
-                    // after them, and their commit covers both
-                    if (u > it.u0) {
+                        float x0, x1;
+                        unpair(add2(sums[0], sums[1]), x0, x1);
+                        sum = x0 + x1;
+                        const float best = fmaxf(top[0], top[1]);  // against ref
+                        // (a row that has seen no key takes its first reference too)
+                        const bool raise =
+                            best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
+                        if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
+                            break;
+                        const float now = fmaxf(m, best + ref - kLift);
+                        const float by = m == now ? 1.f : ex2(m - now);
+                        m = now;
+                        l *= by;
+                        // The output so far (its products are complete: this block's scores
+                        // were issued after them, and their commit covers both) and this
+                        // block's probabilities so far, which lie over scores already used.
+                        tmem_wait_st();
+                        if (u > it.u0) {
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + i, o);
+                                tmem_wait_ld16(o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+                                tmem_st16(tO + i, o);
+                            }
+                        }
+                        const uint32_t by16 = pack_f16(by, by);
+#pragma unroll 1
+                        for (int i = 0; i < c / 2; i += 16) {
                             uint32_t o[16];
-                            tmem_ld16(tO + i, o);
+                            tmem_ld16(tS + i, o);
                             tmem_wait_ld16(o);
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-                            tmem_st16(tO + i, o);
+                                o[j] = f16x2_mul(o[j], by16);
+                            tmem_st16(tS + i, o);
                         }
                     }
+                    l += sum;
+                    tmem_st16(tS + c / 2, p16);
                 }
-                l += sum;
-                tmem_st32(tS, p16);
-                tmem_st32(tS + 32, p16 + 32);
                 tmem_wait_st();
                 fence_before();
                 warp_arrive(pfull);
@@ -666,31 +681,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             write_lse(mt, lt);
         }
     } else if (warp < kMmaWarp) {
-        // ---- decode: 32 tokens of a block a warp -------------------------------------------------
-        const int row0 = 32 * (warp - kDecodeWarp);
+        // ---- decode: 16 tokens of a block a warp -------------------------------------------------
+        const int row0 = kDecodeRows * (warp - kDecodeWarp);
         bool bad = false;
-        // a block's rows are loaded a block ahead, their pages (16 tokens each) two
+        // a block's rows are loaded a block ahead, their page two
         Raw<D> k, v;
-        int32_t pages[2] = {-1, -1};
+        int32_t page = -1;
         auto look_up = [&](const KvItem& y, int32_t u) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int32_t tok = (y.first + u) * kKeys + row0 + 16 * i, b = tok >> a.c.page_shift;
-                int32_t page = -1;
-                if (tok < y.q.seq && b < a.max_blocks) {
-                    page = a.table[y.r * a.table_stride + b];
-                    if (page < 0 || page >= a.c.num_pages) {
-                        bad = true;
-                        page = -1;
-                    }
+            const int32_t tok = (y.first + u) * kKeys + row0, b = tok >> a.c.page_shift;
+            page = -1;
+            if (tok < y.q.seq && b < a.max_blocks) {
+                page = a.table[y.r * a.table_stride + b];
+                if (page < 0 || page >= a.c.num_pages) {
+                    bad = true;
+                    page = -1;
                 }
-                pages[i] = page;
             }
         };
         auto load = [&](const KvItem& y, int32_t u) {
             const int32_t tok0 = (y.first + u) * kKeys + row0;
-            load_rows<D>(k, a, pages, tok0, y.q.seq, y.h, false);
-            load_rows<D>(v, a, pages, tok0, y.q.seq, y.h, true);
+            load_rows<D>(k, a, page, tok0, y.q.seq, y.h, false);
+            load_rows<D>(v, a, page, tok0, y.q.seq, y.h, true);
         };
         int32_t u = 0;
         auto advance = [&]() {  // to the block after u of `it`
@@ -735,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
     } else {
-        // ---- warp 12: the MMAs --------------------------------------------------------------------
+        // ---- warp 16: the MMAs --------------------------------------------------------------------
         uint32_t one;
         asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
