@@ -118,37 +118,34 @@ __device__ __forceinline__ void fence_before()
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 
-// 32 columns of this warp's 32 rows, a thread a row (tmem_wait_ld before use).
-__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* v)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
-          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(t));
-}
+// 16 or 32 columns of this warp's 32 rows, a thread a row; complete on return.
 __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* v)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+        "}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(t));
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(t)
+        : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t* v)
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* v)
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
-        "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
-        "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-                 :
-                 : "memory");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%"
+        "21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+        "}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31])
+        : "r"(t)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v)
 {
@@ -159,20 +156,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v)
         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
         "r"(v[14]), "r"(v[15])
         : "memory");
-}
-// The loads are complete; the values are tied to the wait so that no use of
-// theirs can be scheduled before it.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t* v)
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
-                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                 "+r"(v[30]), "+r"(v[31])
-                 :
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st()
 {
@@ -479,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     for (int c = 0; c < kKeys; c += 32) {
                         uint32_t s[32];
                         tmem_ld32(tS + c, s);
-                        tmem_wait_ld(s);
                         if (edge)
                             hide(c, s);
 #pragma unroll
@@ -506,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                         uint64_t sums[2] = {0ull, 0ull};
                         uint32_t s[32];
                         tmem_ld32(tS + c, s);
-                        tmem_wait_ld(s);
                         if (edge)
                             hide(c, s);
 #pragma unroll
@@ -543,7 +524,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                             for (int i = 0; i < D; i += 16) {
                                 uint32_t o[16];
                                 tmem_ld16(tO + i, o);
-                                tmem_wait_ld16(o);
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
                                     o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
@@ -555,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                         for (int i = 0; i < c / 2; i += 16) {
                             uint32_t o[16];
                             tmem_ld16(tS + i, o);
-                            tmem_wait_ld16(o);
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
                                 o[j] = f16x2_mul(o[j], by16);
@@ -616,7 +595,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             for (int i = 0; i < D; i += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + i, o);
-                tmem_wait_ld(o);
                 float x[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)

@@ -39,11 +39,18 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 // Wait for phase `parity`; false when the budget (or another wait's) ran out.
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                            unsigned* status)
+// Clock and flag are looked at once in kKvPolls tests only: at every test they
+// took a quarter of the issue slots of a kernel whose warps wait in turn.
+constexpr int kKvPolls = 64;
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
+                                                   volatile int* abort_flag, unsigned* status)
 {
     const long long t0 = clock64();
-    while (!mbar_test(bar, parity)) {
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < kKvPolls; ++i)
+            if (mbar_test(bar, parity))
+                return true;
         if (*abort_flag)
             return false;
         if (clock64() - t0 > kKvWaitBudget) {
@@ -52,7 +59,6 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
             return false;
         }
     }
-    return true;
 }
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           unsigned* status)
