@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
     __shared__ typename Work::Smem work_sm;
-    __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_f[R];
+    __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_f[R], sm_sum[R];
     __shared__ int32_t sm_pos[R];
     __shared__ int last_s, abort_s;
     float4* red = reinterpret_cast<float4*>(smem + C::kRingBytes);
@@ -152,10 +152,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     }
     kv_pdl_begin();
 
-    // at least an item's cost and a group for each pair of warps
+    // at least as many groups as the warps take in one round
     Share sh;
     Item it;
-    bool more = Work::template start<kThreads>(a, work_sm, kItemCost + 2, sh, it);
+    bool more = Work::template start<kThreads>(a, work_sm, kWarps / kSub, sh, it);
     if (sh.lo >= sh.hi)
         return;
 
@@ -623,25 +623,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                   tok * a.group] =
                 ltot == 0.f ? -INFINITY : 0.6931471805599453f * (mtot + log2f(ltot));
         };
-        // reference and sum of a column over the warps
-        auto column = [&](int col, float& mtot, float& ltot) {
-            mtot = -INFINITY;
+        // a column's largest reference of the warps, by which all rescale
+        auto column = [&](int col) {
+            float mt = sm_m[0][col];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                mtot = fmaxf(mtot, sm_m[w][col]);
-            ltot = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                ltot += sm_m[w][col] == mtot ? sm_l[w][col] : sm_l[w][col] * ex2(sm_m[w][col] - mtot);
+            for (int w = 1; w < kWarps; ++w)
+                mt = fmaxf(mt, sm_m[w][col]);
+            return mt;
         };
+        if (tid < R) {
+            const float mt = column(tid);
+            float lt = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                lt += sm_m[w][tid] == mt ? sm_l[w][tid] : sm_l[w][tid] * ex2(sm_m[w][tid] - mt);
+            sm_sum[tid] = lt;
+            if (whole) {
+                store_lse(tid, mt, lt);
+            } else {
+                float* ml = a.part + slot * kPart + (int64_t)NT * kFrag * 4;
+                ml[tid] = mt;
+                ml[R + tid] = lt;
+            }
+        }
 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float mt[2], lt[2], by[2];
+            float by[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                column(nt * 8 + 2 * t + e, mt[e], lt[e]);
-                by[e] = m[nt][e] == mt[e] ? 1.f : ex2(m[nt][e] - mt[e]);
+                const float mt = column(nt * 8 + 2 * t + e);
+                by[e] = m[nt][e] == mt ? 1.f : ex2(m[nt][e] - mt);
             }
 #pragma unroll
             for (int i = 0; i < KS; ++i)
@@ -657,31 +669,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                 }
                 if (whole) {
-                    store2(nt * 8 + 2 * t, e >> 5, e & 31, v.x, v.z, lt[0]);
-                    store2(nt * 8 + 2 * t + 1, e >> 5, e & 31, v.y, v.w, lt[1]);
+                    const int col = nt * 8 + 2 * (e & 3);
+                    store2(col, e >> 5, e & 31, v.x, v.z, sm_sum[col]);
+                    store2(col + 1, e >> 5, e & 31, v.y, v.w, sm_sum[col + 1]);
                 } else {
                     reinterpret_cast<float4*>(a.part + slot * kPart)[nt * kFrag + e] = v;
                 }
             }
             compute_sync();
         }
-        if (tid < R) {
-            float mt, lt;
-            column(tid, mt, lt);
-            if (whole) {
-                store_lse(tid, mt, lt);
-            } else {
-                float* ml = a.part + slot * kPart + (int64_t)NT * kFrag * 4;
-                ml[tid] = mt;
-                ml[R + tid] = lt;
-            }
-        }
         if (!whole) {
             // ---- join the CTAs: the last to arrive sums all parts in CTA order ----------------
             const int ca = Work::first_cta(sh, it), cb = Work::last_cta(sh, it);
-            __threadfence();
-            compute_sync();
             if (tid == 0) {
+                __threadfence();  // the CTA's writes (the barrier above orders them before)
                 const unsigned seen = atomicAdd(a.count + ca, 1u);
                 last_s = seen == (unsigned)(cb - ca);
                 if (last_s)
@@ -690,37 +691,80 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             }
             compute_sync();
             if (last_s) {
-                for (int nt = 0; nt < NT; ++nt)
-                    for (int e = tid; e < kFrag; e += kCompute) {
-                        const int col = nt * 8 + 2 * (e & 3);
-                        float mt[2] = {-INFINITY, -INFINITY}, lt[2] = {0.f, 0.f};
-                        for (int c = ca; c <= cb; ++c) {
-                            const float* ml = a.part + (2 * c + (c == ca)) * kPart +
-                                              (int64_t)NT * kFrag * 4 + col;
-                            mt[0] = fmaxf(mt[0], __ldcg(ml));
-                            mt[1] = fmaxf(mt[1], __ldcg(ml + 1));
-                        }
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int c = ca; c <= cb; ++c) {
-                            const float* pc = a.part + (2 * c + (c == ca)) * kPart;
-                            const float* ml = pc + (int64_t)NT * kFrag * 4 + col;
-                            const float4 o =
-                                __ldcg(reinterpret_cast<const float4*>(pc) + nt * kFrag + e);
-                            const float m0 = __ldcg(ml), m1 = __ldcg(ml + 1);
-                            const float b0 = m0 == mt[0] ? 1.f : ex2(m0 - mt[0]);
-                            const float b1 = m1 == mt[1] ? 1.f : ex2(m1 - mt[1]);
-                            lt[0] += b0 * __ldcg(ml + R);
-                            lt[1] += b1 * __ldcg(ml + R + 1);
-                            v.x = fmaf(o.x, b0, v.x), v.y = fmaf(o.y, b1, v.y);
-                            v.z = fmaf(o.z, b0, v.z), v.w = fmaf(o.w, b1, v.w);
-                        }
-                        store2(col, e >> 5, e & 31, v.x, v.z, lt[0]);
-                        store2(col + 1, e >> 5, e & 31, v.y, v.w, lt[1]);
-                        if (e < 4) {  // one entry a column pair
-                            store_lse(col, mt[0], lt[0]);
-                            store_lse(col + 1, mt[1], lt[1]);
+                // references and sums of column `col` of part c
+                auto ml = [&](int c) {
+                    return a.part + (2 * c + (c == ca)) * kPart + (int64_t)NT * kFrag * 4;
+                };
+                // over all parts, kStep threads a column, joined in order
+                constexpr int kStep = kCompute / R;
+                float* scratch = reinterpret_cast<float*>(red);
+                const int col = tid % R, k0 = tid / R;
+                float mt = -INFINITY;
+                for (int c = ca + k0; c <= cb; c += kStep)
+                    mt = fmaxf(mt, __ldcg(ml(c) + col));
+                scratch[tid] = mt;
+                compute_sync();
+                for (int k = 0; k < kStep; ++k)
+                    mt = fmaxf(mt, scratch[k * R + col]);
+                float lt = 0.f;
+                for (int c = ca + k0; c <= cb; c += kStep) {
+                    const float mc = __ldcg(ml(c) + col);
+                    lt += __ldcg(ml(c) + R + col) * (mc == mt ? 1.f : ex2(mc - mt));
+                }
+                compute_sync();
+                scratch[tid] = lt;
+                if (tid < R)
+                    sm_f[col] = mt;
+                compute_sync();
+                if (tid < R) {
+                    lt = scratch[col];
+                    for (int k = 1; k < kStep; ++k)
+                        lt += scratch[k * R + col];
+                    sm_sum[col] = lt;
+                    store_lse(col, mt, lt);
+                }
+                // the parts, as many at a time as their factors fit
+                constexpr int kPiece = C::kRedBytes / (4 * R);
+                constexpr int kOwn = (NT * kFrag + kCompute - 1) / kCompute;
+                float4 v[kOwn];
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j)
+                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c0 = ca; c0 <= cb; c0 += kPiece) {
+                    const int n = min(kPiece, cb - c0 + 1);
+                    compute_sync();
+                    for (int k = tid; k < n * R; k += kCompute) {
+                        const float mc = __ldcg(ml(c0 + k / R) + k % R), top = sm_f[k % R];
+                        scratch[k] = mc == top ? 1.f : ex2(mc - top);
+                    }
+                    compute_sync();
+#pragma unroll
+                    for (int j = 0; j < kOwn; ++j) {
+                        const int e = tid + j * kCompute;
+                        if (e >= NT * kFrag)
+                            break;
+                        const float* by = scratch + (e / kFrag) * 8 + 2 * (e & 3);
+#pragma unroll 4
+                        for (int k = 0; k < n; ++k) {
+                            const int c = c0 + k;
+                            const float4 o = __ldcg(
+                                reinterpret_cast<const float4*>(a.part + (2 * c + (c == ca)) * kPart) +
+                                e);
+                            const float b0 = by[k * R], b1 = by[k * R + 1];
+                            v[j].x = fmaf(o.x, b0, v[j].x), v[j].y = fmaf(o.y, b1, v[j].y);
+                            v[j].z = fmaf(o.z, b0, v[j].z), v[j].w = fmaf(o.w, b1, v[j].w);
                         }
                     }
+                }
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) {
+                    const int e = tid + j * kCompute, f = e % kFrag;
+                    if (e >= NT * kFrag)
+                        break;
+                    const int c2 = (e / kFrag) * 8 + 2 * (e & 3);
+                    store2(c2, f >> 5, f & 31, v[j].x, v[j].z, sm_sum[c2]);
+                    store2(c2 + 1, f >> 5, f & 31, v[j].y, v[j].w, sm_sum[c2 + 1]);
+                }
             }
         }
         compute_sync();  // shared memory is free for the next item

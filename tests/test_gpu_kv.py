@@ -572,3 +572,60 @@ def test_growing_scores_in_tiles(nv):
     for kernel in (nv.KERNEL_KV_ROWS, nv.KERNEL_KV_TILE):
         out, lse = nv.kv_attention(cache, q, table, ints([900]), return_lse=True, kernel=kernel)
         check_attention(out, lse, attention(cache, q, table, [900], [300]), BF16)
+
+
+# ---- append, more ----------------------------------------------------------------------
+
+def test_append_ties_and_signs(nv):
+    """Elements on every rounding boundary of E2M1, both signs, zeros of both
+    signs, saturation; the block scale is exactly 1 (maximum 6, tensor scale 1)."""
+    grid = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]
+    vals = grid + [np.nextafter(np.float32(x), np.float32(s)) for x in grid[:7] for s in (0, 9)] + [0.0]
+    x = torch.tensor(np.array(vals + [-v for v in vals], np.float32))
+    rows = x[torch.randint(0, len(x), (64, 128), generator=torch.Generator().manual_seed(1))]
+    rows[:, ::16] = 6.0
+    rows[::2, 5::16] = -0.0
+    rows = rows.cuda()
+    one = ints([1.0], FP32)
+    cache, whole = make_cache(nv, 4, 1, 128, 16, one, one)
+    nv.kv_append(cache, rows[:, None], -rows[:, None], torch.arange(64, device="cuda"))
+    kk, vv = page_values(cache.pool, 16, 128)
+    for got, want in ((kk, rows), (vv, -rows)):
+        q, s = oracle.quantize(want.cpu().numpy(), np.float32(1.0))
+        q = torch.from_numpy(q).cuda()
+        part = cache.pool[:, 0, :1024] if want is rows else cache.pool[:, 0, 1024:2048]
+        assert torch.equal(part.reshape(64, 64), q)
+        assert (s == 0x38).all()
+        assert (got[:, 0].reshape(64, 128) - want.double()).abs().max() <= 1.0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -130, 2.0 ** -110, 2.0 ** 105, 2.0 ** 118])
+def test_append_extreme_magnitudes(nv, scale):
+    """Blocks whose scale leaves the domain of the reciprocal's correction."""
+    x = (torch.randn((40, 2, 64), generator=torch.Generator().manual_seed(3)) * scale).cuda()
+    x[3] = 0.0
+    g = nv.global_scale(x)
+    cache, whole = make_cache(nv, 3, 2, 64, 16, g, g)
+    nv.kv_append(cache, x, x, torch.arange(40, device="cuda"))
+    q, s = oracle.quantize(x.cpu().numpy().reshape(80, 64), np.float32(g.item()))
+    got = torch.cat([cache.pool[t // 16, h, t % 16 * 32:t % 16 * 32 + 32][None]
+                     for t in range(40) for h in range(2)])
+    assert torch.equal(got.cpu(), torch.from_numpy(q))
+
+
+@pytest.mark.parametrize("tokens", [9000, 30001])
+def test_append_many_tokens(nv, tokens):
+    """Many tokens (several a thread), unaligned BF16 rows, against few at a time."""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    flat = torch.randn((tokens, 2 * 4 * 64 + 4), generator=gen, device="cuda").to(BF16)
+    k, v = (flat[:, 4 + 256 * i:4 + 256 * (i + 1)].unflatten(1, (4, 64)) for i in range(2))
+    g = ints([0.002], FP32)
+    pages = -(-tokens // 64) + 1
+    a, pool_a = make_cache(nv, pages, 4, 64, 64, g, g, fill=0)
+    b, pool_b = make_cache(nv, pages, 4, 64, 64, g, g, fill=0)
+    slots = torch.randperm(pages * 64, generator=gen, device="cuda")[:tokens].contiguous()
+    slots[5::11] = -1
+    nv.kv_append(a, k, v, slots)
+    for i in range(0, tokens, 1000):
+        nv.kv_append(b, k[i:i + 1000].float().contiguous(), v[i:i + 1000].float().contiguous(), slots[i:i + 1000])
+    assert torch.equal(pool_a, pool_b)
