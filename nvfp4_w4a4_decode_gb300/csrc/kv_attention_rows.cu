@@ -508,43 +508,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                         }
 
                     // ---- O^T += V^T P^T: this lane's eighth of the head dim, tokens of rows 2t .. --
+                    uint32_t vw[HB][4][D / 64], vs[HB][2];
 #pragma unroll
                     for (int h = 0; h < HB; ++h) {
                         const uint8_t* sv = st + (h0 + h) * code_half + v_part;
                         const uint8_t* ss = sk + (h0 + h) * scale_half + s_part;
-                        uint32_t vw[4][D / 64], vs[4];
+                        uint32_t one[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int vt = v_tok + (k >> 1) * 8 + (k & 1) * v_odd;
                             if constexpr (D == 128) {
                                 const uint2 v = *reinterpret_cast<const uint2*>(sv + vt * 64 + 8 * g);
-                                vw[k][0] = v.x, vw[k][1] = v.y;
-                                vs[k] = ss[vt * 8 + g];
+                                vw[h][k][0] = v.x, vw[h][k][1] = v.y;
+                                one[k] = ss[vt * 8 + g];
                             } else {
-                                vw[k][0] = *reinterpret_cast<const uint32_t*>(sv + vt * 32 + 4 * g);
-                                vs[k] = ss[vt * 4 + (g >> 1)];
+                                vw[h][k][0] = *reinterpret_cast<const uint32_t*>(sv + vt * 32 + 4 * g);
+                                one[k] = ss[vt * 4 + (g >> 1)];
                             }
                         }
                         if (tok0 + 16 * h + 16 > it.q.seq) {  // past the end may be anything
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (tok0 + 16 * h + v_tok + (k >> 1) * 8 + (k & 1) * v_odd >= it.q.seq) {
-                                    vs[k] = 0;
+                                    one[k] = 0;
 #pragma unroll
                                     for (int w = 0; w < D / 64; ++w)
-                                        vw[k][w] = 0;
+                                        vw[h][k][w] = 0;
                                 }
                         }
-                        const uint32_t s01 = e4m3x2_to_f16x2_bits(vs[0] | (vs[1] << 8));
-                        const uint32_t s23 = e4m3x2_to_f16x2_bits(vs[2] | (vs[3] << 8));
+                        vs[h][0] = one[0] | (one[1] << 8);
+                        vs[h][1] = one[2] | (one[3] << 8);
+                    }
+                    if (h0 + HB == kUnit / 16) {  // all read: the slot can be filled again
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(empty0 + 8 * slot);
+                    }
+#pragma unroll
+                    for (int h = 0; h < HB; ++h) {
+                        const uint32_t s01 = e4m3x2_to_f16x2_bits(vs[h][0]);
+                        const uint32_t s23 = e4m3x2_to_f16x2_bits(vs[h][1]);
 #pragma unroll
                         for (int w = 0; w < D / 64; ++w) {
                             constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                            const uint32_t x0 = vw[h][0][w], x1 = vw[h][1][w];
+                            const uint32_t x2 = vw[h][2][w], x3 = vw[h][3][w];
                             uint32_t e0[4], e1[4], o0[4], o1[4];  // even / odd elements, token pairs
-                            e2m1x8_to_f16((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), e0);
-                            e2m1x8_to_f16(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), o0);
-                            e2m1x8_to_f16((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), e1);
-                            e2m1x8_to_f16(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), o1);
+                            e2m1x8_to_f16((x0 & kLow) | ((x1 << 4) & ~kLow), e0);
+                            e2m1x8_to_f16(((x0 >> 4) & kLow) | (x1 & ~kLow), o0);
+                            e2m1x8_to_f16((x2 & kLow) | ((x3 << 4) & ~kLow), e1);
+                            e2m1x8_to_f16(((x2 >> 4) & kLow) | (x3 & ~kLow), o1);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t a0 = f16x2_mul(e0[k], s01), a1 = f16x2_mul(o0[k], s01);
@@ -559,10 +572,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                         }
                     }
                 }
-                __syncwarp();  // every lane has read the slot
-            }
-            if (lane == 0)
+            } else if (lane == 0) {
                 mbar_arrive(empty0 + 8 * slot);
+            }
         }
 
         // ---- join the warps ---------------------------------------------------------------
