@@ -49,7 +49,7 @@ constexpr int kUnit = 32;       // tokens a unit
 constexpr int kGroup = 64;      // tokens a group
 constexpr int kSub = kGroup / kUnit;
 #ifndef KV_BATCH
-#define KV_BATCH 2
+#define KV_BATCH 3
 #endif
 constexpr int kBatch = KV_BATCH;
 #ifndef KV_WARPS
