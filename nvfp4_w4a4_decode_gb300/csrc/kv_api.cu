@@ -11,9 +11,17 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
-// Query rows a request (tokens * heads of a group) above which the tcgen05
-// kernel takes BF16 attention.
-constexpr int64_t kTileRows = 64;
+// Whether the tcgen05 kernel takes an attention call: its tiles of 128 rows and
+// its start of some 8 us an item want many rows a request, and enough of them
+// in all.  Measured both ways on GB300 (rows kernel / tile kernel, us): 64
+// requests of 4000 tokens, 8 kv heads of 128, 32 rows a request 186 / 277, 48 rows 336 /
+// 278; 16 of 1000, 64 rows 51 / 44; 16 of 8000, 4 kv heads of 64, 64 rows 57 / 64, 96 rows
+// 81 / 64; one of 30000, 8 kv heads, 128 rows 87 / 100, 256 rows 146 / 106; one of 2000,
+// 256 rows 34 / 42.
+bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
+{
+    return rows > 32 && reqs * heads * rows >= 2048;
+}
 
 bool aligned(const void* p, uintptr_t a)
 {
@@ -207,7 +215,8 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     a.q_bf16 = q_bf16;
     a.out_bf16 = out_bf16;
     const bool tile = kern == NVFP4_KERNEL_KV_TILE ||
-                      (kern == NVFP4_KERNEL_AUTO && all_bf16 && (int64_t)a.max_q * a.group > kTileRows);
+                      (kern == NVFP4_KERNEL_AUTO && all_bf16 &&
+                       use_tile(a.reqs, a.c.heads, (int64_t)a.max_q * a.group));
     const auto launch = tile ? nvfp4::launch_kv_tile : nvfp4::launch_kv_rows;
     return from_cuda(launch(a, workspace, (int64_t)workspace_bytes,
                             static_cast<cudaStream_t>(stream), (options & NVFP4_FLAG_PDL) != 0));

@@ -48,17 +48,8 @@ namespace {
 constexpr int kUnit = 32;       // tokens a unit
 constexpr int kGroup = 64;      // tokens a group
 constexpr int kSub = kGroup / kUnit;
-#ifndef KV_BATCH
-#define KV_BATCH 3
-#endif
-constexpr int kBatch = KV_BATCH;
-#ifndef KV_WARPS
-#define KV_WARPS 7
-#endif
-#ifndef KV_CTAS
-#define KV_CTAS 2
-#endif
-constexpr int kWarps = KV_WARPS;       // compute warps: with the copying warp eight, two
+constexpr int kBatch = 3;       // groups the copying warp brings at a time
+constexpr int kWarps = 7;       // compute warps: with the copying warp eight, two
                                 // for each of the SM's four register files
 constexpr int kCompute = 32 * kWarps;
 constexpr int kThreads = kCompute + 32;
@@ -105,11 +96,8 @@ struct Cfg {
     static constexpr int kStageBytes = kGroup * D * 9 / 8;
     // two CTAs an SM where the registers allow it: the joins and starts of one
     // overlap the other's stream
-    static constexpr int kCtas = NT == 1 && !SPLIT ? KV_CTAS : 1;
-    #ifndef KV_ST
-#define KV_ST 7
-#endif
-    static constexpr int kStages = KV_ST;
+    static constexpr int kCtas = NT == 1 && !SPLIT ? 2 : 1;
+        static constexpr int kStages = 7;
     static constexpr int kQTerms = SPLIT ? 2 : 1;
     static constexpr int kQBytes = kQTerms * NT * KS * 32 * 8;
     static constexpr int kRingBytes = kStages * kStageBytes;
@@ -256,10 +244,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     const int code_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 2);
     const int scale_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 16);
     const int ka = token_of_row(g), v_tok = token_of_row(2 * t), v_odd = token_of_row(2 * t + 1) - v_tok;
-    #ifndef KV_HB
-#define KV_HB 2
-#endif
-    constexpr int HB = NT == 1 ? KV_HB : 1;  // 16-token halves in flight at once
+        constexpr int HB = NT == 1 ? kUnit / 16 : 1;  // 16-token halves in flight at once
 
     // four consecutive elements of row c of an item's query tile
     auto query = [&](const Item& x, int c) {
