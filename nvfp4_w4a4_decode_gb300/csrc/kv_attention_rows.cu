@@ -679,80 +679,97 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             // ---- join the CTAs: the last to arrive sums all parts in CTA order ----------------
             const int ca = Work::first_cta(sh, it), cb = Work::last_cta(sh, it);
             if (tid == 0) {
-                __threadfence();  // the CTA's writes (the barrier above orders them before)
-                const unsigned seen = atomicAdd(a.count + ca, 1u);
+                // releases the CTA's writes (the barrier above orders them before) and,
+                // for the last to arrive, acquires the others'
+                unsigned seen;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                             : "=r"(seen) : "l"(a.count + ca) : "memory");
                 last_s = seen == (unsigned)(cb - ca);
                 if (last_s)
                     a.count[ca] = 0u;
-                __threadfence();
             }
             compute_sync();
             if (last_s) {
-                // references and sums of column `col` of part c
-                auto ml = [&](int c) {
-                    return a.part + (2 * c + (c == ca)) * kPart + (int64_t)NT * kFrag * 4;
-                };
-                // over all parts, kStep threads a column, joined in order
+                // part c's entries, then references [R] and sums [R]
+                auto part_of = [&](int c) { return a.part + (2 * c + (c == ca)) * kPart; };
+                constexpr int64_t kMl = (int64_t)NT * kFrag * 4;
+                // a thread a (column, part) of up to kStep parts at a time
                 constexpr int kStep = kCompute / R;
-                float* scratch = reinterpret_cast<float*>(red);
-                const int col = tid % R, k0 = tid / R;
-                float mt = -INFINITY;
-                for (int c = ca + k0; c <= cb; c += kStep)
-                    mt = fmaxf(mt, __ldcg(ml(c) + col));
-                scratch[tid] = mt;
-                compute_sync();
-                for (int k = 0; k < kStep; ++k)
-                    mt = fmaxf(mt, scratch[k * R + col]);
-                float lt = 0.f;
-                for (int c = ca + k0; c <= cb; c += kStep) {
-                    const float mc = __ldcg(ml(c) + col);
-                    lt += __ldcg(ml(c) + R + col) * (mc == mt ? 1.f : ex2(mc - mt));
-                }
-                compute_sync();
-                scratch[tid] = lt;
-                if (tid < R)
-                    sm_f[col] = mt;
-                compute_sync();
-                if (tid < R) {
-                    lt = scratch[col];
-                    for (int k = 1; k < kStep; ++k)
-                        lt += scratch[k * R + col];
-                    sm_sum[col] = lt;
-                    store_lse(col, mt, lt);
-                }
-                // the parts, as many at a time as their factors fit
-                constexpr int kPiece = C::kRedBytes / (4 * R);
                 constexpr int kOwn = (NT * kFrag + kCompute - 1) / kCompute;
+                float* scratch = reinterpret_cast<float*>(red);       // [kStep][R] references
+                float* factor = scratch + kCompute;                   // [kStep][R] factors
+                float* summed = factor + kCompute;                    // [kStep][R] sums
+                static_assert(3 * kCompute * 4 <= C::kRedBytes, "the join's tables");
+                const int col = tid % R, k0 = tid / R;
+                float mt = -INFINITY, lt = 0.f;  // so far, of column col
                 float4 v[kOwn];
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j)
                     v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c0 = ca; c0 <= cb; c0 += kPiece) {
-                    const int n = min(kPiece, cb - c0 + 1);
-                    compute_sync();
-                    for (int k = tid; k < n * R; k += kCompute) {
-                        const float mc = __ldcg(ml(c0 + k / R) + k % R), top = sm_f[k % R];
-                        scratch[k] = mc == top ? 1.f : ex2(mc - top);
+                for (int c0 = ca; c0 <= cb; c0 += kStep) {
+                    const int n = min(kStep, cb - c0 + 1);
+                    float mc = -INFINITY, lc = 0.f;
+                    if (k0 < n) {
+                        const float* ml = part_of(c0 + k0) + kMl + col;
+                        mc = __ldcg(ml);
+                        lc = __ldcg(ml + R);
                     }
+                    scratch[tid] = mc;
                     compute_sync();
+                    float top = mt;
+                    for (int k = 0; k < n; ++k)
+                        top = fmaxf(top, scratch[k * R + col]);
+                    const float by = mc == top ? 1.f : ex2(mc - top);
+                    factor[tid] = by;
+                    summed[tid] = by * lc;
+                    if (k0 == 0)  // what was joined so far, against the new reference
+                        sm_f[col] = mt == top ? 1.f : ex2(mt - top);
+                    compute_sync();
+                    lt *= mt == top ? 1.f : ex2(mt - top);
+                    for (int k = 0; k < n; ++k)
+                        lt += summed[k * R + col];
+                    mt = top;
 #pragma unroll
                     for (int j = 0; j < kOwn; ++j) {
-                        const int e = tid + j * kCompute;
-                        if (e >= NT * kFrag)
-                            break;
-                        const float* by = scratch + (e / kFrag) * 8 + 2 * (e & 3);
-#pragma unroll 4
-                        for (int k = 0; k < n; ++k) {
-                            const int c = c0 + k;
-                            const float4 o = __ldcg(
-                                reinterpret_cast<const float4*>(a.part + (2 * c + (c == ca)) * kPart) +
-                                e);
-                            const float b0 = by[k * R], b1 = by[k * R + 1];
-                            v[j].x = fmaf(o.x, b0, v[j].x), v[j].y = fmaf(o.y, b1, v[j].y);
-                            v[j].z = fmaf(o.z, b0, v[j].z), v[j].w = fmaf(o.w, b1, v[j].w);
-                        }
+                        const int c2 = ((tid + j * kCompute) / kFrag) * 8 + 2 * (tid & 3);
+                        const float o0 = c2 < R ? sm_f[c2] : 0.f, o1 = c2 < R ? sm_f[c2 + 1] : 0.f;
+                        v[j].x *= o0, v[j].y *= o1, v[j].z *= o0, v[j].w *= o1;
                     }
+                    // kAhead parts' entries on their way at once
+                    constexpr int kAhead = kOwn <= 2 ? 8 : 2;
+                    for (int k = 0; k < n; k += kAhead) {
+                        float4 o[kAhead][kOwn];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                            for (int j = 0; j < kOwn; ++j) {
+                                const int e = tid + j * kCompute;
+                                o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (k + i < n && e < NT * kFrag)
+                                    o[i][j] = __ldcg(
+                                        reinterpret_cast<const float4*>(part_of(c0 + k + i)) + e);
+                            }
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                            for (int j = 0; j < kOwn; ++j) {
+                                const int e = tid + j * kCompute;
+                                if (k + i < n && e < NT * kFrag) {
+                                    const float* by = factor + (k + i) * R + (e / kFrag) * 8 + 2 * (e & 3);
+                                    v[j].x = fmaf(o[i][j].x, by[0], v[j].x);
+                                    v[j].y = fmaf(o[i][j].y, by[1], v[j].y);
+                                    v[j].z = fmaf(o[i][j].z, by[0], v[j].z);
+                                    v[j].w = fmaf(o[i][j].w, by[1], v[j].w);
+                                }
+                            }
+                    }
+                    compute_sync();  // the tables are free
                 }
+                if (k0 == 0) {
+                    sm_sum[col] = lt;
+                    store_lse(col, mt, lt);
+                }
+                compute_sync();
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) {
                     const int e = tid + j * kCompute, f = e % kFrag;

@@ -286,12 +286,100 @@ struct KvWork {
         int r;
     };
 
+    // The share of this CTA, of a list of `total` places; false when it is empty.
+    static __device__ __forceinline__ bool cut_share(const KvAttnArgs& a, int64_t total, int64_t least,
+                                                     KvShare& sh)
+    {
+        sh.size = max(kv_divide(total + gridDim.x - 1, gridDim.x), least);
+        sh.lo = sh.size * blockIdx.x;
+        sh.hi = min(sh.lo + sh.size, total);
+        sh.cut = a.part != nullptr;
+        return sh.lo < total;
+    }
+
+    // The item at place sh.lo, `rem` places into request `it.r` (it.q, it.rows and
+    // the request's places of a head are known); then the first with a unit.
+    static __device__ __forceinline__ bool locate(const KvAttnArgs& a, const KvShare& sh, KvItem& it,
+                                                  int64_t rem, int64_t head)
+    {
+        it.begin = sh.lo - rem;
+        it.h = (int)kv_divide(rem, head);
+        it.begin += it.h * head;
+        it.tile = 0;
+        const int tiles = (it.rows + R - 1) / R, lane = threadIdx.x & 31;
+        for (int t0 = 0; tiles > 1 && t0 < tiles; t0 += 32) {  // 32 tiles at a time
+            int32_t first, n = 0;
+            const int t = t0 + lane;
+            if (t < tiles) {
+                tile_units(a, it.q, t * R, min(t * R + R, it.rows), first, n);
+                n += COST;
+            }
+            int32_t sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d)
+                    sum += o;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, it.begin + sum <= sh.lo);
+            const int skip = __popc(past);  // whole tiles before sh.lo
+            if (skip < 32) {
+                it.tile = t0 + skip;
+                it.begin += skip ? __shfl_sync(0xFFFFFFFFu, sum, skip - 1) : 0;
+                break;
+            }
+            it.begin += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        units(a, it);
+        return settle(a, sh, it, true);
+    }
+
+    // Up to 32 requests of few tiles: every warp finds the share by itself, a lane a
+    // request, without a barrier (the CTA-wide form took 3 of a single request's 12 us).
+    static __device__ __forceinline__ bool start_warp(const KvAttnArgs& a, int64_t least, KvShare& sh,
+                                                      KvItem& it)
+    {
+        const int lane = threadIdx.x & 31;
+        KvReq q = {0, 0, 0};
+        int64_t head = 0;
+        if (lane < a.reqs) {
+            q = kv_req(a, lane);
+            head = head_places(a, q, 0, 1);
+            if (blockIdx.x == 0 && kv_too_long(a, lane))
+                atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
+        }
+        const int64_t mine = a.c.heads * head;
+        int64_t inc = mine;
+        for (int d = 1; d < a.reqs; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            if (lane >= d)
+                inc += o;
+        }
+        if (!cut_share(a, __shfl_sync(0xFFFFFFFFu, inc, a.reqs - 1), least, sh))
+            return false;
+        // the first request that ends behind sh.lo
+        const uint32_t behind = __ballot_sync(0xFFFFFFFFu, lane < a.reqs && inc > sh.lo);
+        it.r = __ffs(behind) - 1;
+        const int64_t rem = sh.lo - __shfl_sync(0xFFFFFFFFu, inc - mine, it.r);
+        head = __shfl_sync(0xFFFFFFFFu, head, it.r);
+        it.q.seq = __shfl_sync(0xFFFFFFFFu, q.seq, it.r);
+        it.q.base = __shfl_sync(0xFFFFFFFFu, q.base, it.r);
+        it.q.nq = __shfl_sync(0xFFFFFFFFu, q.nq, it.r);
+        it.rows = it.q.nq * a.group;
+        return locate(a, sh, it, rem, head);
+    }
+
     // The whole CTA (THREADS threads) computes its share of the list and the
     // first item with a unit in it; false when there is none.
     template <int THREADS>
     static __device__ bool start(const KvAttnArgs& a, Smem& sm, int64_t least, KvShare& sh,
                                  KvItem& it)
     {
+        if (a.reqs <= 32 && (int64_t)a.tokens * a.group <= 4 * R * (int64_t)a.reqs) {
+            const bool more = start_warp(a, least, sh, it);
+            __syncthreads();  // what the caller initialised
+            return more;
+        }
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         // few requests of many tiles: a warp sums a request; else a thread a run of them
         const bool by_warp = a.reqs <= 256 && (int64_t)a.tokens * a.group > 2 * (int64_t)R * a.reqs;
@@ -332,11 +420,7 @@ struct KvWork {
                 before += sm.warp_sum[w];
             total += sm.warp_sum[w];
         }
-        sh.size = max(kv_divide(total + gridDim.x - 1, gridDim.x), least);
-        sh.lo = sh.size * blockIdx.x;
-        sh.hi = min(sh.lo + sh.size, total);
-        sh.cut = a.part != nullptr;
-        if (sh.lo >= total)
+        if (!cut_share(a, total, least, sh))
             return false;
         if (sh.lo >= before && sh.lo < before + mine) {
             int64_t at = before;
@@ -351,39 +435,9 @@ struct KvWork {
             }
         }
         __syncthreads();
-        it.begin = sh.lo - sm.rem;
         if (!request(a, it, sm.r))
             return false;
-        // the head, then the tile, that holds place sh.lo; 32 tiles at a time
-        const int64_t head = places_of_head(a, it.q);
-        it.h = (int)kv_divide(sm.rem, head);
-        it.begin += it.h * head;
-        const int tiles = (it.rows + R - 1) / R;
-        for (int t0 = 0; t0 < tiles; t0 += 32) {
-            int32_t first, n = 0;
-            const int t = t0 + lane;
-            if (t < tiles) {
-                tile_units(a, it.q, t * R, min(t * R + R, it.rows), first, n);
-                n += COST;
-            }
-            int32_t sum = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int32_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-                if (lane >= d)
-                    sum += o;
-            }
-            const uint32_t past = __ballot_sync(0xFFFFFFFFu, it.begin + sum <= sh.lo);
-            const int skip = __popc(past);  // whole tiles before sh.lo
-            if (skip < 32) {
-                it.tile = t0 + skip;
-                it.begin += skip ? __shfl_sync(0xFFFFFFFFu, sum, skip - 1) : 0;
-                break;
-            }
-            it.begin += __shfl_sync(0xFFFFFFFFu, sum, 31);
-        }
-        units(a, it);
-        return settle(a, sh, it, true);
+        return locate(a, sh, it, sm.rem, places_of_head(a, it.q));
     }
 
 private:
