@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
 {
     using C = Cfg<D, NT, SPLIT>;
     constexpr int R = C::R, KS = C::KS, ST = C::kStages;
-    using Work = KvWork<R, kGroup, kItemCost>;
+    using Work = KvWork<R, kGroup, kItemCost, 4>;
     using Item = KvItem;
     using Share = KvShare;
     extern __shared__ __align__(128) uint8_t smem[];

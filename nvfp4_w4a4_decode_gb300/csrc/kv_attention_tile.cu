@@ -54,7 +54,7 @@ constexpr float kRaise = 8.0f;             // log2 a score may pass the referenc
 constexpr float kLift = 7.0f;              // p = 2^(s - m + kLift)
 constexpr uint32_t kColS = 0, kColO = 256;  // scores and outputs, 128 columns a tile
 
-using Work = KvWork<kRows, kKeys, kItemCost>;
+using Work = KvWork<kRows, kKeys, kItemCost, 2>;
 
 template <int D>
 struct Cfg {

@@ -154,13 +154,16 @@ struct KvItem {
     int32_t u0, u1;  // the units of this CTA's share
 };
 
-// A CTA's share of the list, and whether items may be cut between shares.
+// A CTA's share of the list.  Items of up to `least` units are not cut between
+// shares: joining their parts would take longer than the units do.
 struct KvShare {
     int64_t lo, hi, size;
-    bool cut;
+    int32_t least;
+    bool cut;  // longer items may be
 };
 
-template <int R, int UT, int COST>
+// Items of up to WHOLE units, or an eighth of a share, stay whole.
+template <int R, int UT, int COST, int WHOLE>
 struct KvWork {
     // Units [first, first + n) of the rows [row0, row1) of a request.
     static __device__ __forceinline__ void tile_units(const KvAttnArgs& a, const KvReq& q, int row0,
@@ -227,12 +230,12 @@ struct KvWork {
             const int64_t at = it.begin + COST;  // place of unit 0
             if (at >= s.hi)
                 return false;
-            if (s.cut) {
+            if (s.cut && it.n > s.least) {
                 it.u0 = (int32_t)max((int64_t)0, s.lo - at);
                 it.u1 = (int32_t)min((int64_t)it.n, s.hi - at);
                 if (it.u0 < it.u1)
                     return true;
-            } else {  // an uncut item belongs to the share that holds its unit 0
+            } else {  // a whole item belongs to the share that holds its unit 0
                 it.u0 = 0;
                 it.u1 = it.n;
                 if (at >= s.lo)
@@ -294,6 +297,7 @@ struct KvWork {
         sh.lo = sh.size * blockIdx.x;
         sh.hi = min(sh.lo + sh.size, total);
         sh.cut = a.part != nullptr;
+        sh.least = (int32_t)min(max((int64_t)WHOLE, sh.size >> 3), (int64_t)INT32_MAX);
         return sh.lo < total;
     }
 
