@@ -1,7 +1,10 @@
 """Build step of the CUDA library: compiles ``csrc/*.cu`` for sm_103a with
 nvcc (one process per translation unit, in parallel) and links
 ``libnvfp4_gb300.so`` next to this file.  No CMake, no torch extension
-machinery: the library is plain C ABI + CUDA."""
+machinery: the library is plain C ABI + CUDA.  ``csrc/kv_binding.cpp`` (argument
+checks and output tensors of the paged cache's calls) becomes a Python
+extension module of its own, ``_kv_binding.so``, compiled by the host compiler
+against torch's headers."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -9,11 +12,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4_gb300.so")
+BINDING = os.path.join(HERE, "_kv_binding.so")
+BINDING_SRC = os.path.join(CSRC, "kv_binding.cpp")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,11 +43,33 @@ def _deps():
         sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _fresh(made, deps) -> bool:
+    if not os.path.exists(made):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(made)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def up_to_date() -> bool:
+    return _fresh(LIB, _deps()) and _fresh(
+        BINDING, [BINDING_SRC, *sorted(glob.glob(os.path.join(INCLUDE, "*.h")))])
+
+
+def _compile_binding():
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    lib, inc = os.path.join(root, "lib"), os.path.join(root, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SRC, "-o", tmp,
+           "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {BINDING_SRC} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -61,8 +89,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

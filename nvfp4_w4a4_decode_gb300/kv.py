@@ -1,8 +1,12 @@
 """Python binding of the paged NVFP4 key/value cache (``include/nvfp4_kv.h``):
-``kv_tables``, ``kv_append`` and ``kv_attention`` over a ``KVCache``."""
+``kv_tables``, ``kv_append`` and ``kv_attention`` over a ``KVCache``.  The checks
+of their arguments and their output tensors are made in ``csrc/kv_binding.cpp``."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 from collections import namedtuple
 
@@ -37,52 +41,34 @@ _CACHE = struct.Struct("@PPPqqiii4x")
 _ATTENTION = struct.Struct("@PqqPqqPPqqqfqPqP")
 
 
-from . import (FLAG_PDL, FLAG_X_BF16, FLAG_Y_BF16, KERNEL_AUTO, Nvfp4Error,  # noqa: E402
-               library)
+from . import FLAG_PDL, KERNEL_AUTO, Nvfp4Error, library  # noqa: E402
+from . import build as _build  # noqa: E402
 
 
-# The checks run before every call of a decode step, so they read each tensor's
-# properties once and in their cheapest form (get_device() is -1 on the host).
+_calls = None
 
-def _vector(t, dtype, name, dev, n=-1):
-    """Checks a contiguous vector (of n elements) on CUDA device index dev; its address."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor (device {dev})")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or not t.is_contiguous() or (n >= 0 and t.numel() != n):
-        raise ValueError(f"{name} must be a contiguous vector" + (f" of {n}" if n >= 0 else ""))
+
+def _binding():
+    """The compiled half of this module, bound to the library (raises if either is not built)."""
+    global _calls
+    if _calls is None:
+        lib = library()
+        if not os.path.exists(_build.BINDING):
+            raise ImportError(f"{_build.BINDING} is not built; run nvfp4_w4a4_decode_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_kv_binding", _build.BINDING)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_kv_binding", _build.BINDING, loader=loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.nvfp4_kv_tables, lib.nvfp4_kv_append, lib.nvfp4_kv_attention)), Nvfp4Error)
+        _calls = module
+    return _calls
+
+
+def _scale(t, name, dev):
+    if t.get_device() != dev or t.dtype is not torch.float32 or t.numel() != 1:
+        raise ValueError(f"{name} must be one float32 on CUDA device {dev}")
     return t.data_ptr()
-
-
-def _table(t, rows, dev):
-    """(address, row stride, entries a row) of a block table whose rows are contiguous."""
-    if t.get_device() != dev or t.dtype is not torch.int32:
-        raise ValueError(f"block_table must be an int32 tensor on device {dev}")
-    if t.dim() != 2:
-        raise ValueError(f"block_table must be [{rows}, blocks]")
-    n, blocks = t.shape
-    step, one = t.stride()
-    if n != rows or (blocks > 1 and one != 1) or (rows > 1 and step < blocks):
-        raise ValueError(f"block_table must be [{rows}, blocks] with contiguous rows")
-    return t.data_ptr(), (step if rows > 1 else blocks), blocks
-
-
-def _heads(t, name, dev, dim):
-    """(tokens, heads, token stride) of [tokens, heads, dim] with contiguous token rows."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor (device {dev})")
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, {dim}]")
-    tokens, heads, d = t.shape
-    step, head, one = t.stride()
-    if d != dim:
-        raise ValueError(f"{name} must be [tokens, heads, {dim}]")
-    if one != 1 or (heads > 1 and head != dim) or (tokens > 1 and step < heads * dim):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return tokens, heads, (step if tokens > 1 else heads * dim)
 
 
 def nvfp4_kv_page_bytes(page_size: int, num_kv_heads: int, head_dim: int) -> int:
@@ -128,8 +114,7 @@ class KVCache:
         self.page_size, self.head_dim = int(page_size), int(head_dim)
         self.device, self._dev = pool.device, pool.get_device()
         self._desc = _CACHE.pack(
-            pool.data_ptr(), _vector(k_g, torch.float32, "k_g", self._dev, 1),
-            _vector(v_g, torch.float32, "v_g", self._dev, 1), pages,
+            pool.data_ptr(), _scale(k_g, "k_g", self._dev), _scale(v_g, "v_g", self._dev), pages,
             pool.stride(0) if pages > 1 else want, page_size, heads, head_dim)
         self._workspaces = {}
 
@@ -162,6 +147,8 @@ def _raw_stream(dev: int) -> int:
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
+_OUT = {None: 0, torch.float32: 1, torch.bfloat16: 2}
+
 KVTables = namedtuple("KVTables", "seq_len q_start slots positions free_head")
 
 
@@ -177,51 +164,19 @@ def nvfp4_kv_tables(kv_len, q_len, free_pages, free_head, block_table, page_size
     [reqs + 1], slots [tokens] int64, positions [tokens], free_head [1])``,
     the last being the free list's next head.  A free list or table that is
     too short sets DEVICE_KV_RANGE in ``device_status()``."""
-    dev, reqs = kv_len.get_device(), kv_len.numel()
-    p_len = _vector(kv_len, torch.int32, "kv_len", dev)
-    p_new = _vector(q_len, torch.int32, "q_len", dev, reqs)
-    p_free = _vector(free_pages, torch.int32, "free_pages", dev)
-    p_head = _vector(free_head, torch.int32, "free_head", dev, 1)
-    tp, ts, blocks = _table(block_table, reqs, dev)
-    if out is None:
-        at = kv_len.device
-        seq = torch.empty(reqs, dtype=torch.int32, device=at)
-        start = torch.empty(reqs + 1, dtype=torch.int32, device=at)
-        slots = torch.empty(tokens, dtype=torch.int64, device=at)
-        positions = torch.empty(tokens, dtype=torch.int32, device=at)
-        head = torch.empty(1, dtype=torch.int32, device=at)
-        out = KVTables(seq, start, slots, positions, head)
-        outs = (seq.data_ptr(), start.data_ptr(), slots.data_ptr(), positions.data_ptr(), tokens,
-                head.data_ptr())
-    else:
-        outs = (_vector(out.seq_len, torch.int32, "seq_len", dev, reqs),
-                _vector(out.q_start, torch.int32, "q_start", dev, reqs + 1),
-                _vector(out.slots, torch.int64, "slots", dev, tokens),
-                _vector(out.positions, torch.int32, "positions", dev, tokens), tokens,
-                _vector(out.free_head, torch.int32, "free_head", dev, 1))
-    status = library().nvfp4_kv_tables(p_len, p_new, reqs, page_size, p_free, free_pages.numel(),
-                                       p_head, tp, ts, blocks, *outs, FLAG_PDL if pdl else 0,
-                                       _stream(dev))
-    if status:
-        raise Nvfp4Error("nvfp4_kv_tables", status)
-    return out
+    dev = kv_len.get_device()
+    made = (_calls or _binding()).tables(
+        kv_len, q_len, free_pages, free_head, block_table, page_size, tokens, out,
+        FLAG_PDL if pdl else 0, _stream(dev) if dev >= 0 else 0)
+    return tuple.__new__(KVTables, made) if out is None else out
 
 
 def nvfp4_kv_append(cache: KVCache, k, v, slots, pdl: bool = False) -> None:
     """Quantise keys and values [tokens, num_kv_heads, head_dim] (float32 or
     bfloat16; slices of a projection's rows need no copy) into the cache at
     ``slots`` int64 [tokens] (-1: skipped)."""
-    dev = cache._dev
-    tokens, heads, ks = _heads(k, "k", dev, cache.head_dim)
-    vtokens, vheads, vs = _heads(v, "v", dev, cache.head_dim)
-    if heads != cache.num_kv_heads or vheads != heads or vtokens != tokens or k.dtype is not v.dtype:
-        raise ValueError(f"k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}] of one dtype")
-    status = library().nvfp4_kv_append(
-        cache._desc, k.data_ptr(), ks, v.data_ptr(), vs, tokens,
-        _vector(slots, torch.int64, "slots", dev, tokens),
-        (FLAG_PDL if pdl else 0) | (FLAG_X_BF16 if k.dtype is torch.bfloat16 else 0), _stream(dev))
-    if status:
-        raise Nvfp4Error("nvfp4_kv_append", status)
+    (_calls or _binding()).append(cache._desc, cache._dev, k, v, slots, FLAG_PDL if pdl else 0,
+                                  _stream(cache._dev))
 
 
 def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
@@ -241,49 +196,20 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     for this stream; False: none, long requests are then not cut).  Output
     float32 or bfloat16 (``out_dtype``, by default q's); with ``return_lse``
     also the natural-log sums [tokens, num_q_heads] float32."""
-    dev, dim = cache._dev, cache.head_dim
-    tokens, heads, qs = _heads(q, "q", dev, dim)
-    reqs = seq_len.numel()
-    p_seq = _vector(seq_len, torch.int32, "seq_len", dev)
-    if q_start is not None:
-        p_start = _vector(q_start, torch.int32, "q_start", dev, reqs + 1)
-    else:
-        p_start = 0
-        if reqs and tokens % reqs:
-            raise ValueError("without q_start every request has the same number of rows")
-    if heads % cache.num_kv_heads:
-        raise ValueError(f"{heads} query heads do not share {cache.num_kv_heads} kv heads")
-    tp, ts, blocks = _table(block_table, reqs, dev)
-    if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=out_dtype or q.dtype, device=cache.device)
-        os_ = heads * dim
-        if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
-            raise ValueError(f"the output must be float32 or bfloat16, got {out.dtype}")
-    else:
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        os_ = _heads(out, "out", dev, dim)[2]
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device) if return_lse else None
-    stream = _stream(dev)
+    stream = _stream(cache._dev)
     if workspace is None:
-        wp, wn, _keep = cache._workspace(stream)
+        wp, wn, _keep = cache._workspaces.get(stream) or cache._workspace(stream)
     elif workspace is False:
         wp = wn = 0
     else:
-        wp, wn = _vector(workspace, torch.uint8, "workspace", dev), workspace.numel()
-    if max_q is None:
-        max_q = tokens if q_start is not None else (tokens // reqs if reqs else 0)
-    args = _ATTENTION.pack(
-        q.data_ptr(), qs, heads, tp, ts, blocks, p_seq, p_start, reqs, tokens, max_q,
-        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), os_,
-        lse.data_ptr() if return_lse else 0)
-    status = library().nvfp4_kv_attention(
-        cache._desc, args,
-        kernel | (FLAG_PDL if pdl else 0) | (FLAG_X_BF16 if q.dtype is torch.bfloat16 else 0)
-        | (FLAG_Y_BF16 if out.dtype is torch.bfloat16 else 0), wp, wn, stream)
-    if status:
-        raise Nvfp4Error("nvfp4_kv_attention", status)
-    return (out, lse) if return_lse else out
+        if workspace.get_device() != cache._dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on CUDA device {cache._dev}")
+        wp, wn = workspace.data_ptr(), workspace.nbytes
+    if out_dtype not in _OUT:
+        raise ValueError(f"the output must be float32 or bfloat16, got {out_dtype}")
+    return (_calls or _binding()).attention(
+        cache._desc, cache._dev, q, block_table, seq_len, q_start, max_q, scale, window, out,
+        _OUT[out_dtype], return_lse, kernel | FLAG_PDL if pdl else kernel, wp, wn, stream)
 
 
 kv_page_bytes = nvfp4_kv_page_bytes

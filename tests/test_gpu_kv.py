@@ -629,3 +629,50 @@ def test_append_many_tokens(nv, tokens):
     for i in range(0, tokens, 1000):
         nv.kv_append(b, k[i:i + 1000].float().contiguous(), v[i:i + 1000].float().contiguous(), slots[i:i + 1000])
     assert torch.equal(pool_a, pool_b)
+
+
+# ---- what the binding refuses ------------------------------------------------------------
+
+def test_binding_refusals(nv):
+    cache, table, gen = filled(nv, [20, 9], 2, 64, 16)
+    q = torch.randn((2, 8, 64), generator=gen, device="cuda")
+    lens = ints([20, 9])
+    ok = dict(cache=cache, q=q, block_table=table, seq_len=lens)
+    for change in (dict(q=q.half()), dict(q=q.cpu()), dict(q=q[0]), dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)),
+                   dict(q=q[:, :7]), dict(block_table=table.long()), dict(block_table=table[:1]),
+                   dict(block_table=table.T), dict(seq_len=lens.long()), dict(seq_len=lens[:1].cpu()),
+                   dict(q_start=lens), dict(q_start=ints([0, 1, 2], torch.int64)), dict(out=q[:1]),
+                   dict(out=q.half()), dict(out_dtype=torch.float16), dict(q=torch.cat([q, q[:1]])),
+                   dict(workspace=torch.zeros(100, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            nv.kv_attention(**{**ok, **change})
+    for change in (dict(window=-1), dict(scale=math.nan), dict(kernel=77)):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.kv_attention(**{**ok, **change})
+    with pytest.raises(TypeError):
+        nv.kv_attention(**{**ok, "scale": "x"})
+    k = torch.randn((3, 2, 64), device="cuda")
+    slots = torch.arange(3, device="cuda")
+    for args in ((k, k[:2], slots), (k, k.to(BF16), slots), (k, k, slots.to(torch.int32)), (k, k, slots[:2]),
+                 (k[:, :1], k[:, :1], slots), (k.transpose(0, 1), k, slots), (k.cpu(), k.cpu(), slots), (None, k, slots)):
+        with pytest.raises(ValueError):
+            nv.kv_append(cache, *args)
+    t = dict(kv_len=lens, q_len=lens, free_pages=lens, free_head=lens[:1], block_table=table, page_size=16, tokens=29)
+    for change in (dict(q_len=lens[:1]), dict(kv_len=lens.float()), dict(free_head=lens), dict(tokens=-1),
+                   dict(block_table=table[:1]), dict(free_pages=lens.cpu()), dict(out=(lens,) * 5)):
+        with pytest.raises(ValueError):
+            nv.kv_tables(**{**t, **change})
+    with pytest.raises(nv.Nvfp4Error):
+        nv.kv_tables(**{**t, "page_size": 20})
+    assert nv.device_status() == 0
+
+
+def test_tables_into_given_tensors(nv):
+    past, new, free = ints([5, 16]), ints([3, 1]), ints([7, 8, 9])
+    table = ints([[1, -1], [2, -1]])
+    first = nv.kv_tables(past, new, free, ints([0]), table, page_size=16, tokens=6)
+    out = nv.KVTables(*(torch.full_like(x, 77) for x in first))
+    again = nv.kv_tables(past, new, free, ints([0]), table, page_size=16, tokens=6, out=out)
+    assert again is out
+    for a, b in zip(first, out):
+        assert torch.equal(a, b)
