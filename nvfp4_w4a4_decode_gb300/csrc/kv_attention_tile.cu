@@ -12,27 +12,34 @@
 //   warps 0..3, 4..7   softmax of tile 0, 1, a thread a row: the queries into
 //                      shared memory, scores out of tensor memory, probabilities
 //                      back into it over the scores, at the end the output.  The
-//                      exponentials of 32 scores are taken against the reference
+//                      exponentials of 64 scores are taken against the reference
 //                      at hand, with their maximum as a by-product; only where
 //                      that passes the reference by 2^8 is it raised, what was
-//                      accumulated rescaled and the 32 scores done again
-//   warps 8..15        decode the cache, 16 tokens each: codes and scales of
+//                      accumulated rescaled and the 64 scores done again
+//   warps 8..11        decode the cache, 32 tokens each: codes and scales of
 //                      the next block of keys are loaded while this block's are
 //                      converted to f16 and written as 128-byte-swizzled tiles
-//   warp 16            one lane issues the MMAs: S = Q K^T (both operands in
+//   warp 12            one lane issues the MMAs: S = Q K^T (both operands in
 //                      shared memory) and O += P V (P in tensor memory, V in
 //                      shared memory with the head dim contiguous)
 // The two tiles alternate: while one's scores are in the softmax the other's
 // products run, and both use each decoded block, so the decode costs one pass
 // per 256 rows.  Keys of all items are one list cut into equal shares
 // (kv_work.cuh); items cut between CTAs are joined by the last to arrive, in CTA
-// order.  Bound by the tensor pipe and, close to it, the issue slots of the
-// softmax.
+// order.
+//
+// What bounds it: the chain scores -> exponentials -> probabilities of a tile
+// (about 2600 cycles a block beside the 1024 of its products, of which the other
+// tile's run meanwhile) and shared memory, which the products of both tiles and the
+// decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
+// cycles.  2048 queries of 32 heads on 32049 keys: 776 us, 1.34 PFLOP/s.
 //
 // Waits have clock budgets; when one runs out NVFP4_DEVICE_WAIT_TIMEOUT is set,
 // later waits are passed over, MMAs in flight are drained and tensor memory is
 // freed.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "formats.cuh"
 #include "kv_work.cuh"
@@ -47,9 +54,10 @@ constexpr int kRowsTile = 128;             // query rows of an MMA tile
 constexpr int kRows = 2 * kRowsTile;       // of an item
 constexpr int kKeys = 128;                 // keys of a block
 constexpr int kItemCost = 2;               // blocks that an item's start and end cost
-constexpr int kDecodeWarp = 8, kMmaWarp = 16;
-constexpr int kDecodeRows = 16;            // tokens of a block a decoding warp
-constexpr int kThreads = 544;
+constexpr int kDecodeWarp = 8, kMmaWarp = 12;
+constexpr int kDecodeRows = kKeys / (kMmaWarp - kDecodeWarp);  // tokens a decoding warp
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSpan = 64;                  // keys between two looks at the reference
 constexpr float kRaise = 8.0f;             // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;              // p = 2^(s - m + kLift)
 constexpr uint32_t kColS = 0, kColO = 256;  // scores and outputs, 128 columns a tile
@@ -157,6 +165,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v)
         "r"(v[14]), "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+        "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -217,8 +237,8 @@ struct Barriers {
     uint64_t drain;
 };
 
-// ---- warps 8..15: the cache to f16 ----------------------------------------------------
-// 16 tokens of a block a warp: a lane takes 32 elements (16 bytes of codes, two
+// ---- warps 8..11: the cache to f16 ----------------------------------------------------
+// 32 tokens of a block a warp: a lane takes 32 elements (16 bytes of codes, two
 // scales) of every kRpi-th row, neighbouring lanes neighbouring bytes.
 template <int D>
 struct Raw {
@@ -229,28 +249,28 @@ struct Raw {
     uint32_t s[kIters];
 };
 
-// The K or V rows of a warp's 16 tokens, which lie in one page (-1: nothing
-// there, the rows become zeros).
+// The K or V rows of a warp's tokens; page[i] holds the i-th 16 of them (-1:
+// nothing there, the rows become zeros).
 template <int D>
-__device__ __forceinline__ void load_rows(Raw<D>& x, const KvAttnArgs& a, int32_t page, int32_t tok0,
+__device__ __forceinline__ void load_rows(Raw<D>& x, const KvAttnArgs& a,
+                                          const int32_t (&page)[kDecodeRows / 16], int32_t tok0,
                                           int32_t seq, int h, bool is_v)
 {
     using X = Raw<D>;
     const int P = a.c.page_shift, lane = threadIdx.x & 31;
-    const int32_t off0 = tok0 & ((1 << P) - 1);
-    const uint8_t* p = a.c.pool + page * a.c.page_stride + h * kv_head_bytes(P, D);
-    const uint8_t* codes = p + (is_v ? (D / 2) << P : 0) + off0 * (D / 2) + lane * 16;
-    const uint8_t* scales =
-        p + (D << P) + (is_v ? (D / 16) << P : 0) + off0 * (D / 16) + lane * 2;
+    const int64_t part = h * kv_head_bytes(P, D);
+    const int64_t codes = part + (is_v ? (D / 2) << P : 0) + lane * 16;
+    const int64_t scales = part + (D << P) + (is_v ? (D / 16) << P : 0) + lane * 2;
 #pragma unroll
     for (int i = 0; i < X::kIters; ++i) {
-        const int row = i * X::kRpi + lane / X::kLanes;
-        const bool there = page >= 0 && tok0 + row < seq;
+        const int row0 = i * X::kRpi;  // rows row0 .. row0 + kRpi - 1 lie in one page
+        const int32_t pg = page[row0 / 16], off = (tok0 + row0) & ((1 << P) - 1);
         x.c[i] = make_uint4(0u, 0u, 0u, 0u);
         x.s[i] = 0u;
-        if (there) {
-            x.c[i] = __ldg(reinterpret_cast<const uint4*>(codes + i * 512));
-            x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + i * 64));
+        if (pg >= 0 && tok0 + row0 + lane / X::kLanes < seq) {
+            const uint8_t* p = a.c.pool + pg * a.c.page_stride;
+            x.c[i] = __ldg(reinterpret_cast<const uint4*>(p + codes + off * (D / 2)));
+            x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(p + scales + off * (D / 16)));
         }
     }
 }
@@ -474,76 +494,90 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     m = fmaxf(top[0], top[1]);
                     m = m == -INFINITY ? m : m * f - kLift;
                 }
+                // kSpan keys at a time (with a look at the reference every 32 a chunk of
+                // 2048 rows on 30000 keys took 858 us, every 64 776, every 128 784);
+                // blocks that every row of the warp sees whole skip the masks
+                auto exponentials = [&](auto masked) {
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
-                    uint32_t p16[16];
-                    float sum;
-                    // usually once; a second time when the reference had to be raised
+                    for (int h = 0; h < kKeys; h += kSpan) {
+                        uint32_t p16[kSpan / 2];
+                        float sum;
+                        // usually once; a second time when the reference had to be raised
 #pragma unroll 1
-                    for (int pass = 0;; ++pass) {
-                        // no key seen yet: every score is -inf, against any finite reference
-                        const float ref = m == -INFINITY ? 0.f : m;
-                        const uint64_t neg = pair(-ref, -ref);
-                        float top[2] = {-INFINITY, -INFINITY};
-                        uint64_t sums[2] = {0ull, 0ull};
-                        uint32_t s[32];
-                        tmem_ld32(tS + c, s);
-                        if (edge)
-                            hide(c, s);
+                        for (int pass = 0;; ++pass) {
+                            // no key seen yet: every score is -inf, against any finite reference
+                            const float ref = m == -INFINITY ? 0.f : m;
+                            const uint64_t neg = pair(-ref, -ref);
+                            float top[2] = {-INFINITY, -INFINITY};
+                            uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const uint64_t x = fma2(
-                                pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2, neg);
-                            float p0, p1;
-                            unpair(x, p0, p1);
-                            top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(p0, p1));
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], pair(p0, p1));
-                            p16[i / 2] = pack_f16(p0, p1);
-                        }
-                        float x0, x1;
-                        unpair(add2(sums[0], sums[1]), x0, x1);
-                        sum = x0 + x1;
-                        const float best = fmaxf(top[0], top[1]);  // against ref
-                        // (a row that has seen no key takes its first reference too)
-                        const bool raise =
-                            best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
-                        if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
-                            break;
-                        const float now = fmaxf(m, best + ref - kLift);
-                        const float by = m == now ? 1.f : ex2(m - now);
-                        m = now;
-                        l *= by;
-                        // The output so far (its products are complete: this block's scores
-                        // were issued after them, and their commit covers both) and this
-                        // block's probabilities so far, which lie over scores already used.
-                        tmem_wait_st();
-                        if (u > it.u0) {
+                            for (int c = 0; c < kSpan; c += 32) {
+                                uint32_t s[32];
+                                tmem_ld32(tS + h + c, s);
+                                if constexpr (masked)
+                                    hide(h + c, s);
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    const uint64_t x = fma2(pair(__uint_as_float(s[i]),
+                                                                 __uint_as_float(s[i + 1])), f2, neg);
+                                    float p0, p1;
+                                    unpair(x, p0, p1);
+                                    top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(p0, p1));
+                                    p0 = ex2(p0);
+                                    p1 = ex2(p1);
+                                    sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], pair(p0, p1));
+                                    p16[(c + i) / 2] = pack_f16(p0, p1);
+                                }
+                            }
+                            float x0, x1;
+                            unpair(add2(sums[0], sums[1]), x0, x1);
+                            sum = x0 + x1;
+                            const float best = fmaxf(top[0], top[1]);  // against ref
+                            // (a row that has seen no key takes its first reference too)
+                            const bool raise =
+                                best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
+                            if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
+                                break;
+                            const float now = fmaxf(m, best + ref - kLift);
+                            const float by = m == now ? 1.f : ex2(m - now);
+                            m = now;
+                            l *= by;
+                            // The output so far (its products are complete: this block's scores
+                            // were issued after them, and their commit covers both) and the
+                            // probabilities of the first half, over scores already used.
+                            tmem_wait_st();
+                            if (u > it.u0) {
 #pragma unroll 1
-                            for (int i = 0; i < D; i += 16) {
+                                for (int i = 0; i < D; i += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + i, o);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j)
+                                        o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+                                    tmem_st16(tO + i, o);
+                                }
+                            }
+                            const uint32_t by16 = pack_f16(by, by);
+#pragma unroll 1
+                            for (int i = 0; i < h / 2; i += 16) {
                                 uint32_t o[16];
-                                tmem_ld16(tO + i, o);
+                                tmem_ld16(tS + i, o);
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-                                tmem_st16(tO + i, o);
+                                    o[j] = f16x2_mul(o[j], by16);
+                                tmem_st16(tS + i, o);
                             }
                         }
-                        const uint32_t by16 = pack_f16(by, by);
-#pragma unroll 1
-                        for (int i = 0; i < c / 2; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(tS + i, o);
+                        l += sum;
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                o[j] = f16x2_mul(o[j], by16);
-                            tmem_st16(tS + i, o);
-                        }
+                        for (int i = 0; i < kSpan / 2; i += 32)
+                            tmem_st32(tS + h / 2 + i, p16 + i);
                     }
-                    l += sum;
-                    tmem_st16(tS + c / 2, p16);
-                }
+                };
+                if (__any_sync(0xFFFFFFFFu, edge))
+                    exponentials(std::true_type{});
+                else
+                    exponentials(std::false_type{});
                 tmem_wait_st();
                 fence_before();
                 warp_arrive(pfull);
@@ -659,20 +693,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             write_lse(mt, lt);
         }
     } else if (warp < kMmaWarp) {
-        // ---- decode: 16 tokens of a block a warp -------------------------------------------------
+        // ---- decode: 32 tokens of a block a warp -------------------------------------------------
         const int row0 = kDecodeRows * (warp - kDecodeWarp);
         bool bad = false;
         // a block's rows are loaded a block ahead, their page two
         Raw<D> k, v;
-        int32_t page = -1;
+        int32_t page[kDecodeRows / 16];
         auto look_up = [&](const KvItem& y, int32_t u) {
-            const int32_t tok = (y.first + u) * kKeys + row0, b = tok >> a.c.page_shift;
-            page = -1;
-            if (tok < y.q.seq && b < a.max_blocks) {
-                page = a.table[y.r * a.table_stride + b];
-                if (page < 0 || page >= a.c.num_pages) {
-                    bad = true;
-                    page = -1;
+#pragma unroll
+            for (int i = 0; i < kDecodeRows / 16; ++i) {
+                const int32_t tok = (y.first + u) * kKeys + row0 + 16 * i, b = tok >> a.c.page_shift;
+                page[i] = -1;
+                if (tok < y.q.seq && b < a.max_blocks) {
+                    page[i] = a.table[y.r * a.table_stride + b];
+                    if (page[i] < 0 || page[i] >= a.c.num_pages) {
+                        bad = true;
+                        page[i] = -1;
+                    }
                 }
             }
         };
@@ -724,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
     } else {
-        // ---- warp 16: the MMAs --------------------------------------------------------------------
+        // ---- warp 12: the MMAs --------------------------------------------------------------------
         uint32_t one;
         asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
