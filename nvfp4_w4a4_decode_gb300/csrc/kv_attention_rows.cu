@@ -53,7 +53,9 @@ constexpr int kWarps = 7;       // compute warps: with the copying warp eight, t
                                 // for each of the SM's four register files
 constexpr int kCompute = 32 * kWarps;
 constexpr int kThreads = kCompute + 32;
-constexpr int kItemCost = 2;    // groups that an item's start and end cost
+// Groups that an item's start and join cost (us for 24 requests of 1..6000 tokens, FP32
+// queries / three FP32 prompts: 1 25 / 72, 2 21 / 59, 5 20 / 45, 8 18.8 / 42, 12 20 / 44).
+constexpr int kItemCost = 8;
 constexpr int kMaxCtas = 512;   // workspace extent
 constexpr int kMaxRows = 32;
 constexpr float kRaise = 8.0f;  // log2 a score may pass the reference by
@@ -95,15 +97,16 @@ struct Cfg {
     static constexpr int KS = D / 16;            // k16 steps of Q K, m16 tiles of V
     static constexpr int kStageBytes = kGroup * D * 9 / 8;
     // two CTAs an SM where the registers allow it: the joins and starts of one
-    // overlap the other's stream
-    static constexpr int kCtas = NT == 1 && !SPLIT ? 2 : 1;
+    // overlap the other's stream (with FP32 terms that takes the queries out of
+    // registers and one half at a time: 24 ragged requests 25.9 -> 20.9 us)
+    static constexpr int kCtas = NT == 1 ? 2 : 1;
         static constexpr int kStages = 7;
     static constexpr int kQTerms = SPLIT ? 2 : 1;
     static constexpr int kQBytes = kQTerms * NT * KS * 32 * 8;
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kRedBytes = kWarps * KS * 32 * 16;
     static constexpr int kSmem = kRingBytes + kRedBytes + kQBytes;
-    static constexpr bool kQRegs = NT * kQTerms <= 2;  // queries held in registers
+    static constexpr bool kQRegs = NT <= 2 && !SPLIT;  // queries held in registers
     // A parity tells a phase from its neighbours only: a warp must see every
     // phase of the slots it reads.  Units are dealt by their number in the CTA's
     // whole sequence, so a unit's place in the ring always has the same warp.
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     const int code_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 2);
     const int scale_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 16);
     const int ka = token_of_row(g), v_tok = token_of_row(2 * t), v_odd = token_of_row(2 * t + 1) - v_tok;
-        constexpr int HB = NT == 1 ? kUnit / 16 : 1;  // 16-token halves in flight at once
+        constexpr int HB = NT == 1 && !SPLIT ? kUnit / 16 : 1;  // 16-token halves in flight at once
 
     // four consecutive elements of row c of an item's query tile
     auto query = [&](const Item& x, int c) {
