@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 s[h][nt][e] = 0.f;
+                        float rest[SPLIT ? NT : 1][4] = {};
                         uint32_t wa[D / 32], wb[D / 32];
                         uint32_t sa[D / 64], sb[D / 64];  // block scales of the two rows, doubled
                         if constexpr (D == 128) {
@@ -403,9 +404,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                                         const int j = (x * NT + nt) * KS + 2 * w + e;
                                         const uint2 b =
                                             C::kQRegs ? qf[C::kQRegs ? j : 0] : sq[j * 32 + lane];
-                                        mma_m16n8k16(s[h][nt], ha[2 * e], hb[2 * e], ha[2 * e + 1],
-                                                     hb[2 * e + 1], b.x, b.y);
+                                        // small terms (the queries' second) on their own
+                                        mma_m16n8k16(x ? rest[nt] : s[h][nt], ha[2 * e], hb[2 * e],
+                                                     ha[2 * e + 1], hb[2 * e + 1], b.x, b.y);
                                     }
+                        }
+                        if constexpr (SPLIT) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    s[h][nt][e] += rest[nt][e];
                         }
                     }
 
@@ -551,11 +560,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                                 const uint32_t a0 = f16x2_mul(e0[k], s01), a1 = f16x2_mul(o0[k], s01);
                                 const uint32_t a2 = f16x2_mul(e1[k], s23), a3 = f16x2_mul(o1[k], s23);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float(&o)[4] = acc[nt][4 * w + k];
+                                    if constexpr (SPLIT) {
+                                        // the MMA's own sums are cut off, not rounded: these 16
+                                        // tokens are summed alone and added in FP32
+                                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma_m16n8k16(sum, a0, a1, a2, a3, pb[h][1][nt][0], pb[h][1][nt][1]);
+                                        mma_m16n8k16(sum, a0, a1, a2, a3, pb[h][0][nt][0], pb[h][0][nt][1]);
 #pragma unroll
-                                    for (int y = 0; y < C::kQTerms; ++y)
-                                        mma_m16n8k16(acc[nt][4 * w + k], a0, a1, a2, a3,
-                                                     pb[h][y][nt][0], pb[h][y][nt][1]);
+                                        for (int e = 0; e < 4; ++e)
+                                            o[e] += sum[e];
+                                    } else {
+                                        mma_m16n8k16(o, a0, a1, a2, a3, pb[h][0][nt][0], pb[h][0][nt][1]);
+                                    }
+                                }
                             }
                         }
                     }
