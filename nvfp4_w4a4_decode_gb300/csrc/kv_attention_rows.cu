@@ -11,7 +11,12 @@
 // is raised only when a score passes it by more than 2^8 (any reference gives
 // the same quotient; p stays below 2^15 and f16 resolves 2^-31 of the largest),
 // row sums in FP32 from the unrounded p.  p goes into the second MMA as one
-// f16 (outputs in BF16) or two (FP32), against exact values.
+// f16 (outputs in BF16) or two (FP32), against exact values.  The tensor cores'
+// own accumulation truncates, which a chain of thousands of tokens would carry
+// into the sixth digit: with FP32 terms 16 tokens' products are summed alone and
+// added in FP32, and the queries' second terms have an accumulator of their own
+// (largest error of 24 requests of 1..6000 tokens: 4e-7 of the largest output,
+// from 0.8..2.1e-6, in the same time).
 //
 // Layout.  The query rows (token, head of the group) are the narrow side of
 // m16n8k16 tiles, 8 NT of them: S^T = K Q^T and O^T = V^T P^T, so a single
@@ -23,7 +28,7 @@
 // a token.  V's codes of two tokens are interleaved as nibbles before they are
 // converted, which gives the f16 pairs along the tokens that the MMA wants.
 //
-// Work.  One list of 64-token groups for all requests (kv.cuh), equal shares a
+// Work.  One list of 64-token groups for all requests (kv_work.cuh), equal shares a
 // CTA; the 32-token units of an item's groups are dealt to the CTA's seven
 // compute warps in turn.  An eighth warp runs ahead through the list, across
 // items: it looks up the pages and fills a ring of groups with bulk copies --
@@ -35,7 +40,13 @@
 // requests take equal time.  Every wait has a clock budget: one that runs out
 // sets NVFP4_DEVICE_WAIT_TIMEOUT and all waits after it are passed over.
 //
-// Bound by the cache's bytes for one token a request.
+// What bounds it: for many tokens the issue slots, about 335 warp instructions for 16
+// tokens of a kv head of 128, most of them conversions of codes and scales at
+// half rate, on 14 compute warps an SM (64 requests of 6000..8191 tokens, 8 kv
+// heads, a token each: 112 us, 4.5 TB/s of codes and scales; two of 100000..131071:
+// 60 us, 4.2 TB/s).  For few tokens the chain list - queries - units - join, about 9 us (one
+// request of 1000); a launch's fixed parts measured in cycles: list 2300, queries
+// 1700, first units 2800, warps' join 1400, part and counter 2000, CTAs' join 5000.
 #include "formats.cuh"
 #include "kv_work.cuh"
 #include "launch_cache.cuh"
@@ -100,13 +111,15 @@ struct Cfg {
     // overlap the other's stream (with FP32 terms that takes the queries out of
     // registers and one half at a time: 24 ragged requests 25.9 -> 20.9 us)
     static constexpr int kCtas = NT == 1 ? 2 : 1;
-        static constexpr int kStages = 7;
+    static constexpr int kStages = 7;
     static constexpr int kQTerms = SPLIT ? 2 : 1;
     static constexpr int kQBytes = kQTerms * NT * KS * 32 * 8;
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kRedBytes = kWarps * KS * 32 * 16;
     static constexpr int kSmem = kRingBytes + kRedBytes + kQBytes;
-    static constexpr bool kQRegs = NT <= 2 && !SPLIT;  // queries held in registers
+    // queries held in registers while the accumulators leave room (32 rows, or FP32
+    // terms, read them from shared memory at each use)
+    static constexpr bool kQRegs = NT <= 2 && !SPLIT;
     // A parity tells a phase from its neighbours only: a warp must see every
     // phase of the slots it reads.  Units are dealt by their number in the CTA's
     // whole sequence, so a unit's place in the ring always has the same warp.
@@ -154,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     const uint32_t ring = smem_u32(smem);
 
     if (warp == kWarps) {
-        // ---- the copying warp: four groups at a time, four lanes a group -----------------
+        // ---- the copying warp: kBatch groups at a time, four lanes a group ----------------
         // pages of up to 64 tokens: a piece is a page; longer ones: K codes, V
         // codes, K scales, V scales of the group's part of the page.  (One group
         // at a time took this warp about 800 cycles each, the SM's whole time
@@ -247,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     const int code_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 2);
     const int scale_step = bs == 4 ? 2 * whole_block : bs == 5 ? whole_block : kUnit * (D / 16);
     const int ka = token_of_row(g), v_tok = token_of_row(2 * t), v_odd = token_of_row(2 * t + 1) - v_tok;
-        constexpr int HB = NT == 1 && !SPLIT ? kUnit / 16 : 1;  // 16-token halves in flight at once
+    constexpr int HB = NT == 1 && !SPLIT ? kUnit / 16 : 1;  // 16-token halves in flight at once
 
     // four consecutive elements of row c of an item's query tile
     auto query = [&](const Item& x, int c) {

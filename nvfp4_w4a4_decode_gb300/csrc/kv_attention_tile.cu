@@ -32,7 +32,9 @@
 // (about 2600 cycles a block beside the 1024 of its products, of which the other
 // tile's run meanwhile) and shared memory, which the products of both tiles and the
 // decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
-// cycles.  2048 queries of 32 heads on 32049 keys: 776 us, 1.34 PFLOP/s.
+// cycles.  2048 queries of 32 heads on 32049 keys: 776 us, 1.34 PFLOP/s; four prompts of
+// 333..4096 tokens: 750 us, 0.91 PFLOP/s (an item adds 8 to 18 us of queries, first
+// decode and output to its keys).
 //
 // Waits have clock budgets; when one runs out NVFP4_DEVICE_WAIT_TIMEOUT is set,
 // later waits are passed over, MMAs in flight are drained and tensor memory is

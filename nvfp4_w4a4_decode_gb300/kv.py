@@ -23,7 +23,6 @@ DEVICE_KV_RANGE = 2
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
-_i32 = ctypes.c_int32
 _u32 = ctypes.c_uint32
 
 SIGNATURES = {
@@ -36,9 +35,7 @@ SIGNATURES = {
 }
 
 
-# nvfp4_kv_cache and nvfp4_kv_attention_args as native struct layouts
-_CACHE = struct.Struct("@PPPqqiii4x")
-_ATTENTION = struct.Struct("@PqqPqqPPqqqfqPqP")
+_CACHE = struct.Struct("@PPPqqiii4x")  # nvfp4_kv_cache
 
 
 from . import FLAG_PDL, KERNEL_AUTO, Nvfp4Error, library  # noqa: E402
@@ -94,10 +91,15 @@ class KVCache:
     (``kv_pool``) with contiguous pages; the pages themselves may be strided
     (one pool for several layers).  ``k_g`` / ``v_g`` are the tensor scales of
     keys and values ([1] float32, ``global_scale`` of calibration data).  The
-    tensors must stay alive and in place while the cache is used.
+    tensors must stay alive and in place while the cache is used, and the
+    cache as long as a graph that holds its calls.
 
-    Attention calls on a stream share a zeroed workspace that the cache makes
-    at the first of them (one per stream)."""
+    Attention calls on a stream share a workspace that the cache makes at the
+    first of them (17 MB for each stream used).  A call captured into a graph
+    keeps the workspace of the stream it is captured on, where that has one: a
+    graph that may run at the same time as other attention calls of that stream
+    takes its own (``workspace=kv_attention_workspace(...)``).  The caches of
+    several layers may be given the same one."""
 
     def __init__(self, pool, k_g, v_g, page_size: int, head_dim: int):
         if pool.get_device() < 0 or pool.dtype is not torch.uint8 or pool.dim() != 3:

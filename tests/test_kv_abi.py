@@ -1,11 +1,15 @@
 """The paged NVFP4 cache's entry points refuse what they cannot take, on the
 host, before any launch.  CPU only: the calls below never reach a kernel."""
+import struct
+
 import pytest
 import torch
 
 import nvfp4_w4a4_decode_gb300 as nv
 from nvfp4_w4a4_decode_gb300 import build as nvbuild
-from nvfp4_w4a4_decode_gb300.kv import _ATTENTION, _CACHE
+from nvfp4_w4a4_decode_gb300.kv import _CACHE
+
+_ATTENTION = struct.Struct("@PqqPqqPPqqqfqPqP")  # nvfp4_kv_attention_args
 
 FAKE = 1 << 20  # a non-null, aligned value never dereferenced
 OK, INVALID, UNSUPPORTED = 0, 1, 2
