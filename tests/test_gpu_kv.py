@@ -676,3 +676,21 @@ def test_tables_into_given_tensors(nv):
     assert again is out
     for a, b in zip(first, out):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("reqs,tokens", [(1, 1), (3, 0), (5, 7), (8, 33)])
+def test_tables_outputs_are_separate(nv, reqs, tokens):
+    past, new = ints([4] * reqs), ints([1] * reqs)
+    table = torch.full((reqs, 2), 3, dtype=torch.int32, device="cuda")
+    got = nv.kv_tables(past, new, ints([7]), ints([0]), table, page_size=16, tokens=max(tokens, reqs))
+    sizes = [reqs, reqs + 1, max(tokens, reqs), max(tokens, reqs), 1]
+    for i, (t, n) in enumerate(zip(got, sizes)):
+        assert t.shape == (n,) and t.is_contiguous() and t.data_ptr() % 16 == 0
+        assert t.dtype == (torch.int64 if i == 2 else torch.int32)
+        t.fill_(-100 - i)                                  # each has its own bytes
+    for i, t in enumerate(got):
+        assert (t == -100 - i).all()
+    kept = got.positions
+    del got
+    other = torch.zeros(1 << 12, dtype=torch.int32, device="cuda")  # takes freed memory, if there is any
+    assert (kept == -103).all() and (other == 0).all()
