@@ -71,7 +71,8 @@ using Work = KvWork<kRows, kKeys, kItemCost, 2>;
 template <int D>
 struct Cfg {
     static constexpr int kTile = kKeys * D * 2;                  // bytes of a K, V or Q tile
-    static constexpr size_t kSmem = (size_t)6 * kTile + 1024;    // Q 2, K 2, V 2, alignment
+    static constexpr int kStage = kRows * 64;                    // 32 outputs a row on their way
+    static constexpr size_t kSmem = (size_t)6 * kTile + kStage + 1024;  // Q 2, K 2, V 2, alignment
     static constexpr int64_t kPart = (int64_t)(D + 2) * kRowsTile;  // floats of a partial tile
 };
 
@@ -362,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
         const uint32_t qfull = smem_u32(&bars.qfull[st]), sfull = smem_u32(&bars.sfull[st]),
                        pfull = smem_u32(&bars.pfull[st]), ofull = smem_u32(&bars.ofull[st]);
-        uint8_t* tile = smem + st * C::kTile;  // the queries; at the end the outputs
+        uint8_t* tile = smem + st * C::kTile;                    // the queries
+        uint8_t* staged = smem + 6 * C::kTile + warp * (32 * 64);  // the warp's outputs
         constexpr int kRowLanes = D / 4, kRowsAtOnce = 32 / kRowLanes;  // 8 bytes a lane
         const int my_part = lane % kRowLanes, my_row = lane / kRowLanes;
         // a negative factor goes into the queries' signs, so that larger scores are
@@ -370,88 +372,103 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         const float vg = a.c.v_g[0], signed_qk = a.scale_log2 * a.c.k_g[0], qk = fabsf(signed_qk);
         const uint32_t flip = signed_qk < 0.f ? 0x80008000u : 0u;
         uint32_t blocks = 0, items = 0;  // this tile's so far
-        KvItem nx;
-        for (; more; it = nx) {
-            __syncwarp();
-            const int tile0 = it.row0 + st * kRowsTile;
-            if (tile0 >= it.row1) {  // the item has no second tile
-                nx = it;
-                more = Work::next(a, sh, nx);
-                continue;
-            }
-            const int row = tile0 + r;
-            const bool live = row < it.row1;
-            // this thread's row: token and head; the others' by shuffle
-            const int tok = live ? kv_token(a, row) : 0;
-            const int head = it.h * a.group + (live ? row - tok * a.group : 0);
-            auto row_at = [&](int64_t stride) {
-                return (it.q.base + tok) * stride + (int64_t)head * D;
-            };
-            const int rows_here = min(it.row1 - tile0 - wrow, 32);  // of the warp's 32
-
-            // the warp's 32 rows of queries: as they are into the tile, a row's lanes
-            // reading neighbouring bytes; then a thread a row scales its own by a power of
-            // two and leaves it as f16
-            {
-                const int64_t at = row_at(a.q_stride);
+        // a thread's row of an item's tile
+        struct Row {
+            bool live;
+            int tok, head, rows;  // token and head; rows of the warp's 32 in the item
+        };
+        auto row_of = [&](const KvItem& x) {
+            const int row = x.row0 + st * kRowsTile + r;
+            Row y;
+            y.live = row < x.row1;
+            y.tok = y.live ? kv_token(a, row) : 0;
+            y.head = x.h * a.group + (y.live ? row - y.tok * a.group : 0);
+            y.rows = min(x.row1 - (row - lane), 32);
+            return y;
+        };
+        // on to the next item that has this tile
+        auto advance = [&](KvItem& x) {
+            do {
+                __syncwarp();
+                if (!Work::next(a, sh, x))
+                    return false;
+            } while (x.row0 + st * kRowsTile >= x.row1);
+            return true;
+        };
+        // the warp's 32 rows of queries as they are into the tile, a row's lanes reading
+        // neighbouring bytes
+        auto fetch = [&](const KvItem& x) {
+            const Row y = row_of(x);
+            const int64_t at = (x.q.base + y.tok) * a.q_stride + (int64_t)y.head * D;
 #pragma unroll 4
-                for (int i = 0; i < 32; i += kRowsAtOnce) {
-                    const int x = i + my_row;
-                    const int64_t from = __shfl_sync(0xFFFFFFFFu, at, x);
-                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + from +
-                                               4 * my_part;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
-                                     smem_u32(tile + piece_at(wrow + x, my_part >> 1)) +
-                                     8 * (my_part & 1)),
-                                 "l"(src), "r"(x < rows_here ? 8u : 0u)
-                                 : "memory");
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
+            for (int i = 0; i < 32; i += kRowsAtOnce) {
+                const int z = i + my_row;
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, at, z);
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + from + 4 * my_part;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
+                                 smem_u32(tile + piece_at(wrow + z, my_part >> 1)) +
+                                 8 * (my_part & 1)),
+                             "l"(src), "r"(z < y.rows ? 8u : 0u)
+                             : "memory");
             }
+        };
+        // then a thread a row scales its own by a power of two and leaves it as f16;
+        // returns the factor of the row's scores
+        auto convert = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-            float f;
-            {
-                uint32_t top = 0;  // BF16 magnitudes order like their bits
+            uint32_t top = 0;  // BF16 magnitudes order like their bits
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(tile + piece_at(r, c));
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                                 __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-                }
-                top = max(top & 0xFFFFu, top >> 16);
-                top = min(top, 0x7F80u);  // NaN: any finite factor keeps it
-                const int e = min(max(14 - ((int)(top >> 7) - 127), -100), 100);
-                const float up = top ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
-                f = qk * (top ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4* place = reinterpret_cast<uint4*>(tile + piece_at(r, c));
-                    const uint4 x = *place;
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = pack_f16(__uint_as_float(w[j] << 16) * up,
-                                        __uint_as_float(w[j] & 0xFFFF0000u) * up) ^ flip;
-                    *place = make_uint4(o[0], o[1], o[2], o[3]);
-                }
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(tile + piece_at(r, c));
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                             __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
             }
-            // a factor of 0 (a zero scale) would make -inf of a masked score NaN
-            f = f == 0.f ? 1e-38f : f;
+            top = max(top & 0xFFFFu, top >> 16);
+            top = min(top, 0x7F80u);  // NaN: any finite factor keeps it
+            const int e = min(max(14 - ((int)(top >> 7) - 127), -100), 100);
+            const float up = top ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
+            const float f = qk * (top ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4* place = reinterpret_cast<uint4*>(tile + piece_at(r, c));
+                const uint4 x = *place;
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[j] = pack_f16(__uint_as_float(w[j] << 16) * up,
+                                    __uint_as_float(w[j] & 0xFFFF0000u) * up) ^ flip;
+                *place = make_uint4(o[0], o[1], o[2], o[3]);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            fence_before();  // the last item's reads of the output come before this item's products
             warp_arrive(qfull);
+            // a factor of 0 (a zero scale) would make -inf of a masked score NaN
+            return f == 0.f ? 1e-38f : f;
+        };
+
+        if (more && it.row0 + st * kRowsTile >= it.row1)
+            more = advance(it);
+        float f = 0.f, next_f = 0.f;
+        if (more) {
+            fetch(it);
+            f = convert();
+        }
+        KvItem nx;
+        for (; more; it = nx, f = next_f) {
+            const Row mine = row_of(it);
+            const bool live = mine.live;
+            const int tok = mine.tok, head = mine.head;
 
             // the next item, while this one's first scores are made: its query rows to L2
             nx = it;
-            more = Work::next(a, sh, nx);
-            {
-                const int x = nx.row0 + st * kRowsTile + r;
-                if (more && x < nx.row1) {
-                    const int y = kv_token(a, x);
+            more = advance(nx);
+            if (more) {
+                const Row y = row_of(nx);
+                if (y.live) {
                     const char* q = reinterpret_cast<const char*>(
-                        static_cast<const __nv_bfloat16*>(a.q) + (nx.q.base + y) * a.q_stride +
-                        (int64_t)(nx.h * a.group + x - y * a.group) * D);
+                        static_cast<const __nv_bfloat16*>(a.q) +
+                        (nx.q.base + y.tok) * a.q_stride + (int64_t)y.head * D);
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
                     if constexpr (D > 64)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128));
@@ -587,6 +604,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 warp_arrive(pfull);
             }
 
+            // the next item's queries, during the last products: its first scores are made
+            // during the output below (its own products wait for its probabilities)
+            if (more) {
+                fetch(nx);
+                next_f = convert();
+            }
+
             // ---- the item's output ----------------------------------------------------------
             mbar_wait(ofull, items & 1, abort_flag, a.status);
             ++items;
@@ -597,33 +621,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     a.lse[(int64_t)(it.q.base + tok) * (a.c.heads * a.group) + head] =
                         lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
             };
-            // 32 outputs of the row into the tile, which the products are done with
-            auto stage = [&](int i, const float* o, float scale) {
+            // 32 outputs of each of the warp's rows, over shared memory: a row's lanes write
+            // neighbouring bytes
+            const int64_t row_out = (it.q.base + tok) * a.out_stride + (int64_t)head * D;
+            auto write = [&](int i, const float* o, float scale) {
+                __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
+                for (int j = 0; j < 4; ++j) {
                     uint32_t v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(o[j + 2 * k] * scale,
-                                                                       o[j + 2 * k + 1] * scale);
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(
+                            o[8 * j + 2 * k] * scale, o[8 * j + 2 * k + 1] * scale);
                         v[k] = *reinterpret_cast<const uint32_t*>(&x);
                     }
-                    *reinterpret_cast<uint4*>(tile + piece_at(r, (i + j) / 8)) =
+                    *reinterpret_cast<uint4*>(staged + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
                         make_uint4(v[0], v[1], v[2], v[3]);
                 }
-            };
-            // the warp's staged rows to the output, a row's lanes neighbouring bytes
-            auto write_rows = [&]() {
-                const int64_t at = row_at(a.out_stride);
                 __syncwarp();
-#pragma unroll 4
-                for (int i = 0; i < 32; i += kRowsAtOnce) {
-                    const int x = i + my_row;
-                    const int64_t to = __shfl_sync(0xFFFFFFFFu, at, x);
-                    if (x < rows_here)
-                        *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) + my_part) =
-                            *reinterpret_cast<const uint2*>(tile + piece_at(wrow + x, my_part >> 1) +
-                                                            8 * (my_part & 1));
+                const int part8 = lane & 7;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const int x = j + (lane >> 3);
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, row_out, x);
+                    if (x < mine.rows)
+                        *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to + i) + part8) =
+                            *reinterpret_cast<const uint2*>(
+                                staged + x * 64 + (((part8 >> 1) ^ (x >> 1 & 3)) << 4) + 8 * (part8 & 1));
                 }
             };
             // a partial tile: [D] columns of 128 rows, then references, then sums
@@ -638,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 for (int j = 0; j < 32; ++j)
                     x[j] = __uint_as_float(o[j]);
                 if (whole) {
-                    stage(i, x, scale);
+                    write(i, x, scale);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -646,7 +670,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 }
             }
             if (whole) {
-                write_rows();
                 write_lse(m, l);
                 continue;
             }
@@ -691,9 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     for (int j = 0; j < 32; ++j)
                         x[j] = fmaf(__ldcg(pc + (i + j) * kRowsTile), by, x[j]);
                 }
-                stage(i, x, all);
+                write(i, x, all);
             }
-            write_rows();
             write_lse(mt, lt);
         }
     } else if (warp < kMmaWarp) {
@@ -797,12 +819,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         for (; more && ok; more = Work::next(a, sh, it)) {
             const int tiles = it.row1 - it.row0 > kRowsTile ? 2 : 1;
             const int32_t count = it.u1 - it.u0;
-            if (!wait(bars.qfull[0], items) || (tiles == 2 && !wait(bars.qfull[1], items1)) ||
-                !wait(bars.kfull[n & 1], n >> 1))
+            if (!wait(bars.kfull[n & 1], n >> 1))
                 break;
-            fence_after();
-            for (int st = 0; st < tiles; ++st)
+            for (int st = 0; st < tiles; ++st) {
+                if (!wait(bars.qfull[st], st ? items1 : items))
+                    break;
+                fence_after();
                 scores(st, n & 1);
+            }
             commit(one, smem_u32(&bars.kempty[n & 1]));
             for (int32_t j = 0; j < count && ok; ++j, ++n) {
                 const uint32_t b = n & 1, nb = (n + 1) & 1;
