@@ -32,9 +32,9 @@
 // (about 2600 cycles a block beside the 1024 of its products, of which the other
 // tile's run meanwhile) and shared memory, which the products of both tiles and the
 // decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
-// cycles.  2048 queries of 32 heads on 32049 keys: 776 us, 1.34 PFLOP/s; four prompts of
-// 333..4096 tokens: 750 us, 0.91 PFLOP/s (an item adds 8 to 18 us of queries, first
-// decode and output to its keys).
+// cycles.  2048 queries of 32 heads on 32049 keys: 762 us, 1.37 PFLOP/s; four prompts of
+// 2185..3879 tokens and 64 heads: 710 us, 0.96 PFLOP/s (an item's queries, first
+// block, masked last block and output add about 9 us to its keys).
 //
 // Waits have clock budgets; when one runs out NVFP4_DEVICE_WAIT_TIMEOUT is set,
 // later waits are passed over, MMAs in flight are drained and tensor memory is
@@ -55,9 +55,9 @@ namespace {
 constexpr int kRowsTile = 128;             // query rows of an MMA tile
 constexpr int kRows = 2 * kRowsTile;       // of an item
 constexpr int kKeys = 128;                 // keys of a block
-// Blocks that an item's start and end cost (us for four prompts of 333..4096 tokens: 1 846,
-// 2 806, 3 776, 5 750, 8 820).
-constexpr int kItemCost = 5;
+// Blocks that an item's start and end cost (us for four prompts of 2185..3879 tokens of 64
+// heads / six of 32 heads: 2 739 / 405, 3 710 / 390, 4 731 / 385, 5 718 / 403).
+constexpr int kItemCost = 3;
 constexpr int kDecodeWarp = 8, kMmaWarp = 12;
 constexpr int kDecodeRows = kKeys / (kMmaWarp - kDecodeWarp);  // tokens a decoding warp
 constexpr int kThreads = 32 * (kMmaWarp + 1);
@@ -365,8 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                        pfull = smem_u32(&bars.pfull[st]), ofull = smem_u32(&bars.ofull[st]);
         uint8_t* tile = smem + st * C::kTile;                    // the queries
         uint8_t* staged = smem + 6 * C::kTile + warp * (32 * 64);  // the warp's outputs
-        constexpr int kRowLanes = D / 4, kRowsAtOnce = 32 / kRowLanes;  // 8 bytes a lane
-        const int my_part = lane % kRowLanes, my_row = lane / kRowLanes;
+        // rows move in pieces of 16 bytes, a lane each, where their alignment allows it
+        // (halves of 8 bytes: four prompts 726 us instead of 701).  What runs once an item
+        // is kept in short loops: unrolled to 20 KB, the queries' part spent 18000 cycles
+        // an item on fetching its instructions.
+        constexpr int kPieces = D / 8;
+        const bool q_wide = ((uintptr_t)a.q | (uintptr_t)(2 * a.q_stride)) % 16 == 0;
+        const bool out_wide = ((uintptr_t)a.out | (uintptr_t)(2 * a.out_stride)) % 16 == 0;
         // a negative factor goes into the queries' signs, so that larger scores are
         // larger throughout
         const float vg = a.c.v_g[0], signed_qk = a.scale_log2 * a.c.k_g[0], qk = fabsf(signed_qk);
@@ -400,16 +405,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         auto fetch = [&](const KvItem& x) {
             const Row y = row_of(x);
             const int64_t at = (x.q.base + y.tok) * a.q_stride + (int64_t)y.head * D;
-#pragma unroll 4
-            for (int i = 0; i < 32; i += kRowsAtOnce) {
-                const int z = i + my_row;
+#pragma unroll 2
+            for (int i = 0; i < 32; i += 32 / kPieces) {
+                const int z = i + lane / kPieces, c = lane % kPieces;
                 const int64_t from = __shfl_sync(0xFFFFFFFFu, at, z);
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + from + 4 * my_part;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
-                                 smem_u32(tile + piece_at(wrow + z, my_part >> 1)) +
-                                 8 * (my_part & 1)),
-                             "l"(src), "r"(z < y.rows ? 8u : 0u)
-                             : "memory");
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + from + 8 * c;
+                const uint32_t dst = smem_u32(tile + piece_at(wrow + z, c));
+                if (q_wide) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                                 "r"(z < y.rows ? 16u : 0u)
+                                 : "memory");
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + 8 * k),
+                                     "l"(src + 4 * k), "r"(z < y.rows ? 8u : 0u)
+                                     : "memory");
+                }
             }
         };
         // then a thread a row scales its own by a power of two and leaves it as f16;
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
             uint32_t top = 0;  // BF16 magnitudes order like their bits
-#pragma unroll
+#pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 x = *reinterpret_cast<const uint4*>(tile + piece_at(r, c));
                 top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
@@ -429,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             const int e = min(max(14 - ((int)(top >> 7) - 127), -100), 100);
             const float up = top ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
             const float f = qk * (top ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f);
-#pragma unroll
+#pragma unroll 2
             for (int c = 0; c < D / 8; ++c) {
                 uint4* place = reinterpret_cast<uint4*>(tile + piece_at(r, c));
                 const uint4 x = *place;
@@ -639,15 +651,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                         make_uint4(v[0], v[1], v[2], v[3]);
                 }
                 __syncwarp();
-                const int part8 = lane & 7;
+                const int c = lane & 3;
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const int x = j + (lane >> 3);
+                for (int j = 0; j < 32; j += 8) {
+                    const int x = j + (lane >> 2);
                     const int64_t to = __shfl_sync(0xFFFFFFFFu, row_out, x);
-                    if (x < mine.rows)
-                        *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to + i) + part8) =
-                            *reinterpret_cast<const uint2*>(
-                                staged + x * 64 + (((part8 >> 1) ^ (x >> 1 & 3)) << 4) + 8 * (part8 & 1));
+                    const uint4 v =
+                        *reinterpret_cast<const uint4*>(staged + x * 64 + ((c ^ (x >> 1 & 3)) << 4));
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + to + i + 8 * c;
+                    if (x < mine.rows) {
+                        if (out_wide) {
+                            *reinterpret_cast<uint4*>(dst) = v;
+                        } else {
+                            reinterpret_cast<uint2*>(dst)[0] = make_uint2(v.x, v.y);
+                            reinterpret_cast<uint2*>(dst)[1] = make_uint2(v.z, v.w);
+                        }
+                    }
                 }
             };
             // a partial tile: [D] columns of 128 rows, then references, then sums

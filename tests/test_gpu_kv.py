@@ -694,3 +694,23 @@ def test_tables_outputs_are_separate(nv, reqs, tokens):
     del got
     other = torch.zeros(1 << 12, dtype=torch.int32, device="cuda")  # takes freed memory, if there is any
     assert (kept == -103).all() and (other == 0).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shift,extra", [(4, 0), (0, 4), (4, 4)])
+def test_rows_on_8_byte_boundaries(nv, dim, shift, extra):
+    """BF16 queries and outputs that are aligned to 8 bytes only give what aligned copies give."""
+    lens = [300, 41]
+    cache, table, gen = filled(nv, lens, 2, dim, 32)
+    row = 8 * dim + extra
+    flat = torch.randn(80 * row + 8, generator=gen, device="cuda").to(BF16)
+    q = flat[shift:].as_strided((80, 8, dim), (row, dim, 1))
+    start = ints([0, 47, 80])
+    for kernel in (nv.KERNEL_KV_ROWS, nv.KERNEL_KV_TILE):
+        want = nv.kv_attention(cache, q.contiguous(), table, ints(lens), start, max_q=47, kernel=kernel)
+        room = torch.full((80 * row + 8,), 7.0, dtype=BF16, device="cuda")
+        out = room[shift:].as_strided((80, 8, dim), (row, dim, 1))
+        nv.kv_attention(cache, q, table, ints(lens), start, max_q=47, kernel=kernel, out=out)
+        assert torch.equal(out, want)
+        out.fill_(7.0)
+        assert (room == 7.0).all()                      # nothing else was written
