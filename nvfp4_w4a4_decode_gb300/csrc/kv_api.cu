@@ -12,12 +12,12 @@ namespace {
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
 // Whether the tcgen05 kernel takes an attention call: its tiles of 128 rows and
-// its start of some 8 us an item want many rows a request, and enough of them
-// in all.  Measured both ways on GB300 (rows kernel / tile kernel, us): 64
-// requests of 4000 tokens, 8 kv heads of 128, 32 rows a request 186 / 277, 48 rows 336 /
-// 278; 16 of 1000, 64 rows 51 / 44; 16 of 8000, 4 kv heads of 64, 64 rows 57 / 64, 96 rows
-// 81 / 64; one of 30000, 8 kv heads, 128 rows 87 / 100, 256 rows 146 / 106; one of 2000,
-// 256 rows 34 / 42.
+// its start of some microseconds an item want many rows a request, and enough of
+// them in all.  Measured both ways on GB300 (rows kernel / tile kernel, us): 64
+// requests of 4000 tokens, 8 kv heads of 128, 32 rows a request 184 / 233, 48 rows 336 /
+// 230; 16 of 1000, 32 rows 30 / 36, 48 rows 45 / 36; 16 of 8000, 4 kv heads of 64, 32 rows
+// 35 / 53, 64 rows 54 / 52; one of 30000, 8 kv heads of 128, 128 rows 80 / 90, 256 rows
+// 142 / 91; one of 2000, 256 rows 30 / 36.
 bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
 {
     return rows > 32 && reqs * heads * rows >= 2048;

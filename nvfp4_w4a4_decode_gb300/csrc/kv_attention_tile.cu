@@ -33,7 +33,7 @@
 // tile's run meanwhile) and shared memory, which the products of both tiles and the
 // decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
 // cycles.  2048 queries of 32 heads on 32049 keys: 762 us, 1.37 PFLOP/s; four prompts of
-// 2185..3879 tokens and 64 heads: 710 us, 0.96 PFLOP/s (an item's queries, first
+// 2185..3879 tokens and 64 heads: 713 us, 0.95 PFLOP/s (an item's queries, first
 // block, masked last block and output add about 9 us to its keys).
 //
 // Waits have clock budgets; when one runs out NVFP4_DEVICE_WAIT_TIMEOUT is set,
@@ -56,8 +56,9 @@ constexpr int kRowsTile = 128;             // query rows of an MMA tile
 constexpr int kRows = 2 * kRowsTile;       // of an item
 constexpr int kKeys = 128;                 // keys of a block
 // Blocks that an item's start and end cost (us for four prompts of 2185..3879 tokens of 64
-// heads / six of 32 heads: 2 739 / 405, 3 710 / 390, 4 731 / 385, 5 718 / 403).
-constexpr int kItemCost = 3;
+// heads / six of 32 heads / 16 requests of 3..6 tokens on a window of 1024: 3 704 392 28.8,
+// 4 724 384 27.1, 5 716 401 27.0, 7 753 413 27.8).
+constexpr int kItemCost = 5;
 constexpr int kDecodeWarp = 8, kMmaWarp = 12;
 constexpr int kDecodeRows = kKeys / (kMmaWarp - kDecodeWarp);  // tokens a decoding warp
 constexpr int kThreads = 32 * (kMmaWarp + 1);
@@ -377,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         const float vg = a.c.v_g[0], signed_qk = a.scale_log2 * a.c.k_g[0], qk = fabsf(signed_qk);
         const uint32_t flip = signed_qk < 0.f ? 0x80008000u : 0u;
         uint32_t blocks = 0, items = 0;  // this tile's so far
-        // a thread's row of an item's tile
+        // a thread's row of an item's tile (past the item's end: its last row again, which
+        // keeps the thread off the masked path; never written)
         struct Row {
             bool live;
             int tok, head, rows;  // token and head; rows of the warp's 32 in the item
@@ -386,8 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             const int row = x.row0 + st * kRowsTile + r;
             Row y;
             y.live = row < x.row1;
-            y.tok = y.live ? kv_token(a, row) : 0;
-            y.head = x.h * a.group + (y.live ? row - y.tok * a.group : 0);
+            const int at = min(row, x.row1 - 1);
+            y.tok = kv_token(a, at);
+            y.head = x.h * a.group + at - y.tok * a.group;
             y.rows = min(x.row1 - (row - lane), 32);
             return y;
         };
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 }
             }
 
-            const int32_t pos = live ? it.q.seq - it.q.nq + tok : -1;
+            const int32_t pos = it.q.seq - it.q.nq + tok;
             float m = -INFINITY, l = 0.f;  // reference minus kLift, and the sum
             const uint64_t f2 = pair(f, f);
             for (int32_t u = it.u0; u < it.u1; ++u, ++blocks) {
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                     for (int i = 0; i < 32; ++i)
                         s[i] = seen >> i & 1 ? s[i] : 0xFF800000u;
                 };
-                if (u == it.u0) {  // the first reference: the block's largest score
+                if (mine.rows > 0 && u == it.u0) {  // the first reference: the block's largest score
                     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 32) {
@@ -607,7 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                             tmem_st32(tS + h / 2 + i, p16 + i);
                     }
                 };
-                if (__any_sync(0xFFFFFFFFu, edge))
+                if (mine.rows <= 0) {
+                    // no row of the warp is in the item: whatever the products take for it
+                    // stays in rows that are never written
+                } else if (__any_sync(0xFFFFFFFFu, edge))
                     exponentials(std::true_type{});
                 else
                     exponentials(std::false_type{});
