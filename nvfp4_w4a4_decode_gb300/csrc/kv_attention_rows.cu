@@ -354,6 +354,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             const uint32_t group = taken + i / kSub, slot = group % ST;
             const int32_t unit0 = first_tok + i * kUnit;
             mbar_wait(full0 + 8 * slot, (group / ST) & 1, abort_flag, a.status);
+            // Lanes poll each for itself.  One that is still at it when another frees the slot
+            // could find the phase after next and wait for good; and the MMAs want a whole warp.
+            __syncwarp();
             if (unit0 < it.q.seq) {  // else past the end: nothing to do in this unit
                 const uint8_t* st = smem + slot * C::kStageBytes + (i % kSub) * code_step;
                 const uint8_t* sk = smem + slot * C::kStageBytes + 2 * v_part + (i % kSub) * scale_step;

@@ -714,3 +714,19 @@ def test_rows_on_8_byte_boundaries(nv, dim, shift, extra):
         assert torch.equal(out, want)
         out.fill_(7.0)
         assert (room == 7.0).all()                      # nothing else was written
+
+
+# ---- waits -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_ring_of_groups_that_end_early(nv, dtype):
+    """Groups of 64 tokens whose second half lies past the request's end (their warp gives
+    the ring's place back unread), many of them in a row and in every share: no wait runs
+    out and the bits repeat."""
+    rng = np.random.default_rng(11)
+    seqs = (64 * rng.integers(0, 12, 600) + rng.integers(1, 33, 600)).tolist()
+    cache, q, table, out, lse = run_attention(nv, seqs, [1] * 600, 8, 2, 64, 16, dtype)
+    for _ in range(20):
+        o2, l2 = nv.kv_attention(cache, q, table, ints(seqs), starts([1] * 600), max_q=1, return_lse=True)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    assert nv.device_status() == 0
