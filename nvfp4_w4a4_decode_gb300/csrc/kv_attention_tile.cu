@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 const int32_t first = a.window > 0 ? last - a.window + 1 : 0;
                 const bool edge = last < kKeys - 1 || first > 0;
                 mbar_wait(sfull, blocks & 1, abort_flag, a.status);
+                __syncwarp();  // lanes poll each for itself; the loads below want a whole warp
                 fence_after();
                 // scores outside [first, last] of the 32 from c on become -inf
                 auto hide = [&](int c, uint32_t* s) {
@@ -631,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
 
             // ---- the item's output ----------------------------------------------------------
             mbar_wait(ofull, items & 1, abort_flag, a.status);
+            __syncwarp();
             ++items;
             fence_after();
             const bool whole = it.u0 == 0 && it.u1 == it.n;

@@ -730,3 +730,16 @@ def test_ring_of_groups_that_end_early(nv, dtype):
         o2, l2 = nv.kv_attention(cache, q, table, ints(seqs), starts([1] * 600), max_q=1, return_lse=True)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
     assert nv.device_status() == 0
+
+
+def test_tile_waits_of_whole_warps(nv):
+    """Items of one and of two tiles in turn, cut and whole: every wait of the softmax
+    warps before their loads of scores and outputs; the bits repeat and none runs out."""
+    counts = [130, 3, 64, 300, 1, 33] * 4
+    seqs = [c + 700 * (i % 3) for i, c in enumerate(counts)]
+    cache, q, table, out, lse = run_tile(nv, seqs, counts, 8, 2, 64, 16)
+    for _ in range(20):
+        o2, l2 = nv.kv_attention(cache, q, table, ints(seqs), starts(counts), return_lse=True,
+                                 kernel=nv.KERNEL_KV_TILE)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    assert nv.device_status() == 0
