@@ -76,7 +76,9 @@ int64_t nvfp4_kv_page_bytes(int64_t page_size, int64_t num_kv_heads, int64_t hea
  *   slots           int64 [tokens], out
  * A page past the end of the free list is entered as -1 and its tokens get
  * slot -1; tokens past max_blocks * P get slot -1, take no page, and seq_len
- * stops there; both set NVFP4_DEVICE_KV_RANGE.  reqs at most 16384
+ * stops there; both set NVFP4_DEVICE_KV_RANGE, and so do more new tokens than `tokens`.
+ * Lengths may be any int32: positions, q_start and *free_next past 2^31 - 1 are
+ * stored as 2^31 - 1.  reqs at most 16384
  * (NVFP4_ERR_UNSUPPORTED), tokens and max_blocks * P below 2^30.  options:
  * NVFP4_FLAG_PDL.  One kernel.
  */

@@ -743,3 +743,63 @@ def test_tile_waits_of_whole_warps(nv):
                                  kernel=nv.KERNEL_KV_TILE)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
     assert nv.device_status() == 0
+
+
+# ---- block tables at the largest lengths ------------------------------------------------------
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("past,new,tokens", [
+    ([BIG], [5], 8), ([BIG - 3, 4], [5, 2], 7), ([3, BIG, 7], [1, BIG, 2], 40), ([0, 3], [BIG, BIG], 40),
+    ([0] * 4, [2 ** 30] * 4, 33), ([BIG] * 600, [BIG] * 600, 700), ([5, 0], [3, BIG], 90)])
+def test_tables_lengths_up_to_int32(nv, past, new, tokens):
+    """Positions and sums that pass 32 bits are cut off and reported; the table is never
+    left (a guard of 64 rows on both sides of it stays as it was)."""
+    page, blocks, reqs = 16, 4, len(past)
+    cap = page * blocks
+    free = list(range(100, 100 + 3 * reqs))
+    room = torch.full((reqs + 128, blocks), -9, dtype=torch.int32, device="cuda")
+    table = room[64:64 + reqs]
+    held = [-(-min(n, cap) // page) for n in past]
+    for r, h in enumerate(held):
+        table[r, :h] = 10000 + r
+    rows, seq, start, head, want = [], [], [0], 1, table.tolist()
+    for r, (n, c) in enumerate(zip(past, new)):
+        end = min(n + c, cap)
+        for b in range(held[r], -(-end // page)):
+            want[r][b] = free[head] if head < len(free) else -1
+            head += 1
+        for i in range(min(c, tokens - len(rows))):
+            pos = n + i
+            entry = want[r][pos // page] if pos < end else -1
+            rows.append((min(pos, BIG), entry * page + pos % page if entry >= 0 else -1))
+        seq.append(end)
+        start.append(start[-1] + c)
+    rows += [(0, -1)] * (tokens - len(rows))
+    nv.device_status(clear=True)
+    got = nv.kv_tables(ints(past), ints(new), ints(free), ints([1]), table, page_size=page, tokens=tokens)
+    assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+    assert got.seq_len.tolist() == seq
+    assert got.q_start.tolist() == [min(s, BIG) for s in start]
+    assert got.positions.tolist() == [p for p, _ in rows]
+    assert got.slots.tolist() == [s for _, s in rows]
+    assert got.free_head.tolist() == [head]
+    assert table.tolist() == want
+    assert (room[:64] == -9).all() and (room[64 + reqs:] == -9).all()
+
+
+def test_tables_pages_past_32_bits(nv):
+    """More than 2^32 new pages in a table of 17 GB: those past the free list are -1, all of them."""
+    reqs, blocks = 16384, (1 << 18) + 1
+    table = torch.full((reqs, blocks), 7, dtype=torch.int32, device="cuda")
+    new = torch.full((reqs,), BIG, dtype=torch.int32, device="cuda")
+    nv.device_status(clear=True)
+    got = nv.kv_tables(torch.zeros_like(new), new, ints([50, 51, 52]), ints([-2]), table, page_size=16, tokens=100)
+    assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+    assert table[0, :6].tolist() == [-1, -1, 50, 51, 52, -1]
+    table[0, 2:5] = -1
+    for rows in table.split(1024):
+        assert (rows == -1).all()
+    assert got.free_head.tolist() == [BIG] and got.q_start[-1].item() == BIG
+    assert got.slots[:32].tolist() == [-1] * 32 and got.slots[32:80].tolist() == list(range(800, 848))
