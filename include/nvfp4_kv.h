@@ -114,6 +114,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* k, int64_t k_stride
  *     lse = ln sum_j exp(s_j)
  * A row that sees no key (an empty request, positions below 0) gets zeros and
  * lse = -inf.  Whatever the cache holds past a request's end does not matter.
+ * Keys and values on a page that is not in the pool count as zeros
+ * (NVFP4_DEVICE_KV_RANGE is set).
  * Scores, softmax statistics and sums are FP32; the cached values enter
  * exactly, FP32 queries and (for FP32 outputs) probabilities as two f16 terms
  * each, else probabilities as one f16.

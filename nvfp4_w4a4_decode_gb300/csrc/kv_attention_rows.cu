@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         const int row_bytes = by_page ? D * 9 / 8 : piece < 2 ? D / 2 : D / 16;
         const uint32_t bytes = by_page ? (uint32_t)row_bytes << P : (uint32_t)row_bytes * kGroup;
         const int before_me = piece < 2 ? piece * (D / 2) : D + (piece - 2) * (D / 16);
-        const uint32_t dst0 = ring + (by_page ? piece * bytes : before_me * kGroup);
+        const uint32_t in_slot = by_page ? piece * bytes : before_me * kGroup;
         const uint8_t* src0 = a.c.pool + (by_page ? 0 : (int64_t)before_me << P);
         bool bad = false;
         uint32_t sent = 0;  // groups so far
@@ -211,8 +211,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             if (!__all_sync(0xFFFFFFFFu, free_slot))
                 break;
             const bool ok = page >= 0 && page < a.c.num_pages;
-            bad |= !ok && page != -2;
-            // a piece without a page is left out: its place holds old bytes
+            // a page outside the pool counts as zeros (no bytes of other pages stay in its place)
+            if (!ok && page != -2) {
+                bad = true;
+                uint8_t* place = smem + slot * C::kStageBytes + in_slot;
+                for (uint32_t i = 0; i < bytes; i += 16)
+                    *reinterpret_cast<uint4*>(place + i) = make_uint4(0u, 0u, 0u, 0u);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            // a piece past the request's end is left out: its place holds old bytes, unread
             const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok) >> (4 * sub) & 0xFu;
             if (piece == 0 && sub < n) {
                 const uint32_t all = by_page ? __popc(there) * bytes : there ? C::kStageBytes : 0;
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             if (ok) {
                 const int32_t off =
                     by_page ? 0 : ((it.first + u + sub) * kGroup) & ((1 << P) - 1);
-                bulk_copy(dst0 + slot * C::kStageBytes,
+                bulk_copy(ring + slot * C::kStageBytes + in_slot,
                           src0 + page * a.c.page_stride + it.h * head_bytes + off * row_bytes,
                           bytes, fb);
             }

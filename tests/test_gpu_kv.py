@@ -803,3 +803,36 @@ def test_tables_pages_past_32_bits(nv):
         assert (rows == -1).all()
     assert got.free_head.tolist() == [BIG] and got.q_start[-1].item() == BIG
     assert got.slots[:32].tolist() == [-1] * 32 and got.slots[32:80].tolist() == list(range(800, 848))
+
+
+# ---- pages that are not there ---------------------------------------------------------------
+
+def without_pages(nv, cache, pages):
+    """The same cache with these pages' bytes zero."""
+    pool = cache.pool.clone()
+    pool[pages] = 0
+    return nv.KVCache(pool, cache.k_g, cache.v_g, page_size=cache.page_size, head_dim=cache.head_dim)
+
+
+@pytest.mark.parametrize("name,dtype", [("KERNEL_KV_ROWS", BF16), ("KERNEL_KV_ROWS", FP32), ("KERNEL_KV_TILE", BF16)])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_pages_outside_the_pool_count_as_zeros(nv, name, dtype, page):
+    """Not as what an earlier request left in the place that a page is copied to."""
+    kernel = getattr(nv, name)
+    seqs, counts = [900, 40], [3, 2]
+    other, other_table, _ = filled(nv, [20000] * 8, 2, 64, 64, seed=9)
+    cache, table, gen = filled(nv, seqs, 2, 64, page)
+    q = torch.randn((5, 8, 64), generator=gen, device="cuda").to(dtype)
+    for at in ([0], [2, 3], [-(-900 // page) - 1], list(range(-(-900 // page)))):
+        lost = table[0, at].long()
+        ref = attention(without_pages(nv, cache, lost), q, table, seqs, counts)
+        for value in (-1, cache.num_pages, 1 << 30):
+            broken = table.clone()
+            broken[0, at] = value
+            # what the SMs' shared memory holds before: keys and values of other requests
+            nv.kv_attention(other, q.repeat(2, 1, 1)[:8], other_table, ints([20000] * 8), kernel=kernel)
+            nv.device_status(clear=True)
+            out, lse = nv.kv_attention(cache, q, broken, ints(seqs), starts(counts), max_q=3, return_lse=True,
+                                       kernel=kernel)
+            assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+            check_attention(out, lse, ref, dtype)
