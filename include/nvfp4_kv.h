@@ -113,7 +113,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* k, int64_t k_stride
  *     s_j = scale * q . K_j,  out = sum_j softmax(s)_j V_j,
  *     lse = ln sum_j exp(s_j)
  * A row that sees no key (an empty request, positions below 0) gets zeros and
- * lse = -inf.  Whatever the cache holds past a request's end does not matter.
+ * lse = -inf.  Whatever the cache holds past a request's end, or before the first key that
+ * a request's rows see, does not matter, nor do table entries of pages that lie there
+ * wholly: pages that a window has left can be given to others.
  * Keys and values on a page that is not in the pool count as zeros
  * (NVFP4_DEVICE_KV_RANGE is set).
  * Scores, softmax statistics and sums are FP32; the cached values enter

@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         auto page_of = [&](const Item& x, int32_t u) {
             const int32_t tok = (x.first + u + sub) * kGroup + (by_page ? piece << P : 0);
             const int32_t b = tok >> P;
-            return mine_to_copy && u + sub < x.u1 && tok < x.q.seq && b < a.max_blocks
+            return mine_to_copy && u + sub < x.u1 && tok < x.q.seq && b < a.max_blocks &&
+                           ((b + 1) << P) > Work::first_key(a, x)
                        ? a.table[x.r * a.table_stride + b]
                        : -2;  // nothing of the request there
         };
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             __syncwarp();
-            // a piece past the request's end is left out: its place holds old bytes, unread
+            // a piece past the request's end or before its window is left out: its place
+            // holds old bytes, which count for nothing
             const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok) >> (4 * sub) & 0xFu;
             if (piece == 0 && sub < n) {
                 const uint32_t all = by_page ? __popc(there) * bytes : there ? C::kStageBytes : 0;
@@ -357,6 +359,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         const int32_t p0 = it.q.seq - it.q.nq + kv_token(a, it.row0);
         const int32_t p1 = it.q.seq - it.q.nq + kv_token(a, it.row1 - 1);
         const int32_t all_hi = p0, all_lo = a.window > 0 ? p1 - a.window + 1 : 0;
+        // where 16 tokens are all of keys [key0, seq)
+        const int32_t key0 = Work::first_key(a, it);
+        const uint32_t inner = (uint32_t)max(it.q.seq - 15 - key0, 0);
 
         for (int i = (warp + kWarps - taken * kSub % kWarps) % kWarps; i < units; i += kWarps) {
             const uint32_t group = taken + i / kSub, slot = group % ST;
@@ -547,15 +552,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                                 one[k] = ss[vt * 4 + (g >> 1)];
                             }
                         }
-                        if (tok0 + 16 * h + 16 > it.q.seq) {  // past the end may be anything
+                        // past the end and before the window may be anything
+                        if ((uint32_t)(tok0 + 16 * h - key0) >= inner) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (tok0 + 16 * h + v_tok + (k >> 1) * 8 + (k & 1) * v_odd >= it.q.seq) {
+                            for (int k = 0; k < 4; ++k) {
+                                const int32_t tok = tok0 + 16 * h + v_tok + (k >> 1) * 8 + (k & 1) * v_odd;
+                                if (tok >= it.q.seq || tok < key0) {
                                     one[k] = 0;
 #pragma unroll
                                     for (int w = 0; w < D / 64; ++w)
                                         vw[h][k][w] = 0;
                                 }
+                            }
                         }
                         vs[h][0] = one[0] | (one[1] << 8);
                         vs[h][1] = one[2] | (one[3] << 8);

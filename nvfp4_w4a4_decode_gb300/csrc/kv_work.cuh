@@ -182,6 +182,13 @@ struct KvWork {
         n = (hi + UT - 1) / UT - first;
     }
 
+    // The first key that any row of an item sees.  What lies before it in the item's
+    // first unit is not looked at: its page may serve another request by now.
+    static __device__ __forceinline__ int32_t first_key(const KvAttnArgs& a, const KvItem& it)
+    {
+        return a.window > 0 ? max(0, it.q.seq - it.q.nq + kv_token(a, it.row0) - a.window + 1) : 0;
+    }
+
     static __device__ __forceinline__ void units(const KvAttnArgs& a, KvItem& it)
     {
         it.row0 = it.tile * R;

@@ -836,3 +836,34 @@ def test_pages_outside_the_pool_count_as_zeros(nv, name, dtype, page):
                                        kernel=kernel)
             assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
             check_attention(out, lse, ref, dtype)
+
+
+@pytest.mark.parametrize("name,dtype", [("KERNEL_KV_ROWS", BF16), ("KERNEL_KV_ROWS", FP32), ("KERNEL_KV_TILE", BF16)])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 32), (64, 64), (128, 128), (64, 256)])
+@pytest.mark.parametrize("window", [1, 37, 100, 256])
+def test_pages_that_a_window_has_left(nv, name, dtype, dim, page, window):
+    """Keys before every row's window: NaN bytes, or pages given away and their entries gone."""
+    kernel = getattr(nv, name)
+    seqs, counts = [1000, 400, 90, 777], [1, 5, 90, 40]
+    cache, table, gen = filled(nv, seqs, 2, dim, page)
+    q = torch.randn((sum(counts), 8, dim), generator=gen, device="cuda").to(dtype)
+    args = dict(max_q=max(counts), window=window, return_lse=True, kernel=kernel)
+    good, good_lse = nv.kv_attention(cache, q, table, ints(seqs), starts(counts), **args)
+    check_attention(good, good_lse, attention(cache, q, table, seqs, counts, window=window), dtype)
+    half, block = page * dim // 2, page * dim // 16
+    parts = [cache.pool[:, :, a:a + page * n].unflatten(2, (page, n)) for a, n in (
+        (0, dim // 2), (half, dim // 2), (2 * half, dim // 16), (2 * half + block, dim // 16))]
+    firsts = [max(0, n - c - window + 1) for n, c in zip(seqs, counts)]
+    for r, first in enumerate(firsts):
+        pos = torch.arange(first, device="cuda")
+        for part in parts:
+            part[table[r, pos // page].long(), :, pos % page] = 255
+    for entry in (None, -1, cache.num_pages):
+        left = table.clone()
+        for r, first in enumerate(firsts):
+            if entry is not None:
+                left[r, :first // page] = entry
+        nv.device_status(clear=True)
+        out, lse = nv.kv_attention(cache, q, left, ints(seqs), starts(counts), **args)
+        assert nv.device_status(clear=True) == 0
+        assert torch.equal(out, good) and torch.equal(lse, good_lse)
