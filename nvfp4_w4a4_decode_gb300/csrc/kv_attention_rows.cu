@@ -183,17 +183,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         const uint8_t* src0 = a.c.pool + (by_page ? 0 : (int64_t)before_me << P);
         bool bad = false;
         uint32_t sent = 0;  // groups so far
-        // the page of this lane's piece of groups u .. of an item
+        // the page of this lane's piece of groups u .. of an item (any below 0: none in the
+        // pool; kNothing, which no entry becomes: nothing of the request there)
+        constexpr int32_t kNothing = -2;
         auto page_of = [&](const Item& x, int32_t u) {
             const int32_t tok = (x.first + u + sub) * kGroup + (by_page ? piece << P : 0);
             const int32_t b = tok >> P;
             return mine_to_copy && u + sub < x.u1 && tok < x.q.seq && b < a.max_blocks &&
                            ((b + 1) << P) > Work::first_key(a, x)
-                       ? a.table[x.r * a.table_stride + b]
-                       : -2;  // nothing of the request there
+                       ? max(a.table[x.r * a.table_stride + b], -1)
+                       : kNothing;
         };
         int32_t u = more ? it.u0 : 0;
-        int32_t page = more ? page_of(it, u) : -2;
+        int32_t page = more ? page_of(it, u) : kNothing;
         while (more) {
             Item nx = it;
             int32_t nu = u + kBatch;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                 nmore = Work::next(a, sh, nx);
                 nu = nx.u0;
             }
-            const int32_t npage = nmore ? page_of(nx, nu) : -2;
+            const int32_t npage = nmore ? page_of(nx, nu) : kNothing;
             const int n = min(kBatch, it.u1 - u);
             const uint32_t k = sent + sub, slot = k % ST;
             const uint32_t fb = smem_u32(&full_bar[slot]);
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                 break;
             const bool ok = page >= 0 && page < a.c.num_pages;
             // a page outside the pool counts as zeros (no bytes of other pages stay in its place)
-            if (!ok && page != -2) {
+            if (!ok && page != kNothing) {
                 bad = true;
                 uint8_t* place = smem + slot * C::kStageBytes + in_slot;
                 for (uint32_t i = 0; i < bytes; i += 16)

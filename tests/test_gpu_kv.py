@@ -867,3 +867,18 @@ def test_pages_that_a_window_has_left(nv, name, dtype, dim, page, window):
         out, lse = nv.kv_attention(cache, q, left, ints(seqs), starts(counts), **args)
         assert nv.device_status(clear=True) == 0
         assert torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("name", ["KERNEL_KV_ROWS", "KERNEL_KV_TILE"])
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_every_entry_below_zero_is_reported(nv, name, page):
+    cache, table, gen = filled(nv, [300, 40], 2, 64, page)
+    q = torch.randn((2, 8, 64), generator=gen, device="cuda").to(BF16)
+    ref = attention(without_pages(nv, cache, table[0, 1:2].long()), q, table, [300, 40], [1, 1])
+    for value in (-1, -2, -3, -77, -2 ** 31):
+        broken = table.clone()
+        broken[0, 1] = value
+        nv.device_status(clear=True)
+        out, lse = nv.kv_attention(cache, q, broken, ints([300, 40]), return_lse=True, kernel=getattr(nv, name))
+        assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
+        check_attention(out, lse, ref, BF16)
