@@ -152,7 +152,10 @@ typedef struct {
  *   NVFP4_KERNEL_KV_TILE       tcgen05 tiles of 128 query rows: many rows a
  *                              request; BF16 queries and outputs only
  *                              (NVFP4_ERR_UNSUPPORTED otherwise)
- * -- OR-ed with NVFP4_FLAG_X_BF16, NVFP4_FLAG_Y_BF16, NVFP4_FLAG_PDL.
+ * -- OR-ed with NVFP4_FLAG_X_BF16, NVFP4_FLAG_Y_BF16, NVFP4_FLAG_PDL,
+ * NVFP4_FLAG_ALL_ROWS.  Rows of no request (before q_start[0], from q_start[reqs]
+ * on: the padding of a fixed-size batch; every row when reqs is 0) are left as
+ * they are, or with NVFP4_FLAG_ALL_ROWS get zeros and lse = -inf.
  * The keys of all requests are one list of work that the SMs share equally:
  * a request cut between SMs is joined through the workspace in a fixed order
  * (results do not depend on timing).
@@ -166,6 +169,7 @@ typedef struct {
  */
 #define NVFP4_KERNEL_KV_ROWS 1u
 #define NVFP4_KERNEL_KV_TILE 2u
+#define NVFP4_FLAG_ALL_ROWS 0x20000u
 
 int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
                        uint32_t options, void* workspace, size_t workspace_bytes, void* stream);

@@ -86,6 +86,7 @@ struct KvAttnArgs {
     int64_t out_stride;
     float* lse;
     int32_t q_bf16, out_bf16;
+    int32_t all_rows;  // rows of no request are written too
     float* part;      // partial results of items cut between CTAs (null: none is cut)
     unsigned* count;  // arrival counters, zero between calls
     unsigned* status;

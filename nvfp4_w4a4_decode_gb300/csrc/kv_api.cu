@@ -161,7 +161,8 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     if (st != NVFP4_OK)
         return st;
     if (args == nullptr || (options & ~(uint32_t)(NVFP4_KERNEL_MASK | NVFP4_FLAG_PDL |
-                                                  NVFP4_FLAG_X_BF16 | NVFP4_FLAG_Y_BF16)) != 0)
+                                                  NVFP4_FLAG_X_BF16 | NVFP4_FLAG_Y_BF16 |
+                                                  NVFP4_FLAG_ALL_ROWS)) != 0)
         return NVFP4_ERR_INVALID_ARG;
     const nvfp4_kv_attention_args& r = *args;
     if (workspace == nullptr ? workspace_bytes != 0 : !aligned(workspace, 16))
@@ -179,13 +180,14 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     if (kern != NVFP4_KERNEL_AUTO && kern != NVFP4_KERNEL_KV_ROWS &&
         !(kern == NVFP4_KERNEL_KV_TILE && all_bf16))
         return NVFP4_ERR_UNSUPPORTED;
-    if (r.tokens == 0 || r.reqs == 0)
+    const bool all_rows = (options & NVFP4_FLAG_ALL_ROWS) != 0;
+    if (r.tokens == 0 || (r.reqs == 0 && !all_rows))
         return NVFP4_OK;
     const bool q_bf16 = (options & NVFP4_FLAG_X_BF16) != 0;
     const bool out_bf16 = (options & NVFP4_FLAG_Y_BF16) != 0;
     const int64_t row = r.num_q_heads * a.c.dim;
-    if (r.q == nullptr || r.out == nullptr || r.seq_len == nullptr ||
-        (r.max_blocks > 0 && r.block_table == nullptr) || !aligned(r.q, q_bf16 ? 8 : 16) ||
+    if (r.q == nullptr || r.out == nullptr || (r.reqs > 0 && r.seq_len == nullptr) ||
+        (r.reqs > 0 && r.max_blocks > 0 && r.block_table == nullptr) || !aligned(r.q, q_bf16 ? 8 : 16) ||
         !aligned(r.out, out_bf16 ? 8 : 16) || !aligned(r.block_table, 4) ||
         !aligned(r.seq_len, 4) || !aligned(r.q_start, 4) || !aligned(r.lse, 4) ||
         (r.q_stride % 4) != 0 || (r.out_stride % 4) != 0 ||
@@ -200,7 +202,7 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     a.max_blocks = (int32_t)r.max_blocks;
     a.seq_len = r.seq_len;
     a.q_start = r.q_start;
-    a.q_per_req = (int32_t)(r.q_start ? 0 : r.tokens / r.reqs);
+    a.q_per_req = (int32_t)(r.q_start || r.reqs == 0 ? 0 : r.tokens / r.reqs);
     a.reqs = (int32_t)r.reqs;
     a.tokens = (int32_t)r.tokens;
     a.max_q = (int32_t)(r.max_q < r.tokens ? r.max_q : r.tokens);
@@ -214,6 +216,7 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
     a.lse = r.lse;
     a.q_bf16 = q_bf16;
     a.out_bf16 = out_bf16;
+    a.all_rows = all_rows;
     const bool tile = kern == NVFP4_KERNEL_KV_TILE ||
                       (kern == NVFP4_KERNEL_AUTO && all_bf16 &&
                        use_tile(a.reqs, a.c.heads, (int64_t)a.max_q * a.group));

@@ -160,8 +160,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     Share sh;
     Item it;
     bool more = Work::template start<kThreads>(a, work_sm, kWarps / kSub, sh, it);
-    if (sh.lo >= sh.hi)
+    if (sh.lo >= sh.hi) {
+        if (a.all_rows && warp == kWarps)
+            kv_write_other_rows(a, lane, 32);
         return;
+    }
 
     const int64_t head_bytes = kv_head_bytes(a.c.page_shift, D);
     const uint32_t ring = smem_u32(smem);
@@ -256,6 +259,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             }
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
+        if (a.all_rows)
+            kv_write_other_rows(a, lane, 32);
         return;
     }
 

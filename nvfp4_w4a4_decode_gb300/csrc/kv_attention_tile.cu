@@ -347,8 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     KvShare sh;
     KvItem it;
     bool more = Work::start<kThreads>(a, work_sm, kItemCost + 1, sh, it);
-    if (sh.lo >= sh.hi)
+    constexpr int kDecodeThreads = 32 * (kMmaWarp - kDecodeWarp);
+    const bool decodes = warp >= kDecodeWarp && warp < kMmaWarp;
+    if (sh.lo >= sh.hi) {
+        if (a.all_rows && decodes)
+            kv_write_other_rows(a, tid - 32 * kDecodeWarp, kDecodeThreads);
         return;
+    }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_base_s)),
@@ -818,6 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         }
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
+        if (a.all_rows)
+            kv_write_other_rows(a, tid - 32 * kDecodeWarp, kDecodeThreads);
     } else {
         // ---- warp 12: the MMAs --------------------------------------------------------------------
         uint32_t one;

@@ -263,7 +263,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     r.scale = a[7] != Py_None ? (float)number(a[7]) : 1.0f / std::sqrt((float)dim);
     r.window = integer(a[8]);
     Tensor out, lse;
-    if (a[9] == Py_None) {
+    // rows of no request are written where the memory is new, left alone in a given output
+    const bool new_out = a[9] == Py_None;
+    if (new_out) {
         const int64_t type = integer(a[10]);
         out = at::empty({r.tokens, r.num_q_heads, dim},
                         q.options().dtype(type == 0   ? q.scalar_type()
@@ -279,12 +281,15 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     r.out = out.data_ptr();
     const bool with_lse = PyObject_IsTrue(a[11]) == 1;
     if (with_lse) {
-        lse = at::empty({r.tokens, r.num_q_heads}, q.options().dtype(at::kFloat));
+        const auto lse_options = q.options().dtype(at::kFloat);
+        lse = new_out ? at::empty({r.tokens, r.num_q_heads}, lse_options)
+                      : at::full({r.tokens, r.num_q_heads}, -INFINITY, lse_options);
         r.lse = static_cast<float*>(lse.data_ptr());
     }
     const uint32_t options = (uint32_t)integer(a[12]) |
                              (q.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_X_BF16 : 0u) |
-                             (out.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_Y_BF16 : 0u);
+                             (out.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_Y_BF16 : 0u) |
+                             (new_out ? NVFP4_FLAG_ALL_ROWS : 0u);
     if (failed("nvfp4_kv_attention", fn_attention(c, &r, options, address(a[13]),
                                                   (size_t)integer(a[14]), address(a[15]))))
         return nullptr;

@@ -119,6 +119,44 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
     return q;
 }
 
+// Zeros (and lse = -inf) for the call's rows [0, begin) and [end, tokens), by `threads`
+// threads of every CTA.  A function of its own, its arguments by value: the common call
+// has no such rows, and in line it cost the tcgen05 kernel 2 % of a chunk.
+static __device__ __noinline__ void kv_fill_rows(const KvAttnArgs a, int32_t begin, int32_t end,
+                                                 int thread, int threads)
+{
+    const int64_t rows = begin + a.tokens - end;
+    const int heads = a.c.heads * a.group;
+    const int64_t at = (int64_t)blockIdx.x * threads + thread, step = (int64_t)gridDim.x * threads;
+    // four elements at a time (rows are aligned to that)
+    const int parts = heads * a.c.dim / 4, part = a.out_bf16 ? 8 : 16;
+    for (int64_t i = at; i < rows * parts; i += step) {
+        const int64_t j = i / parts, t = j < begin ? j : j - begin + end;
+        uint8_t* p = static_cast<uint8_t*>(a.out) + t * a.out_stride * (part / 4) + (i - j * parts) * part;
+        if (a.out_bf16)
+            *reinterpret_cast<uint2*>(p) = make_uint2(0u, 0u);
+        else
+            *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (a.lse)
+        for (int64_t i = at; i < rows * heads; i += step) {
+            const int64_t j = i / heads, t = j < begin ? j : j - begin + end;
+            a.lse[t * heads + (i - j * heads)] = -INFINITY;
+        }
+}
+
+// The rows that lie before the first or behind the last request.
+__device__ __forceinline__ void kv_write_other_rows(const KvAttnArgs& a, int thread, int threads)
+{
+    int32_t begin = 0, end = a.reqs ? a.tokens : 0;
+    if (a.q_start) {
+        begin = min(max(a.q_start[0], 0), a.tokens);
+        end = min(max(a.q_start[a.reqs], begin), a.tokens);
+    }
+    if (begin > 0 || end < a.tokens)
+        kv_fill_rows(a, begin, end, thread, threads);
+}
+
 // Whether a request is longer than its table (its end is then cut off).
 __device__ __forceinline__ bool kv_too_long(const KvAttnArgs& a, int r)
 {

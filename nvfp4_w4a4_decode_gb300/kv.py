@@ -193,7 +193,9 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     last tokens; a row sees its own and earlier positions, the last ``window``
     of them when that is not 0.  ``max_q``: the most rows a request has, if
     known (a hint).  ``kernel`` forces KERNEL_KV_ROWS or KERNEL_KV_TILE
-    (bfloat16 q and output only).  Rows that see nothing get zeros and lse = -inf.
+    (bfloat16 q and output only).  Rows that see nothing get zeros and lse = -inf,
+    and so do rows of no request (the padding of a fixed-size batch); in a given
+    ``out`` the latter are left as they are.
     ``workspace``: one of ``kv_attention_workspace`` (None: the cache's own
     for this stream; False: none, long requests are then not cut).  Output
     float32 or bfloat16 (``out_dtype``, by default q's); with ``return_lse``

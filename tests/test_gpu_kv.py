@@ -882,3 +882,68 @@ def test_every_entry_below_zero_is_reported(nv, name, page):
         out, lse = nv.kv_attention(cache, q, broken, ints([300, 40]), return_lse=True, kernel=getattr(nv, name))
         assert nv.device_status(clear=True) == nv.DEVICE_KV_RANGE
         check_attention(out, lse, ref, BF16)
+
+
+# ---- rows of no request ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("name,q_dtype,out_dtype", [("KERNEL_KV_ROWS", BF16, BF16), ("KERNEL_KV_ROWS", FP32, FP32),
+                                                    ("KERNEL_KV_ROWS", BF16, FP32), ("KERNEL_KV_TILE", BF16, BF16)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("counts,before,after", [([1, 1, 1], 0, 5), ([1, 1, 1], 2, 0), ([60, 0, 3], 3, 700),
+                                                 ([0, 0, 0], 0, 9), ([0, 0, 0], 6, 0), ([], 0, 7), ([], 3, 1)])
+def test_rows_of_no_request(nv, name, q_dtype, out_dtype, dim, counts, before, after):
+    """Zeros and -inf in new outputs, whatever their memory held; given outputs keep them."""
+    kernel = getattr(nv, name)
+    seqs = [300 + c for c in counts]
+    cache, table, gen = filled(nv, seqs or [5], 2, dim, 16)
+    table = table[:len(counts)]
+    tokens = before + sum(counts) + after
+    q = torch.randn((tokens, 14, dim), generator=gen, device="cuda").to(q_dtype)
+    start = ints([before + s for s in itertools.accumulate(counts, initial=0)])
+    mine = slice(before, before + sum(counts))
+    ref = attention(cache, q[mine], table, seqs, counts)
+    args = dict(max_q=max(counts, default=0), out_dtype=out_dtype, kernel=kernel)
+    lens = ints(seqs)
+    for _ in range(3):
+        # the call takes memory that held this
+        old = [torch.full((tokens, 14, dim), math.nan, dtype=out_dtype, device="cuda") for _ in range(8)]
+        old += [torch.full((tokens, 14), math.nan, device="cuda") for _ in range(8)]
+        del old
+        out, lse = nv.kv_attention(cache, q, table, lens, start, return_lse=True, **args)
+        if sum(counts):
+            check_attention(out[mine], lse[mine], ref, q_dtype)
+        for rows in (slice(0, before), slice(before + sum(counts), tokens)):
+            assert not out[rows].any() and (lse[rows] == -math.inf).all()
+    given = torch.full((tokens, 16, dim), 7.0, dtype=out_dtype, device="cuda")
+    got, lse2 = nv.kv_attention(cache, q, table, lens, start, out=given[:, 1:15], return_lse=True, **args)
+    assert torch.equal(got[mine], out[mine]) and torch.equal(lse2, lse)
+    given[mine, 1:15] = 7.0
+    assert (given == 7.0).all()
+
+
+def test_rows_without_requests_or_starts(nv):
+    cache, table, gen = filled(nv, [5], 2, 64, 16)
+    q = torch.randn((6, 4, 64), generator=gen, device="cuda")
+    none = ints([])
+    out, lse = nv.kv_attention(cache, q, table[:0], none, return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+    assert nv.kv_attention(cache, q[:0], table[:0], none).shape == (0, 4, 64)
+
+
+def test_padded_step_into_a_linear(nv):
+    """Tables, append, attention and the o linear of a step of 8 rows with 5 requests."""
+    page, reqs, tokens, hq, hkv, dim = 16, 5, 8, 8, 2, 64
+    cache, table, gen = filled(nv, [40, 3, 17, 100, 9], hkv, dim, page)
+    lens = [40, 3, 17, 100, 9]
+    free = ints([cache.num_pages - 1 - i for i in range(3)])
+    for r, n in enumerate(lens):
+        table[r, -(-n // page):] = -1
+    w = nv.pack_weight(torch.randn((128, hq * dim), generator=gen, device="cuda"))
+    rows = torch.randn((tokens, hq + 2 * hkv, dim), generator=gen, device="cuda").to(BF16)
+    t = nv.kv_tables(ints(lens), ints([1] * reqs), free, ints([0]), table, page_size=page, tokens=tokens)
+    nv.kv_append(cache, rows[:, hq:hq + hkv], rows[:, hq + hkv:], t.slots)
+    bad = torch.full((tokens, hq, dim), math.nan, dtype=BF16, device="cuda")
+    del bad
+    y = nv.kv_attention(cache, rows[:, :hq], table, t.seq_len, t.q_start, max_q=1)
+    z = nv.linear(y.flatten(1), cache.v_g, *w)
+    assert torch.isfinite(z).all() and not z[reqs:].any() and z[:reqs].any(1).all()
