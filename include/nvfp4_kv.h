@@ -77,6 +77,8 @@ int64_t nvfp4_kv_page_bytes(int64_t page_size, int64_t num_kv_heads, int64_t hea
  * A page past the end of the free list is entered as -1 and its tokens get
  * slot -1; tokens past max_blocks * P get slot -1, take no page, and seq_len
  * stops there; both set NVFP4_DEVICE_KV_RANGE, and so do more new tokens than `tokens`.
+ * What is written (the outputs, the table) shares no memory with another operand
+ * (NVFP4_ERR_INVALID_ARG): lengths are not updated in place.
  * Lengths may be any int32: positions, q_start and *free_next past 2^31 - 1 are
  * stored as 2^31 - 1.  reqs at most 16384
  * (NVFP4_ERR_UNSUPPORTED), tokens and max_blocks * P below 2^30.  options:
@@ -91,7 +93,7 @@ int nvfp4_kv_tables(const int32_t* kv_len, const int32_t* q_len, int64_t reqs, i
 /*
  * Quantise new keys and values into the cache: token t's heads go to slot
  * slots[t], by the block recipe of nvfp4.h with *k_g and *v_g (every byte has
- * one right value).  Slot -1 is skipped (padding); slots outside the pool are
+ * one right value; k and v are finite, as there).  Slot -1 is skipped (padding); slots outside the pool are
  * skipped and set NVFP4_DEVICE_KV_RANGE.  No two tokens may have the same slot.
  *   k, v      [tokens][num_kv_heads][head_dim], FP32 (16-byte aligned), or
  *             BF16 with NVFP4_FLAG_X_BF16 (8-byte aligned); k_stride and

@@ -42,6 +42,33 @@ int page_shift(int64_t page_size)
     return -1;
 }
 
+// The bytes of a kv_tables operand: `rows` runs of `size` bytes, `stride` apart.
+struct Span {
+    uintptr_t at;
+    int64_t rows, stride, size;
+    bool written;
+};
+
+template <typename T>
+Span vec(const T* p, int64_t n, bool written)
+{
+    return {reinterpret_cast<uintptr_t>(p), 1, 0, n * (int64_t)sizeof(T), written};
+}
+
+// Whether a run of bytes meets any row of the other.
+bool meets(const Span& run, const Span& rows)
+{
+    if (run.size == 0 || rows.size == 0 || rows.rows == 0)
+        return false;
+    const int64_t lo = (int64_t)(run.at - rows.at), hi = lo + run.size;
+    if (hi <= 0 || rows.rows == 1)
+        return hi > 0 && lo < rows.size;
+    // the row that begins at or before lo, and the next
+    const int64_t r = lo > 0 ? lo / rows.stride : 0;
+    return (r < rows.rows && lo < r * rows.stride + rows.size) ||
+           (r + 1 < rows.rows && hi > (r + 1) * rows.stride);
+}
+
 int check_cache(const nvfp4_kv_cache* c, nvfp4::KvCache* out)
 {
     if (c == nullptr)
@@ -98,6 +125,22 @@ int nvfp4_kv_tables(const int32_t* kv_len, const int32_t* q_len, int64_t reqs, i
         !aligned(q_start, 4) || !aligned(slots, 8) || !aligned(positions, 4) ||
         !aligned(free_next, 4))
         return NVFP4_ERR_INVALID_ARG;
+    // CTAs read the lengths and the free list while others write: nothing written may
+    // share memory with another operand
+    const Span table = {reinterpret_cast<uintptr_t>(block_table), max_blocks ? reqs : 0, 4 * table_stride,
+                        4 * max_blocks, true};
+    const Span v[] = {vec(kv_len, reqs, false),         vec(q_len, reqs, false),
+                      vec(free_pages, num_free, false), vec(free_head, 1, false),
+                      vec(seq_len, reqs, true),         vec(q_start, reqs + 1, true),
+                      vec(slots, tokens, true),         vec(positions, tokens, true),
+                      vec(free_next, 1, true)};
+    for (const Span& x : v) {
+        if (meets(x, table))
+            return NVFP4_ERR_INVALID_ARG;
+        for (const Span& y : v)
+            if (x.written && &x != &y && meets(y, x))
+                return NVFP4_ERR_INVALID_ARG;
+    }
     unsigned* status = nullptr;
     const cudaError_t e = nvfp4::device_status_address(&status);
     if (e != cudaSuccess)

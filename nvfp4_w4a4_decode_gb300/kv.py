@@ -164,7 +164,8 @@ def nvfp4_kv_tables(kv_len, q_len, free_pages, free_head, block_table, page_size
     in; ``tokens``: rows of the step (at least ``q_len``'s sum; the rest is
     padding with slot -1).  Returns ``KVTables(seq_len [reqs], q_start
     [reqs + 1], slots [tokens] int64, positions [tokens], free_head [1])``,
-    the last being the free list's next head.  A free list or table that is
+    the last being the free list's next head (new tensors, or ``out``, which shares
+    no memory with the inputs).  A free list or table that is
     too short sets DEVICE_KV_RANGE in ``device_status()``."""
     dev = kv_len.get_device()
     made = (_calls or _binding()).tables(

@@ -137,3 +137,40 @@ def test_binding_wants_device_tensors():
         nv.kv_tables(host, host, host, host, host, page_size=16, tokens=2)
     with pytest.raises(ValueError):
         nv.KVCache(torch.zeros((2, 1, 1152), dtype=torch.uint8), host, host, page_size=16, head_dim=64)
+
+
+CUDA = 3
+
+# every operand of kv_tables in memory of its own: 4 requests, 10 free pages, 6 rows, a table of 4 x 8 of 12
+APART = dict(kv_len=FAKE, q_len=FAKE + 0x100, reqs=4, page=16, free=FAKE + 0x200, num_free=10, head=FAKE + 0x300,
+             table=FAKE + 0x400, stride=12, blocks=8, seq=FAKE + 0x600, start=FAKE + 0x700, slots=FAKE + 0x800,
+             pos=FAKE + 0x900, tokens=6, nxt=FAKE + 0xA00, opts=0, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(seq=APART["kv_len"]), dict(seq=APART["kv_len"] + 12), dict(seq=APART["kv_len"] - 12),  # lengths in place
+    dict(seq=APART["q_len"]), dict(start=APART["kv_len"] - 16), dict(start=APART["q_len"] + 8),
+    dict(slots=APART["kv_len"] - 40), dict(pos=APART["q_len"] + 4), dict(nxt=APART["kv_len"] + 8),
+    dict(seq=APART["free"] + 36), dict(pos=APART["free"] - 20), dict(start=APART["head"] - 16),
+    dict(nxt=APART["free"]), dict(nxt=APART["head"]), dict(seq=APART["start"]), dict(pos=APART["slots"] + 40),
+    dict(nxt=APART["pos"] + 20), dict(nxt=APART["start"] + 16),                  # the last of reqs + 1
+    dict(kv_len=APART["table"]), dict(free=APART["table"] - 36), dict(head=APART["table"] + 28),
+    dict(seq=APART["table"] + 36), dict(pos=APART["table"] + 24), dict(nxt=APART["table"] + 48 * 3 + 28),
+    dict(slots=APART["table"] + 32), dict(kv_len=APART["table"] + 144 - 12)])    # across a gap of 16 bytes
+def test_tables_operands_apart(lib, change):
+    """A written operand that meets another is refused (kernels would read what others write)."""
+    assert lib.nvfp4_kv_tables(*{**APART, **change}.values()) == INVALID
+
+
+def test_tables_operands_that_touch_only(lib):
+    """Neighbours, and vectors in the gap between a table's rows, are as good as apart:
+    such calls come as far as the device, which is not there."""
+    if torch.cuda.is_available():
+        pytest.skip("these addresses are not memory")
+    at = FAKE
+    for change in ({}, dict(seq=APART["kv_len"] + 16), dict(seq=APART["kv_len"] - 16), dict(nxt=APART["start"] + 20),
+                   dict(kv_len=APART["table"] + 32), dict(kv_len=APART["table"] + 144 + 32),
+                   dict(head=APART["table"] - 4), dict(nxt=APART["table"] + 176), dict(q_len=APART["kv_len"]),
+                   dict(table=at + 0x10000, stride=1 << 24, blocks=1 << 24), dict(reqs=0, seq=FAKE),
+                   dict(tokens=0, slots=FAKE, pos=FAKE), dict(blocks=0, seq=APART["table"])):
+        assert lib.nvfp4_kv_tables(*{**APART, **change}.values()) == CUDA
