@@ -133,7 +133,10 @@ class KVCache:
 
 
 def kv_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
-    """A zeroed workspace for attention calls that do not overlap in time."""
+    """A zeroed workspace for attention calls that do not overlap in time, on the current device."""
+    if device is not None:
+        index = torch.device(device).index
+        _current(torch.cuda.current_device() if index is None else index)
     n = int(library().nvfp4_kv_attention_workspace_size(head_dim))
     if n < 0:
         raise Nvfp4Error("nvfp4_kv_attention_workspace_size", -n)
@@ -147,6 +150,17 @@ def _raw_stream(dev: int) -> int:
 
 # the same handle without building a Stream object, where torch offers it
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _current(dev: int) -> int:
+    """``dev``, which must be the current device: the library launches there, with its
+    status word and number of SMs, whatever device the tensors and the stream are of."""
+    if _device() != dev:
+        raise ValueError(f"the tensors are on CUDA device {dev}, which is not the current one ({_device()})")
+    return dev
 
 
 _OUT = {None: 0, torch.float32: 1, torch.bfloat16: 2}
@@ -170,7 +184,7 @@ def nvfp4_kv_tables(kv_len, q_len, free_pages, free_head, block_table, page_size
     dev = kv_len.get_device()
     made = (_calls or _binding()).tables(
         kv_len, q_len, free_pages, free_head, block_table, page_size, tokens, out,
-        FLAG_PDL if pdl else 0, _stream(dev) if dev >= 0 else 0)
+        FLAG_PDL if pdl else 0, _stream(_current(dev)) if dev >= 0 else 0)
     return tuple.__new__(KVTables, made) if out is None else out
 
 
@@ -179,7 +193,7 @@ def nvfp4_kv_append(cache: KVCache, k, v, slots, pdl: bool = False) -> None:
     bfloat16; slices of a projection's rows need no copy) into the cache at
     ``slots`` int64 [tokens] (-1: skipped)."""
     (_calls or _binding()).append(cache._desc, cache._dev, k, v, slots, FLAG_PDL if pdl else 0,
-                                  _stream(cache._dev))
+                                  _stream(_current(cache._dev)))
 
 
 def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
@@ -201,7 +215,7 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     for this stream; False: none, long requests are then not cut).  Output
     float32 or bfloat16 (``out_dtype``, by default q's); with ``return_lse``
     also the natural-log sums [tokens, num_q_heads] float32."""
-    stream = _stream(cache._dev)
+    stream = _stream(_current(cache._dev))
     if workspace is None:
         wp, wn, _keep = cache._workspaces.get(stream) or cache._workspace(stream)
     elif workspace is False:

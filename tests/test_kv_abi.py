@@ -174,3 +174,20 @@ def test_tables_operands_that_touch_only(lib):
                    dict(table=at + 0x10000, stride=1 << 24, blocks=1 << 24), dict(reqs=0, seq=FAKE),
                    dict(tokens=0, slots=FAKE, pos=FAKE), dict(blocks=0, seq=APART["table"])):
         assert lib.nvfp4_kv_tables(*{**APART, **change}.values()) == CUDA
+
+
+def test_calls_want_the_current_device(lib, monkeypatch):
+    """Tensors of another device than the current one are refused before anything is launched."""
+    class Cache:
+        _dev, _desc, _workspaces = 0, cache(), {}
+
+    class Lengths:
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(nv.kv, "_device", lambda: 1)
+    for call in (lambda: nv.kv_append(Cache, None, None, None), lambda: nv.kv_attention(Cache, None, None, None),
+                 lambda: nv.kv_tables(Lengths(), None, None, None, None, 16, 1),
+                 lambda: nv.kv_attention_workspace(64, "cuda:0"), lambda: nv.kv_attention_workspace(64, 0)):
+        with pytest.raises(ValueError, match="current"):
+            call()
