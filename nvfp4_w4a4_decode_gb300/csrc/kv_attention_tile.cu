@@ -14,8 +14,9 @@
 //                      back into it over the scores, at the end the output.  The
 //                      exponentials of 64 scores are taken against the reference
 //                      at hand, with their maximum as a by-product; only where
-//                      that passes the reference by 2^8 is it raised, what was
-//                      accumulated rescaled and the 64 scores done again
+//                      that passes the reference by 2^8 is it raised, by a power of
+//                      two, what was accumulated rescaled (exactly, so that a
+//                      probability is rounded to f16 once) and the 64 scores done again
 //   warps 8..11        decode the cache, 32 tokens each: codes and scales of
 //                      the next block of keys are loaded while this block's are
 //                      converted to f16 and written as 128-byte-swizzled tiles
@@ -583,9 +584,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                 best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
                             if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
                                 break;
-                            const float now = fmaxf(m, best + ref - kLift);
-                            const float by = m == now ? 1.f : ex2(m - now);
-                            m = now;
+                            // The first reference as it comes; then a whole number of powers of
+                            // two at a time, which takes nothing from probabilities already f16.
+                            float by = 0.f;
+                            if (m == -INFINITY) {
+                                m = best - kLift;
+                            } else {
+                                const float steps = floorf(fmaxf(best - kLift, 0.f));
+                                m += steps;
+                                if (steps < 127.f)
+                                    by = __int_as_float((127 - (int)steps) << 23);
+                            }
                             l *= by;
                             // The output so far (its products are complete: this block's scores
                             // were issued after them, and their commit covers both) and the

@@ -947,3 +947,37 @@ def test_padded_step_into_a_linear(nv):
     y = nv.kv_attention(cache, rows[:, :hq], table, t.seq_len, t.q_start, max_q=1)
     z = nv.linear(y.flatten(1), cache.v_g, *w)
     assert torch.isfinite(z).all() and not z[reqs:].any() and z[:reqs].any(1).all()
+
+
+# ---- probabilities of a block whose second half raises the reference --------------------------
+
+@pytest.mark.parametrize("name", ["KERNEL_KV_ROWS", "KERNEL_KV_TILE"])
+def test_probabilities_are_rounded_once(nv, name):
+    """One f16 rounding of each probability (the bound's 2^-11), also where the reference rises
+    inside a block: 128 keys of score 0, 64 about 2^7 times as probable with values of +1, then 16
+    about 2^9 times with values of -1, so that the rest of the two sums is what roundings leave."""
+    n, group, tail = 256 + 64, 64, 64
+    unit = 1.4426950408889634  # scores below are in powers of two
+    cache, table, gen = filled(nv, [n], 1, 64, 16)
+    k = torch.zeros((n, 1, 64), device="cuda")
+    k[128:192, 0, 0] = 6.0
+    k[192:208, 0, 16] = 6.0
+    k[128:192, 0, 1] = k[192:208, 0, 17] = 0.5  # a twelfth, for scores between those of BF16 queries
+    k[208:, 0, 32] = -6.0                     # as good as unseen
+    v = torch.zeros((n, 1, 64), device="cuda")
+    v[128:192], v[192:208] = 1.0, -1.0
+    cache.k_g.fill_(1.0)
+    cache.v_g.fill_(1.0)
+    slots = table[0, :n // 16].long().repeat_interleave(16) * 16 + torch.arange(n, device="cuda") % 16
+    nv.kv_append(cache, k, v, slots)
+    q = torch.zeros((tail, group, 64), device="cuda")
+    rand = lambda: torch.rand((tail, group), generator=gen, device="cuda")  # noqa: E731
+    q[..., 1], q[..., 17] = rand(), rand()
+    q[..., 0] = (7.0 + 0.08 * rand() - 0.5 * q[..., 1]) / 6.0
+    q[..., 16] = (8.93 + 0.069 * rand() - 0.5 * q[..., 17]) / 6.0
+    q[..., 32] = 10.0
+    q = q.to(BF16)
+    # (no workspace: a request's keys stay with one SM, in order)
+    out, lse = nv.kv_attention(cache, q, table, ints([n]), scale=1.0 / unit, return_lse=True,
+                               kernel=getattr(nv, name), workspace=False)
+    check_attention(out, lse, attention(cache, q, table, [n], [tail], 1.0 / unit), BF16)
