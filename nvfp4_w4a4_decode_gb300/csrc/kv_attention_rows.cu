@@ -250,13 +250,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             page = npage;
             more = nmore;
         }
-        if (*abort_flag)  // copies still in flight must land before the CTA ends
-            for (uint32_t k = sent > ST ? sent - ST : 0; k < sent; ++k) {
-                const long long t0 = clock64();
-                while (!mbar_test(smem_u32(&full_bar[k % ST]), (k / ST) & 1) &&
-                       clock64() - t0 < kKvWaitBudget) {
-                }
+        // copies still in flight must land before the CTA ends, also where a wait of another
+        // warp runs out after this one is through
+        for (uint32_t k = sent > ST ? sent - ST : 0; k < sent; ++k) {
+            const long long t0 = clock64();
+            while (!mbar_test(smem_u32(&full_bar[k % ST]), (k / ST) & 1) &&
+                   clock64() - t0 < kKvWaitBudget) {
             }
+        }
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
         if (a.all_rows)
