@@ -161,9 +161,11 @@ typedef struct {
  * The keys of all requests are one list of work that the SMs share equally:
  * a request cut between SMs is joined through the workspace in a fixed order
  * (results do not depend on timing).
- *   workspace  caller-owned, 16-byte aligned, ZERO before its first use; every
- *              completed call leaves it so, and it may serve any number of
- *              calls that do not overlap in time.  With less than
+ *   workspace  caller-owned, 16-byte aligned, its first
+ *              NVFP4_KV_WORKSPACE_ZERO bytes ZERO before its first use (the rest
+ *              is written before it is read); every completed call leaves them so,
+ *              and it may serve any number of calls that do not overlap in time.
+ *              With less than
  *              nvfp4_kv_attention_workspace_size() bytes (NULL with 0) no
  *              request is cut.
  * reqs at most 16384, num_q_heads / num_kv_heads at most 64, tokens below 2^24,
@@ -172,6 +174,7 @@ typedef struct {
 #define NVFP4_KERNEL_KV_ROWS 1u
 #define NVFP4_KERNEL_KV_TILE 2u
 #define NVFP4_FLAG_ALL_ROWS 0x20000u
+#define NVFP4_KV_WORKSPACE_ZERO 4096
 
 int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
                        uint32_t options, void* workspace, size_t workspace_bytes, void* stream);

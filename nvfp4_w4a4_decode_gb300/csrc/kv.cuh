@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/nvfp4_kv.h"
+
 namespace nvfp4 {
 
 // nvfp4_kv_cache as the kernels take it.  Bytes of one (page, kv head), P
@@ -94,7 +96,7 @@ struct KvAttnArgs {
 
 // The workspace's arrival counters (zero between calls; both kernels' lie
 // here), then partial results.
-constexpr int64_t kKvCountBytes = 4096;
+constexpr int64_t kKvCountBytes = NVFP4_KV_WORKSPACE_ZERO;
 
 // Few query rows a request, any dtype.
 int64_t kv_rows_workspace_bytes(int dim);

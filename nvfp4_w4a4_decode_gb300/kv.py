@@ -19,6 +19,7 @@ __all__ = ["KVCache", "KVTables", "kv_page_bytes", "kv_pool", "kv_tables", "kv_a
 
 KERNEL_KV_ROWS = 1
 KERNEL_KV_TILE = 2
+WORKSPACE_ZERO = 4096  # bytes of an attention workspace that start at zero
 DEVICE_KV_RANGE = 2
 
 _p = ctypes.c_void_p
@@ -95,11 +96,12 @@ class KVCache:
     cache as long as a graph that holds its calls.
 
     Attention calls on a stream share a workspace that the cache makes at the
-    first of them (17 MB for each stream used).  A call captured into a graph
-    keeps the workspace of the stream it is captured on, where that has one: a
-    graph that may run at the same time as other attention calls of that stream
-    takes its own (``workspace=kv_attention_workspace(...)``).  The caches of
-    several layers may be given the same one."""
+    first of them (for each stream used 40 MB at head_dim 128, 20 MB at 64, on 152
+    SMs).  A call captured into a graph keeps the workspace of the stream it is
+    captured on, where that has one: a graph that may run at the same time as other
+    attention calls of that stream takes its own
+    (``workspace=kv_attention_workspace(...)``).  Where it has none, the graph holds
+    one of its own.  The caches of several layers may be given the same one."""
 
     def __init__(self, pool, k_g, v_g, page_size: int, head_dim: int):
         if pool.get_device() < 0 or pool.dtype is not torch.uint8 or pool.dim() != 3:
@@ -126,22 +128,25 @@ class KVCache:
         if ws is None:
             t = kv_attention_workspace(self.head_dim, self.device)
             ws = (t.data_ptr(), t.numel(), t)
-            # one made while a graph is captured is zeroed by that graph only
+            # one made while a graph is captured has its counters zeroed by that graph only
             if not torch.cuda.is_current_stream_capturing():
                 self._workspaces[stream] = ws
         return ws
 
 
 def kv_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
-    """A zeroed workspace for attention calls that do not overlap in time, on the current device."""
+    """A workspace for attention calls that do not overlap in time, on the current
+    device (its counters are zero, the rest is whatever the memory held)."""
     if device is not None:
         index = torch.device(device).index
         _current(torch.cuda.current_device() if index is None else index)
     n = int(library().nvfp4_kv_attention_workspace_size(head_dim))
     if n < 0:
         raise Nvfp4Error("nvfp4_kv_attention_workspace_size", -n)
-    return torch.zeros(n, dtype=torch.uint8,
-                       device=device if device is not None else torch.cuda.current_device())
+    ws = torch.empty(n, dtype=torch.uint8,
+                     device=device if device is not None else torch.cuda.current_device())
+    ws[:WORKSPACE_ZERO].zero_()
+    return ws
 
 
 def _raw_stream(dev: int) -> int:

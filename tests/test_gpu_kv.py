@@ -981,3 +981,43 @@ def test_probabilities_are_rounded_once(nv, name):
     out, lse = nv.kv_attention(cache, q, table, ints([n]), scale=1.0 / unit, return_lse=True,
                                kernel=getattr(nv, name), workspace=False)
     check_attention(out, lse, attention(cache, q, table, [n], [tail], 1.0 / unit), BF16)
+
+
+# ---- workspaces -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name,dtype,counts", [("KERNEL_KV_ROWS", BF16, [1, 1, 1]), ("KERNEL_KV_ROWS", FP32, [7, 1, 30]),
+                                               ("KERNEL_KV_TILE", BF16, [200, 1, 150])])
+def test_workspace_holds_anything_but_counters(nv, name, dtype, counts):
+    """A new workspace has its counters zeroed and nothing else written: a graph that makes
+    its own replays no fill of 40 MB.  What the rest held does not matter."""
+    seqs, kernel = [9000, 300, 5000], getattr(nv, name)
+    cache, q, table, out, lse = run_attention(nv, seqs, counts, 8, 2, 128, 64, dtype, kernel=kernel)
+    zero = torch.zeros_like(nv.kv_attention_workspace(128))
+    old = [torch.full_like(zero, 255) for _ in range(3)]           # NaN in FP32
+    del old
+    ws = nv.kv_attention_workspace(128)
+    assert not ws[:4096].any() and (ws[4096:] == 255).all()
+    for w in (ws, zero, ws):
+        o2, l2 = nv.kv_attention(cache, q, table, ints(seqs), starts(counts), max_q=max(counts), return_lse=True,
+                                 workspace=w, kernel=kernel)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+        assert not w[:4096].any()
+
+
+def test_graph_with_a_workspace_of_its_own(nv):
+    """A default capture (its stream has no workspace yet), replayed beside eager calls."""
+    seqs, counts = [9000, 300, 5000], [1, 1, 1]
+    cache, q, table, out, lse = run_attention(nv, seqs, counts, 8, 2, 128, 64)
+    lens, start = ints(seqs), starts(counts)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, got_lse = nv.kv_attention(cache, q, table, lens, start, max_q=1, return_lse=True)
+        again, _ = nv.kv_attention(cache, q, table, lens, start, max_q=1, return_lse=True)
+    for _ in range(4):
+        for x in (got, got_lse, again):
+            x.fill_(math.nan)
+        graph.replay()
+        eager = nv.kv_attention(cache, q, table, lens, start, max_q=1)
+        for x in (got, again, eager):
+            assert torch.equal(x, out)
+        assert torch.equal(got_lse, lse)
