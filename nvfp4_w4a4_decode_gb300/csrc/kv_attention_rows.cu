@@ -367,9 +367,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
         const int32_t p0 = it.q.seq - it.q.nq + kv_token(a, it.row0);
         const int32_t p1 = it.q.seq - it.q.nq + kv_token(a, it.row1 - 1);
         const int32_t all_hi = p0, all_lo = a.window > 0 ? p1 - a.window + 1 : 0;
-        // where 16 tokens are all of keys [key0, seq)
-        const int32_t key0 = Work::first_key(a, it);
-        const uint32_t inner = (uint32_t)max(it.q.seq - 15 - key0, 0);
 
         for (int i = (warp + kWarps - taken * kSub % kWarps) % kWarps; i < units; i += kWarps) {
             const uint32_t group = taken + i / kSub, slot = group % ST;
@@ -465,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 x[h][nt][e] = fmaf(s[h][nt][e], f[nt][e & 1], -m[nt][e & 1]);
-                    if (tok0 < all_lo || tok0 + 16 * HB - 1 > all_hi) {
+                    const bool edge = tok0 < all_lo || tok0 + 16 * HB - 1 > all_hi;
+                    if (edge) {
 #pragma unroll
                         for (int h = 0; h < HB; ++h)
 #pragma unroll
@@ -560,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                                 one[k] = ss[vt * 4 + (g >> 1)];
                             }
                         }
-                        // past the end and before the window may be anything
-                        if ((uint32_t)(tok0 + 16 * h - key0) >= inner) {
+                        if (edge) {  // past the end and before the window may be anything
+                            const int32_t key0 = Work::first_key(a, it);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const int32_t tok = tok0 + 16 * h + v_tok + (k >> 1) * 8 + (k & 1) * v_odd;
