@@ -17,7 +17,9 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 // requests of 4000 tokens, 8 kv heads of 128, 32 rows a request 184 / 233, 48 rows 336 /
 // 230; 16 of 1000, 32 rows 30 / 36, 48 rows 45 / 36; 16 of 8000, 4 kv heads of 64, 32 rows
 // 35 / 53, 64 rows 54 / 52; one of 30000, 8 kv heads of 128, 128 rows 80 / 90, 256 rows
-// 142 / 91; one of 2000, 256 rows 30 / 36.
+// 142 / 91; one of 2000, 256 rows 30 / 36.  (The last lies on the rule's border and goes to
+// the slower one: neither lengths nor windows enter the rule, and one answer holds for
+// all requests of a call, so that single tokens beside a prompt go with the prompt.)
 bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
 {
     return rows > 32 && reqs * heads * rows >= 2048;

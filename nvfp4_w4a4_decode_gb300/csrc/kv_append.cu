@@ -10,8 +10,10 @@
 // hardware's (round to nearest even, saturating, sign kept), two elements an
 // instruction instead of seven comparisons an element.
 //
-// Bound by the bytes read (16384 tokens of 8 heads of 128 in BF16: 20.6 us for 86
-// MB, 4.2 TB/s): the loads of a thread's blocks (of several tokens,
+// 16384 tokens of 8 heads of 128 in BF16: 20.4 us for 86 MB, 4.2 TB/s.  No unit is full
+// then (issue active 55 %, ALU 55 %, DRAM 41 % of its peak; a warp waits most for its
+// loads): it is bound by the latency of loads and of the chain from block maximum to
+// codes, with 28 warps an SM.  So the loads of a thread's blocks (of several tokens,
 // when there are enough of them to fill the SMs) are issued before its slots are
 // looked up.
 #include "../../include/nvfp4_kv.h"

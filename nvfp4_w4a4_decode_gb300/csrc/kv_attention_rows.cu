@@ -40,12 +40,13 @@
 // requests take equal time.  Every wait has a clock budget: one that runs out
 // sets NVFP4_DEVICE_WAIT_TIMEOUT and all waits after it are passed over.
 //
-// What bounds it: for many tokens the issue slots, about 335 warp instructions for 16
-// tokens of a kv head of 128, most of them conversions of codes and scales at
-// half rate, on 14 compute warps an SM (64 requests of 6000..8191 tokens, 8 kv
-// heads, a token each: 112 us, 4.5 TB/s of codes and scales; two of 100000..131071:
-// 60 us, 4.2 TB/s).  For few tokens the chain list - queries - units - join, about 9 us (one
-// request of 1000); a launch's fixed parts measured in cycles: list 2300, queries
+// What bounds it: for many tokens the latency of its chains, with four warps a scheduler.
+// 16 tokens of a kv head of 128 take about 310 warp instructions, most of them conversions
+// of codes and scales at half rate, each waiting for the last; issue is active 49 % of
+// the time, ALU 44 %, DRAM 56 %, and the registers allow no more warps (64 requests of
+// 6000..8191 tokens, 8 kv heads, a token each: 110 us, 4.6 TB/s of codes and scales; two of
+// 100000..131071: 59.5 us, 4.3 TB/s).  For few tokens the chain list - queries - units -
+// join, about 9.5 us (one request of 1000); a launch's fixed parts measured in cycles: list 2300, queries
 // 1700, first units 2800, warps' join 1400, part and counter 2000, CTAs' join 5000.
 #include "formats.cuh"
 #include "kv_work.cuh"

@@ -33,8 +33,8 @@
 // (about 2600 cycles a block beside the 1024 of its products, of which the other
 // tile's run meanwhile) and shared memory, which the products of both tiles and the
 // decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
-// cycles.  2048 queries of 32 heads on 32049 keys: 762 us, 1.37 PFLOP/s; four prompts of
-// 2185..3879 tokens and 64 heads: 713 us, 0.95 PFLOP/s (an item's queries, first
+// cycles.  2048 queries of 32 heads on 32049 keys: 768 us, 1.36 PFLOP/s; four prompts of
+// 2185..3879 tokens and 64 heads: 723 us, 0.94 PFLOP/s (an item's queries, first
 // block, masked last block and output add about 9 us to its keys).
 //
 // Waits have clock budgets; when one runs out NVFP4_DEVICE_WAIT_TIMEOUT is set,

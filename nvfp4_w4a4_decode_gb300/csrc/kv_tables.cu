@@ -7,10 +7,10 @@
 // or a grid-wide wait -- keeps the sums in shared memory and takes its share
 // of the pages and tokens, finding a token's request by bisection.  Only
 // entries of pages that are new are written and only older ones are read, so
-// no order between CTAs is needed.  Lengths may be anything: sums stop at 2^32 - 1 instead
-// of wrapping (64-bit sums: 3.25 us instead of 3.1 for 8 requests).  Bound by latency, not by its few bytes: 8
-// requests of a token 3.1 us, 1000 requests with 261000 tokens (3.1 MB written)
-// 6.9 us, the launch included.
+// no order between CTAs is needed.  Lengths may be anything: sums stop at 2^32 - 1
+// instead of wrapping (64-bit sums: 3.25 us instead of 3.1 for 8 requests).  Bound by
+// latency, not by its few bytes: 8 requests of a token 3.1 us, 1000 requests with
+// 261000 tokens (3.1 MB written) 7.1 us, the launch included.
 #include "../../include/nvfp4_kv.h"
 #include "kv.cuh"
 #include "launch_cache.cuh"

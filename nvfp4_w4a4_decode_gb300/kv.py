@@ -211,8 +211,9 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     appended) included; ``q_start`` int32 [reqs + 1]: each request's first
     query row (None: the same number each).  A request's query rows are its
     last tokens; a row sees its own and earlier positions, the last ``window``
-    of them when that is not 0.  ``max_q``: the most rows a request has, if
-    known (a hint).  ``kernel`` forces KERNEL_KV_ROWS or KERNEL_KV_TILE
+    of them when that is not 0.  ``max_q``: the most rows a request has (a hint
+    for the choice of kernel, worth giving: without it a call with ``q_start`` is
+    taken for one request of all rows, right but slow for single tokens).  ``kernel`` forces KERNEL_KV_ROWS or KERNEL_KV_TILE
     (bfloat16 q and output only).  Rows that see nothing get zeros and lse = -inf,
     and so do rows of no request (the padding of a fixed-size batch); in a given
     ``out`` the latter are left as they are.
