@@ -1,7 +1,9 @@
 /*
  * nvfp4_kv.h -- C ABI of the paged NVFP4 key/value cache: block tables and
- * slot maps built on the GPU, the quantising append, and attention over the
- * cache (single tokens, a few tokens a request, chunks and whole prompts).
+ * slot maps built on the GPU, the quantising append (with the position rotation
+ * on the way, where wanted), and attention over the cache (single tokens, a few
+ * tokens a request, chunks and whole prompts; requests that share a prefix;
+ * cross attention to an encoder's states).
  *
  * The cache holds keys and values in the library's NVFP4 (nvfp4.h): E2M1 codes
  * two per byte, one E4M3 scale per 16 consecutive elements of the head
@@ -107,6 +109,50 @@ int nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* k, int64_t k_stride
                     void* stream);
 
 /*
+ * The append with the position rotation on the way: keys and queries are turned
+ * by their token's angles, then keys and values quantised into the cache as by
+ * nvfp4_kv_append and the queries written out.
+ *
+ * The first rotary_dim elements of a head are pairs (a, b), at i and i +
+ * rotary_dim / 2 (interleaved: at 2 i and 2 i + 1), i < rotary_dim / 2.  With
+ * (c, s) = (row[i], row[rotary_dim / 2 + i]) of the row positions[t] of `rotary`:
+ *     a' = a c - b s,   b' = b c + a s
+ * in FP32, each product and the difference or sum rounded by itself: every bit of a'
+ * and b' has one right value, and so has every byte of the cache (the keys are not
+ * rounded in between; k, v and the angles are finite).  Queries are rounded once, to
+ * their own type.  The rest of a head, and the values, are not turned.
+ * Rows with slot -1 are not appended (padding).  Rows with a position outside
+ * [0, rotary_rows) are not appended either, their queries are zeros, and unless their slot is
+ * -1 they set NVFP4_DEVICE_KV_RANGE; so do slots outside the pool, as in nvfp4_kv_append.
+ * No two tokens may have the same slot.
+ */
+typedef struct {
+    const void* q;            /* [tokens][num_q_heads][head_dim], the type and alignment of k */
+    int64_t q_stride;         /* elements from token to token, a multiple of 4, here and below */
+    int64_t num_q_heads;      /* 0: no queries (q and q_out are then not used); any number up to
+                                 65536, not only multiples of the kv heads */
+    void* q_out;              /* like q; q itself (the same address and stride) turns it in place,
+                                 any other overlap with q, k, v or the rest is refused */
+    int64_t q_out_stride;
+    const void* k;            /* k, v as in nvfp4_kv_append */
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    int64_t tokens;
+    const int64_t* slots;     /* int64 [tokens] */
+    const int32_t* positions; /* int32 [tokens] */
+    const float* rotary;      /* FP32 [rotary_rows][rotary_dim], 16-byte aligned */
+    int64_t rotary_rows;
+    int64_t rotary_stride;    /* elements from row to row, a multiple of 4 */
+    int32_t rotary_dim;       /* a multiple of 32 (else NVFP4_ERR_UNSUPPORTED), at most head_dim */
+    int32_t interleaved;      /* 0 or 1 */
+} nvfp4_kv_rotary_args;
+
+/* options: NVFP4_FLAG_X_BF16 (q, k, v and q_out), NVFP4_FLAG_PDL.  One kernel. */
+int nvfp4_kv_append_rotary(const nvfp4_kv_cache* cache, const nvfp4_kv_rotary_args* args,
+                           uint32_t options, void* stream);
+
+/*
  * Attention of the step's queries over the cache.  Query row t belongs to
  * request r with q_start[r] <= t < q_start[r + 1] and has position
  * p = seq_len[r] - (q_start[r + 1] - t); it sees the keys j of its request
@@ -182,6 +228,57 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
 /* Workspace bytes of nvfp4_kv_attention on the current device for this
  * head_dim (any shape), or minus a status code.  Host only. */
 int64_t nvfp4_kv_attention_workspace_size(int64_t head_dim);
+
+/*
+ * Cross attention: every query row of request r sees all seq_len[r] tokens that the
+ * cache holds for it (the states of an encoder, say), however many rows it has; with
+ * seq_len[r] = 0 they get zeros and lse = -inf.  All else, the workspace too, as for
+ * nvfp4_kv_attention; args->window is 0 (else NVFP4_ERR_INVALID_ARG).  One kernel.
+ */
+int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
+                             uint32_t options, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Causal attention of requests that share prefixes, each prefix read and multiplied
+ * once for all rows of its requests.  Group g is the requests group_start[g] up to
+ * group_start[g + 1]; their first prefix_len[g] tokens are the same and lie on the pages of
+ * row g of the prefixes' table.  Lengths and positions count them: in args, seq_len[r] is the
+ * whole length, and entry b of a request's own row of args->block_table holds the tokens
+ * b * page_size and on.  Query rows see what they see in nvfp4_kv_attention, with key j of
+ * request r read
+ *     on the prefix's pages for j < prefix_len[g], on the request's own pages from there on
+ * if all rows of r lie behind the prefix (seq_len[r] - rows >= prefix_len[g]); entries of
+ * its own pages wholly before prefix_len[g] are not looked up then.  A request with a row
+ * inside the prefix (an empty one, too) shares nothing: all of its keys are read on its own
+ * pages, as by nvfp4_kv_attention.  Requests of no group share nothing.  A prefix need not
+ * end with a page (the rest of its last page is a request's own page then), and may be
+ * empty (0 or less).
+ * args->window is 0 (else NVFP4_ERR_INVALID_ARG).  Options, workspace, statuses and what is
+ * done about bad entries as for nvfp4_kv_attention, for both tables; the kernel choice
+ * of the options is that of both passes.
+ */
+typedef struct {
+    const int32_t* block_table; /* int32 [groups][table_stride] */
+    int64_t table_stride;
+    int64_t max_blocks;         /* entries of a row that may be used */
+    const int32_t* prefix_len;  /* int32 [groups] */
+    const int32_t* group_start; /* int32 [groups + 1], ascending, or NULL: one group of all
+                                   requests (groups is 1 then) */
+    int64_t groups;             /* at most 16384; 0: nothing is shared */
+    void* scratch;              /* nvfp4_kv_shared_scratch_size() bytes, 16-byte aligned, any contents,
+                                   not used by another call at the same time */
+    size_t scratch_bytes;
+} nvfp4_kv_prefixes;
+
+/* Two kernels: the prefixes, then the requests' own keys and the join. */
+int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
+                              const nvfp4_kv_prefixes* prefixes, uint32_t options,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of nvfp4_kv_prefixes.scratch, or minus a status code.  Host only. */
+int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim,
+                                     int64_t reqs);
 
 #ifdef __cplusplus
 }

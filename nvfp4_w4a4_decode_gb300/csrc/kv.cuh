@@ -67,6 +67,83 @@ struct KvAppendArgs {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream, bool pdl);
 
+struct KvRotaryArgs {
+    KvCache c;
+    const void* q;
+    void* q_out;
+    const void* k;
+    const void* v;
+    int64_t q_stride, q_out_stride, k_stride, v_stride;  // elements
+    int32_t q_heads;
+    const int64_t* slots;
+    const int32_t* positions;
+    int64_t tokens;
+    const float* rotary;  // rows of rot / 2 cosines, then rot / 2 sines
+    int64_t rotary_rows, rotary_stride;
+    int32_t rot;  // a multiple of 32, at most dim
+    int32_t interleaved;
+    unsigned* status;
+};
+
+cudaError_t launch_kv_rotary(const KvRotaryArgs& a, bool bf16, cudaStream_t stream, bool pdl);
+
+// Which keys a query row of a request sees (position p of the row, seq keys in all).
+enum class KvSees {
+    kCausal,  // j <= p, with a window j > p - W
+    kAll,     // j < seq: cross attention, and the prefix that a group's requests share
+    kBehind,  // KvShared::first of its request <= j <= p: a request's own keys
+};
+
+// The two passes of requests that share prefixes.  The first (kAll) takes a group for a
+// request: its rows are those of the group's requests, its table the prefix's.  It leaves
+// every row's sum of p V, its reference (log2) and its sum of p, and which keys each
+// request still has to see.  An item cut between CTAs is not joined there (one SM would
+// read the parts of 256 rows while the others wait): the second pass (kBehind) adds a row's
+// parts to its own sums, in CTA order.
+struct KvShared {
+    float* rows;         // [tokens][query heads][D]: of items that were not cut (null: no such call)
+    float2* stats;       // [tokens][query heads]
+    float* parts;        // [part_total][D]: of the cut ones, two places of an item's rows a CTA
+    float2* part_stats;  // [part_total]
+    int32_t* where;      // [tokens][query heads]: 0, or parts << kKvPartBits | row of the first in `parts`
+    int32_t* first;      // [requests]: the request's first own key, 0 where it shares none
+    int64_t part_total;  // rows of `parts`
+    int32_t item_rows;   // query rows of an item of the first pass
+    // first pass only: the requests
+    const int32_t* group_start;  // first request of each group, or null: one group of all
+    const int32_t* seq_len;
+    int32_t reqs;
+    int64_t cap;       // keys that a request's own table has room for
+};
+
+// Rows of KvShared::parts: two items of 256 rows on each SM, or of 32 rows for 512 CTAs.
+constexpr int kKvPartBits = 17;
+constexpr int64_t kv_part_total(int sms)
+{
+    return (int64_t)(sms > 64 ? sms : 64) * 512;
+}
+
+// Part k's row of the parts that `where` names: the first lies in its CTA's second place, the
+// others in the first places of the CTAs behind.
+__device__ __forceinline__ int64_t kv_part_row(int32_t where, int k, int item_rows)
+{
+    return (where & ((1 << kKvPartBits) - 1)) + (k ? (int64_t)(2 * k - 1) * item_rows : 0);
+}
+
+// What the first pass has written for a row, and the number of its parts.  Starts that go back
+// (the rows of a request are then not those of its group) may leave anything there: such an
+// entry is not followed.
+__device__ __forceinline__ int32_t kv_where(const KvShared& s, int64_t row, int& parts)
+{
+    int32_t w = s.where[row];
+    parts = w >> kKvPartBits;
+    if (w < 0 || (parts > 0 && kv_part_row(w, parts - 1, s.item_rows) >= s.part_total))
+        w = parts = 0;
+    if (parts == 0)
+        w = 0, parts = 1;
+    return w;
+}
+
 struct KvAttnArgs {
     KvCache c;
     const void* q;
@@ -89,6 +166,7 @@ struct KvAttnArgs {
     float* lse;
     int32_t q_bf16, out_bf16;
     int32_t all_rows;  // rows of no request are written too
+    KvShared shared;
     float* part;      // partial results of items cut between CTAs (null: none is cut)
     unsigned* count;  // arrival counters, zero between calls
     unsigned* status;
@@ -100,11 +178,15 @@ constexpr int64_t kKvCountBytes = NVFP4_KV_WORKSPACE_ZERO;
 
 // Few query rows a request, any dtype.
 int64_t kv_rows_workspace_bytes(int dim);
+int kv_rows_item_rows(const KvAttnArgs& a);  // query rows of an item of the launch for these arguments
+template <KvSees S>
 cudaError_t launch_kv_rows(const KvAttnArgs& a, void* workspace, int64_t workspace_bytes,
                            cudaStream_t stream, bool pdl);
 
 // Many query rows a request (tcgen05); BF16 queries and outputs only.
 int64_t kv_tile_workspace_bytes(int dim);
+int kv_tile_item_rows();
+template <KvSees S>
 cudaError_t launch_kv_tile(const KvAttnArgs& a, void* workspace, int64_t workspace_bytes,
                            cudaStream_t stream, bool pdl);
 

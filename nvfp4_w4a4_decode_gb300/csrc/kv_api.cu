@@ -6,8 +6,11 @@
 #include "../../include/nvfp4_kv.h"
 #include "kernels.cuh"
 #include "kv.cuh"
+#include "launch_cache.cuh"
 
 namespace {
+
+using nvfp4::KvSees;
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
@@ -23,6 +26,11 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
 {
     return rows > 32 && reqs * heads * rows >= 2048;
+}
+
+int sm_count()
+{
+    return nvfp4::device_sm_count(nvfp4::current_device());
 }
 
 bool aligned(const void* p, uintptr_t a)
@@ -44,7 +52,7 @@ int page_shift(int64_t page_size)
     return -1;
 }
 
-// The bytes of a kv_tables operand: `rows` runs of `size` bytes, `stride` apart.
+// The bytes of an operand: `rows` runs of `size` bytes, `stride` apart.
 struct Span {
     uintptr_t at;
     int64_t rows, stride, size;
@@ -71,6 +79,33 @@ bool meets(const Span& run, const Span& rows)
            (r + 1 < rows.rows && hi > (r + 1) * rows.stride);
 }
 
+// Rows of `size` bytes of a tensor with token rows.
+Span token_rows(const void* p, int64_t tokens, int64_t stride, int64_t elements, int item, bool written)
+{
+    return {reinterpret_cast<uintptr_t>(p), tokens, stride * item, elements * item, written};
+}
+
+// Whether two tensors with token rows share memory.  Rows of one stride (slices of one
+// projection's rows) by their place in the stride, else by the ranges they lie in.
+bool rows_meet(const Span& x, const Span& y)
+{
+    if (x.rows == 0 || y.rows == 0 || x.size == 0 || y.size == 0)
+        return false;
+    const uintptr_t x_end = x.at + (uintptr_t)((x.rows - 1) * x.stride + x.size);
+    const uintptr_t y_end = y.at + (uintptr_t)((y.rows - 1) * y.stride + y.size);
+    if (x_end <= y.at || y_end <= x.at)
+        return false;
+    if (x.rows == 1)
+        return meets(x, y);
+    if (y.rows == 1)
+        return meets(y, x);
+    if (x.stride != y.stride)
+        return true;
+    const int64_t d = (int64_t)(y.at - x.at) % x.stride;
+    const int64_t place = d < 0 ? d + x.stride : d;  // of y's row in x's
+    return place < x.size || place + y.size > x.stride;
+}
+
 int check_cache(const nvfp4_kv_cache* c, nvfp4::KvCache* out)
 {
     if (c == nullptr)
@@ -87,6 +122,93 @@ int check_cache(const nvfp4_kv_cache* c, nvfp4::KvCache* out)
     *out = {static_cast<uint8_t*>(c->pool), c->k_g, c->v_g, c->num_pages, c->page_stride,
             page_shift(c->page_size), c->num_kv_heads, c->head_dim};
     return NVFP4_OK;
+}
+
+// The checks of an attention call, and its arguments as the kernels take them; `any`: there is
+// something to do.
+int check_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args, uint32_t options,
+                    const void* workspace, size_t workspace_bytes, nvfp4::KvAttnArgs* to, bool* any)
+{
+    nvfp4::KvAttnArgs& a = *to;
+    *any = false;
+    const int st = check_cache(cache, &a.c);
+    if (st != NVFP4_OK)
+        return st;
+    if (args == nullptr || (options & ~(uint32_t)(NVFP4_KERNEL_MASK | NVFP4_FLAG_PDL |
+                                                  NVFP4_FLAG_X_BF16 | NVFP4_FLAG_Y_BF16 |
+                                                  NVFP4_FLAG_ALL_ROWS)) != 0)
+        return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_kv_attention_args& r = *args;
+    if (workspace == nullptr ? workspace_bytes != 0 : !aligned(workspace, 16))
+        return NVFP4_ERR_INVALID_ARG;
+    if (r.reqs < 0 || r.tokens < 0 || r.num_q_heads < 1 || (r.num_q_heads % a.c.heads) != 0 ||
+        r.max_blocks < 0 || r.table_stride < r.max_blocks || r.max_q < 0 || r.window < 0 ||
+        !(r.scale == r.scale) || (r.q_start == nullptr && r.reqs > 0 && (r.tokens % r.reqs) != 0))
+        return NVFP4_ERR_INVALID_ARG;
+    if (r.num_q_heads / a.c.heads > nvfp4::kKvMaxGroup || r.reqs > nvfp4::kKvMaxReqs ||
+        r.tokens >= kMaxTokens / nvfp4::kKvMaxGroup ||
+        r.max_blocks >= (kMaxTokens >> a.c.page_shift))
+        return NVFP4_ERR_UNSUPPORTED;
+    const uint32_t kern = options & NVFP4_KERNEL_MASK;
+    const bool all_bf16 = (options & NVFP4_FLAG_X_BF16) && (options & NVFP4_FLAG_Y_BF16);
+    if (kern != NVFP4_KERNEL_AUTO && kern != NVFP4_KERNEL_KV_ROWS &&
+        !(kern == NVFP4_KERNEL_KV_TILE && all_bf16))
+        return NVFP4_ERR_UNSUPPORTED;
+    const bool all_rows = (options & NVFP4_FLAG_ALL_ROWS) != 0;
+    if (r.tokens == 0 || (r.reqs == 0 && !all_rows))
+        return NVFP4_OK;
+    const bool q_bf16 = (options & NVFP4_FLAG_X_BF16) != 0;
+    const bool out_bf16 = (options & NVFP4_FLAG_Y_BF16) != 0;
+    const int64_t row = r.num_q_heads * a.c.dim;
+    if (r.q == nullptr || r.out == nullptr || (r.reqs > 0 && r.seq_len == nullptr) ||
+        (r.reqs > 0 && r.max_blocks > 0 && r.block_table == nullptr) || !aligned(r.q, q_bf16 ? 8 : 16) ||
+        !aligned(r.out, out_bf16 ? 8 : 16) || !aligned(r.block_table, 4) ||
+        !aligned(r.seq_len, 4) || !aligned(r.q_start, 4) || !aligned(r.lse, 4) ||
+        (r.q_stride % 4) != 0 || (r.out_stride % 4) != 0 ||
+        (r.tokens > 1 && (r.q_stride < row || r.out_stride < row)))
+        return NVFP4_ERR_INVALID_ARG;
+    a.q = r.q;
+    a.q_stride = r.q_stride;
+    a.table = r.block_table;
+    a.table_stride = r.table_stride;
+    a.max_blocks = (int32_t)r.max_blocks;
+    a.seq_len = r.seq_len;
+    a.q_start = r.q_start;
+    a.q_per_req = (int32_t)(r.q_start || r.reqs == 0 ? 0 : r.tokens / r.reqs);
+    a.reqs = (int32_t)r.reqs;
+    a.tokens = (int32_t)r.tokens;
+    a.max_q = (int32_t)(r.max_q < r.tokens ? r.max_q : r.tokens);
+    a.group = (int32_t)(r.num_q_heads / a.c.heads);
+    a.group_magic = (uint32_t)(((uint64_t)1 << 32) / (uint64_t)a.group + 1);
+    a.scale_log2 = r.scale * 1.4426950408889634f;
+    // a window past every length is none
+    a.window = r.window >= kMaxTokens ? 0 : (int32_t)r.window;
+    a.out = r.out;
+    a.out_stride = r.out_stride;
+    a.lse = r.lse;
+    a.q_bf16 = q_bf16;
+    a.out_bf16 = out_bf16;
+    a.all_rows = all_rows;
+    *any = true;
+    return NVFP4_OK;
+}
+
+bool takes_tile(const nvfp4::KvAttnArgs& a, uint32_t options)
+{
+    const uint32_t kern = options & NVFP4_KERNEL_MASK;
+    return kern == NVFP4_KERNEL_KV_TILE || (kern == NVFP4_KERNEL_AUTO && a.q_bf16 && a.out_bf16 &&
+                                            use_tile(a.reqs, a.c.heads, (int64_t)a.max_q * a.group));
+}
+
+template <KvSees S>
+int launch_attention(nvfp4::KvAttnArgs& a, uint32_t options, void* workspace, size_t workspace_bytes,
+                     void* stream)
+{
+    if (a.status == nullptr && nvfp4::device_status_address(&a.status) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+    const auto launch = takes_tile(a, options) ? nvfp4::launch_kv_tile<S> : nvfp4::launch_kv_rows<S>;
+    return from_cuda(launch(a, workspace, (int64_t)workspace_bytes, static_cast<cudaStream_t>(stream),
+                            (options & NVFP4_FLAG_PDL) != 0));
 }
 
 }  // namespace
@@ -187,6 +309,80 @@ int nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* k, int64_t k_stride
                                              (options & NVFP4_FLAG_PDL) != 0));
 }
 
+int nvfp4_kv_append_rotary(const nvfp4_kv_cache* cache, const nvfp4_kv_rotary_args* args,
+                           uint32_t options, void* stream)
+{
+    nvfp4::KvRotaryArgs a = {};
+    const int st = check_cache(cache, &a.c);
+    if (st != NVFP4_OK)
+        return st;
+    if (args == nullptr || (options & ~(uint32_t)(NVFP4_FLAG_PDL | NVFP4_FLAG_X_BF16)) != 0)
+        return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_kv_rotary_args& r = *args;
+    if (r.tokens < 0 || r.num_q_heads < 0 || r.rotary_rows < 0 || r.rotary_dim < 1 ||
+        r.rotary_dim > a.c.dim || r.rotary_stride < 0 || (r.interleaved & ~1) != 0)
+        return NVFP4_ERR_INVALID_ARG;
+    const int64_t pieces = (r.num_q_heads + a.c.heads) * (a.c.dim / 16);  // threads a token, at most
+    if (r.tokens >= kMaxTokens || r.num_q_heads > 65536 || (r.rotary_dim % 32) != 0 ||
+        r.rotary_rows > INT32_MAX || r.tokens * pieces >= ((int64_t)1 << 37))
+        return NVFP4_ERR_UNSUPPORTED;
+    if (r.tokens == 0)
+        return NVFP4_OK;
+    const bool bf16 = (options & NVFP4_FLAG_X_BF16) != 0, with_q = r.num_q_heads > 0;
+    const uintptr_t to = bf16 ? 8 : 16;
+    const int64_t row = (int64_t)a.c.heads * a.c.dim, q_row = r.num_q_heads * a.c.dim;
+    if (r.k == nullptr || r.v == nullptr || r.slots == nullptr || r.positions == nullptr ||
+        (r.rotary_rows > 0 && r.rotary == nullptr) || !aligned(r.k, to) || !aligned(r.v, to) ||
+        !aligned(r.slots, 8) || !aligned(r.positions, 4) || !aligned(r.rotary, 16) ||
+        (r.rotary_stride % 4) != 0 || (r.rotary_rows > 1 && r.rotary_stride < r.rotary_dim) ||
+        (r.k_stride % 4) != 0 || (r.v_stride % 4) != 0 ||
+        (r.tokens > 1 && (r.k_stride < row || r.v_stride < row)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (with_q) {
+        if (r.q == nullptr || r.q_out == nullptr || !aligned(r.q, to) || !aligned(r.q_out, to) ||
+            (r.q_stride % 4) != 0 || (r.q_out_stride % 4) != 0 ||
+            (r.tokens > 1 && (r.q_stride < q_row || r.q_out_stride < q_row)))
+            return NVFP4_ERR_INVALID_ARG;
+        // what other threads read meanwhile is not written over
+        const int item = bf16 ? 2 : 4;
+        const Span out = token_rows(r.q_out, r.tokens, r.q_out_stride, q_row, item, true);
+        const bool in_place = r.q_out == r.q && (r.q_out_stride == r.q_stride || r.tokens == 1);
+        const Span pool = {reinterpret_cast<uintptr_t>(a.c.pool), a.c.num_pages, a.c.page_stride,
+                           nvfp4_kv_page_bytes(cache->page_size, a.c.heads, a.c.dim), true};
+        if ((!in_place && rows_meet(out, token_rows(r.q, r.tokens, r.q_stride, q_row, item, false))) ||
+            rows_meet(out, token_rows(r.k, r.tokens, r.k_stride, row, item, false)) ||
+            rows_meet(out, token_rows(r.v, r.tokens, r.v_stride, row, item, false)) ||
+            rows_meet(out, pool) || meets(vec(r.slots, r.tokens, false), out) ||
+            meets(vec(r.positions, r.tokens, false), out) || meets(vec(a.c.k_g, 1, false), out) ||
+            meets(vec(a.c.v_g, 1, false), out) ||
+            rows_meet(out, token_rows(r.rotary, r.rotary_rows, r.rotary_stride, r.rotary_dim, 4, false)))
+            return NVFP4_ERR_INVALID_ARG;
+    }
+    if (nvfp4::device_status_address(&a.status) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+    if (with_q) {
+        a.q = r.q;
+        a.q_out = r.q_out;
+        a.q_stride = r.q_stride;
+        a.q_out_stride = r.q_out_stride;
+        a.q_heads = (int32_t)r.num_q_heads;
+    }
+    a.k = r.k;
+    a.v = r.v;
+    a.k_stride = r.k_stride;
+    a.v_stride = r.v_stride;
+    a.tokens = r.tokens;
+    a.slots = r.slots;
+    a.positions = r.positions;
+    a.rotary = r.rotary;
+    a.rotary_rows = r.rotary_rows;
+    a.rotary_stride = r.rotary_stride;
+    a.rot = r.rotary_dim;
+    a.interleaved = r.interleaved;
+    return from_cuda(nvfp4::launch_kv_rotary(a, bf16, static_cast<cudaStream_t>(stream),
+                                             (options & NVFP4_FLAG_PDL) != 0));
+}
+
 int64_t nvfp4_kv_attention_workspace_size(int64_t head_dim)
 {
     if (head_dim < 1)
@@ -202,72 +398,91 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_arg
                        uint32_t options, void* workspace, size_t workspace_bytes, void* stream)
 {
     nvfp4::KvAttnArgs a = {};
-    const int st = check_cache(cache, &a.c);
+    bool any;
+    const int st = check_attention(cache, args, options, workspace, workspace_bytes, &a, &any);
+    return st != NVFP4_OK || !any
+               ? st
+               : launch_attention<KvSees::kCausal>(a, options, workspace, workspace_bytes, stream);
+}
+
+int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
+                             uint32_t options, void* workspace, size_t workspace_bytes, void* stream)
+{
+    nvfp4::KvAttnArgs a = {};
+    bool any;
+    if (args != nullptr && args->window != 0)
+        return NVFP4_ERR_INVALID_ARG;
+    const int st = check_attention(cache, args, options, workspace, workspace_bytes, &a, &any);
+    return st != NVFP4_OK || !any
+               ? st
+               : launch_attention<KvSees::kAll>(a, options, workspace, workspace_bytes, stream);
+}
+
+int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim, int64_t reqs)
+{
+    if (tokens < 0 || num_q_heads < 1 || head_dim < 1 || reqs < 0)
+        return -NVFP4_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || tokens >= kMaxTokens || num_q_heads > (1 << 22) ||
+        reqs > nvfp4::kKvMaxReqs)
+        return -NVFP4_ERR_UNSUPPORTED;
+    const int64_t rows = tokens * num_q_heads, parts = nvfp4::kv_part_total(sm_count());
+    return (rows + parts) * (head_dim * 4 + 8) + (rows + reqs) * 4;
+}
+
+int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
+                              const nvfp4_kv_prefixes* prefixes, uint32_t options, void* workspace,
+                              size_t workspace_bytes, void* stream)
+{
+    nvfp4::KvAttnArgs a = {};
+    bool any;
+    if (prefixes == nullptr || (args != nullptr && args->window != 0))
+        return NVFP4_ERR_INVALID_ARG;
+    const int st = check_attention(cache, args, options, workspace, workspace_bytes, &a, &any);
     if (st != NVFP4_OK)
         return st;
-    if (args == nullptr || (options & ~(uint32_t)(NVFP4_KERNEL_MASK | NVFP4_FLAG_PDL |
-                                                  NVFP4_FLAG_X_BF16 | NVFP4_FLAG_Y_BF16 |
-                                                  NVFP4_FLAG_ALL_ROWS)) != 0)
+    const nvfp4_kv_prefixes& p = *prefixes;
+    if (p.groups < 0 || p.max_blocks < 0 || p.table_stride < p.max_blocks ||
+        (p.group_start == nullptr && p.groups > 1))
         return NVFP4_ERR_INVALID_ARG;
-    const nvfp4_kv_attention_args& r = *args;
-    if (workspace == nullptr ? workspace_bytes != 0 : !aligned(workspace, 16))
-        return NVFP4_ERR_INVALID_ARG;
-    if (r.reqs < 0 || r.tokens < 0 || r.num_q_heads < 1 || (r.num_q_heads % a.c.heads) != 0 ||
-        r.max_blocks < 0 || r.table_stride < r.max_blocks || r.max_q < 0 || r.window < 0 ||
-        !(r.scale == r.scale) || (r.q_start == nullptr && r.reqs > 0 && (r.tokens % r.reqs) != 0))
-        return NVFP4_ERR_INVALID_ARG;
-    if (r.num_q_heads / a.c.heads > nvfp4::kKvMaxGroup || r.reqs > nvfp4::kKvMaxReqs ||
-        r.tokens >= kMaxTokens / nvfp4::kKvMaxGroup ||
-        r.max_blocks >= (kMaxTokens >> a.c.page_shift))
+    if (p.groups > nvfp4::kKvMaxReqs || p.max_blocks >= (kMaxTokens >> a.c.page_shift))
         return NVFP4_ERR_UNSUPPORTED;
-    const uint32_t kern = options & NVFP4_KERNEL_MASK;
-    const bool all_bf16 = (options & NVFP4_FLAG_X_BF16) && (options & NVFP4_FLAG_Y_BF16);
-    if (kern != NVFP4_KERNEL_AUTO && kern != NVFP4_KERNEL_KV_ROWS &&
-        !(kern == NVFP4_KERNEL_KV_TILE && all_bf16))
-        return NVFP4_ERR_UNSUPPORTED;
-    const bool all_rows = (options & NVFP4_FLAG_ALL_ROWS) != 0;
-    if (r.tokens == 0 || (r.reqs == 0 && !all_rows))
+    if (!any)
         return NVFP4_OK;
-    const bool q_bf16 = (options & NVFP4_FLAG_X_BF16) != 0;
-    const bool out_bf16 = (options & NVFP4_FLAG_Y_BF16) != 0;
-    const int64_t row = r.num_q_heads * a.c.dim;
-    if (r.q == nullptr || r.out == nullptr || (r.reqs > 0 && r.seq_len == nullptr) ||
-        (r.reqs > 0 && r.max_blocks > 0 && r.block_table == nullptr) || !aligned(r.q, q_bf16 ? 8 : 16) ||
-        !aligned(r.out, out_bf16 ? 8 : 16) || !aligned(r.block_table, 4) ||
-        !aligned(r.seq_len, 4) || !aligned(r.q_start, 4) || !aligned(r.lse, 4) ||
-        (r.q_stride % 4) != 0 || (r.out_stride % 4) != 0 ||
-        (r.tokens > 1 && (r.q_stride < row || r.out_stride < row)))
+    if (p.groups == 0 || a.reqs == 0)
+        return launch_attention<KvSees::kCausal>(a, options, workspace, workspace_bytes, stream);
+    const int64_t rows = (int64_t)a.tokens * args->num_q_heads;
+    if (p.prefix_len == nullptr || (p.max_blocks > 0 && p.block_table == nullptr) || p.scratch == nullptr ||
+        !aligned(p.prefix_len, 4) || !aligned(p.block_table, 4) || !aligned(p.group_start, 4) ||
+        !aligned(p.scratch, 16) ||
+        (int64_t)p.scratch_bytes < nvfp4_kv_shared_scratch_size(a.tokens, args->num_q_heads, a.c.dim, a.reqs))
         return NVFP4_ERR_INVALID_ARG;
-    if (nvfp4::device_status_address(&a.status) != cudaSuccess)
-        return NVFP4_ERR_CUDA;
-    a.q = r.q;
-    a.q_stride = r.q_stride;
-    a.table = r.block_table;
-    a.table_stride = r.table_stride;
-    a.max_blocks = (int32_t)r.max_blocks;
-    a.seq_len = r.seq_len;
-    a.q_start = r.q_start;
-    a.q_per_req = (int32_t)(r.q_start || r.reqs == 0 ? 0 : r.tokens / r.reqs);
-    a.reqs = (int32_t)r.reqs;
-    a.tokens = (int32_t)r.tokens;
-    a.max_q = (int32_t)(r.max_q < r.tokens ? r.max_q : r.tokens);
-    a.group = (int32_t)(r.num_q_heads / a.c.heads);
-    a.group_magic = (uint32_t)(((uint64_t)1 << 32) / (uint64_t)a.group + 1);
-    a.scale_log2 = r.scale * 1.4426950408889634f;
-    // a window past every length is none
-    a.window = r.window >= kMaxTokens ? 0 : (int32_t)r.window;
-    a.out = r.out;
-    a.out_stride = r.out_stride;
-    a.lse = r.lse;
-    a.q_bf16 = q_bf16;
-    a.out_bf16 = out_bf16;
-    a.all_rows = all_rows;
-    const bool tile = kern == NVFP4_KERNEL_KV_TILE ||
-                      (kern == NVFP4_KERNEL_AUTO && all_bf16 &&
-                       use_tile(a.reqs, a.c.heads, (int64_t)a.max_q * a.group));
-    const auto launch = tile ? nvfp4::launch_kv_tile : nvfp4::launch_kv_rows;
-    return from_cuda(launch(a, workspace, (int64_t)workspace_bytes,
-                            static_cast<cudaStream_t>(stream), (options & NVFP4_FLAG_PDL) != 0));
+    const int64_t parts = nvfp4::kv_part_total(sm_count());
+    a.shared.rows = static_cast<float*>(p.scratch);
+    a.shared.parts = a.shared.rows + rows * a.c.dim;
+    a.shared.stats = reinterpret_cast<float2*>(a.shared.parts + parts * a.c.dim);
+    a.shared.part_stats = a.shared.stats + rows;
+    a.shared.where = reinterpret_cast<int32_t*>(a.shared.part_stats + parts);
+    a.shared.first = a.shared.where + rows;
+    a.shared.part_total = parts;
+    nvfp4::KvAttnArgs g = a;
+    g.shared.group_start = p.group_start;
+    g.shared.seq_len = a.seq_len;
+    g.shared.reqs = a.reqs;
+    g.shared.cap = (int64_t)a.max_blocks << a.c.page_shift;
+    g.table = p.block_table;
+    g.table_stride = p.table_stride;
+    g.max_blocks = (int32_t)p.max_blocks;
+    g.seq_len = p.prefix_len;
+    g.reqs = (int32_t)p.groups;
+    // rows of a group, on the average
+    g.max_q = (int32_t)((a.tokens + p.groups - 1) / p.groups);
+    g.all_rows = 0;
+    a.shared.item_rows = takes_tile(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
+    const int first = launch_attention<KvSees::kAll>(g, options, workspace, workspace_bytes, stream);
+    if (first != NVFP4_OK)
+        return first;
+    a.status = g.status;
+    return launch_attention<KvSees::kBehind>(a, options | NVFP4_FLAG_PDL, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

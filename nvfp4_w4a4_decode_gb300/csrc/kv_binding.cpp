@@ -1,4 +1,4 @@
-// kv_binding.cpp -- the Python side of the paged cache's three calls of a step:
+// kv_binding.cpp -- the Python side of the paged cache's calls of a step:
 // argument checks, output tensors, one call of the C ABI each.
 //
 // A decode step makes these calls in every layer, and on the kernels' few
@@ -22,6 +22,10 @@ using at::Tensor;
 decltype(&nvfp4_kv_tables) fn_tables = nullptr;
 decltype(&nvfp4_kv_append) fn_append = nullptr;
 decltype(&nvfp4_kv_attention) fn_attention = nullptr;
+decltype(&nvfp4_kv_append_rotary) fn_rotary = nullptr;
+decltype(&nvfp4_kv_cross_attention) fn_cross = nullptr;
+decltype(&nvfp4_kv_attention_shared) fn_shared = nullptr;
+decltype(&nvfp4_kv_shared_scratch_size) fn_scratch = nullptr;
 PyObject* error_class = nullptr;  // Nvfp4Error(function, status)
 
 // A failed check: a ValueError with this text.
@@ -65,12 +69,12 @@ struct Table {
 };
 
 // A block table [rows][blocks] with contiguous rows.
-Table table(const Tensor& t, int64_t rows, int64_t dev)
+Table table(const Tensor& t, int64_t rows, int64_t dev, const char* name = "block_table")
 {
-    on_device(t, "block_table", dev);
+    on_device(t, name, dev);
     if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != rows ||
         (t.size(1) > 1 && t.stride(1) != 1) || (rows > 1 && t.stride(0) < t.size(1)))
-        refuse("block_table must be int32 [" + std::to_string(rows) +
+        refuse(std::string(name) + " must be int32 [" + std::to_string(rows) +
                ", blocks] with contiguous rows");
     return {static_cast<int32_t*>(t.data_ptr()), rows > 1 ? t.stride(0) : t.size(1), t.size(1)};
 }
@@ -227,93 +231,240 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// append_rotary(cache, device, q or None, k, v, slots, positions, rotary, interleaved, out or None,
+// options, stream) -> the turned queries, or None
+PyObject* append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 12)
+        refuse("append_rotary takes 12 arguments");
+    const nvfp4_kv_cache* c = cache_of(a[0]);
+    const int64_t dev = integer(a[1]), dim = c->head_dim;
+    const Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
+    nvfp4_kv_rotary_args r = {};
+    r.k_stride = heads_stride(k, "k", dev, dim);
+    r.v_stride = heads_stride(v, "v", dev, dim);
+    if (k.size(1) != c->num_kv_heads || k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type())
+        refuse("k and v must be [tokens, " + std::to_string(c->num_kv_heads) + ", " + std::to_string(dim) +
+               "] of one dtype");
+    r.k = k.data_ptr();
+    r.v = v.data_ptr();
+    r.tokens = k.size(0);
+    r.slots = vector<int64_t>(tensor(a[5], "slots"), at::kLong, "slots", dev, r.tokens);
+    r.positions = vector<int32_t>(tensor(a[6], "positions"), at::kInt, "positions", dev, r.tokens);
+    const Tensor& rotary = tensor(a[7], "rotary");
+    on_device(rotary, "rotary", dev);
+    if (rotary.scalar_type() != at::kFloat || rotary.dim() != 2 || rotary.size(1) < 1 || rotary.size(1) > dim ||
+        (rotary.size(1) > 1 && rotary.stride(1) != 1) ||
+        (rotary.size(0) > 1 && rotary.stride(0) < rotary.size(1)))
+        refuse("rotary must be float32 [positions, elements of a head that are turned] with contiguous rows");
+    r.rotary = static_cast<const float*>(rotary.data_ptr());
+    r.rotary_rows = rotary.size(0);
+    r.rotary_stride = r.rotary_rows > 1 ? rotary.stride(0) : rotary.size(1);
+    r.rotary_dim = (int32_t)rotary.size(1);
+    const int interleaved = PyObject_IsTrue(a[8]);
+    if (interleaved < 0)
+        throw python_error();
+    r.interleaved = interleaved;
+    Tensor out;
+    if (a[2] != Py_None) {
+        const Tensor& q = tensor(a[2], "q");
+        r.q_stride = heads_stride(q, "q", dev, dim);
+        if (q.size(0) != r.tokens || q.scalar_type() != k.scalar_type())
+            refuse("q must have the tokens and the dtype of k");
+        if (a[9] == Py_None) {
+            out = at::empty(q.sizes(), q.options());
+            r.q_out_stride = q.size(1) * dim;
+        } else {
+            out = tensor(a[9], "out");
+            r.q_out_stride = heads_stride(out, "out", dev, dim);
+            if (out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type())
+                refuse("out must have q's shape and dtype");
+        }
+        r.q = q.data_ptr();
+        r.q_out = out.data_ptr();
+        r.num_q_heads = q.size(1);
+    } else if (a[9] != Py_None) {
+        refuse("out is for the turned queries: there are none");
+    }
+    const uint32_t options = (uint32_t)integer(a[10]) |
+                             (k.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_X_BF16 : 0u);
+    if (failed("nvfp4_kv_append_rotary", fn_rotary(c, &r, options, address(a[11]))))
+        return nullptr;
+    if (!out.defined())
+        Py_RETURN_NONE;
+    return THPVariable_Wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// The operands that every attention call has, checked; its outputs.
+struct Attention {
+    nvfp4_kv_attention_args r = {};
+    Tensor out, lse;
+    uint32_t options = 0;
+
+    // q, block_table, seq_len, q_start or None, max_q or None, scale or None, window or None (none),
+    // out or None, output dtype (0: q's, 1: float32, 2: bfloat16), with lse, options
+    Attention(const nvfp4_kv_cache* c, int64_t dev, PyObject* q_, PyObject* table_, PyObject* seq_len_,
+              PyObject* q_start_, PyObject* max_q_, PyObject* scale_, PyObject* window_, PyObject* out_,
+              PyObject* type_, PyObject* lse_, PyObject* options_)
+    {
+        const int64_t dim = c->head_dim;
+        const Tensor& q = tensor(q_, "q");
+        r.q_stride = heads_stride(q, "q", dev, dim);
+        r.q = q.data_ptr();
+        r.tokens = q.size(0);
+        r.num_q_heads = q.size(1);
+        const Tensor& seq_len = tensor(seq_len_, "seq_len");
+        r.seq_len = vector<int32_t>(seq_len, at::kInt, "seq_len", dev);
+        r.reqs = seq_len.size(0);
+        if (q_start_ != Py_None)
+            r.q_start = vector<int32_t>(tensor(q_start_, "q_start"), at::kInt, "q_start", dev, r.reqs + 1);
+        else if (r.reqs && r.tokens % r.reqs)
+            refuse("without q_start every request has the same number of rows");
+        if (r.num_q_heads % c->num_kv_heads)
+            refuse(std::to_string(r.num_q_heads) + " query heads do not share " +
+                   std::to_string(c->num_kv_heads) + " kv heads");
+        const Table t = table(tensor(table_, "block_table"), r.reqs, dev);
+        r.block_table = t.p;
+        r.table_stride = t.stride;
+        r.max_blocks = t.blocks;
+        r.max_q = max_q_ != Py_None ? integer(max_q_)
+                  : r.q_start       ? r.tokens
+                                    : (r.reqs ? r.tokens / r.reqs : 0);
+        r.scale = scale_ != Py_None ? (float)number(scale_) : 1.0f / std::sqrt((float)dim);
+        r.window = window_ ? integer(window_) : 0;
+        // rows of no request are written where the memory is new, left alone in a given output
+        const bool new_out = out_ == Py_None;
+        if (new_out) {
+            const int64_t type = integer(type_);
+            out = at::empty({r.tokens, r.num_q_heads, dim},
+                            q.options().dtype(type == 0   ? q.scalar_type()
+                                              : type == 1 ? at::kFloat
+                                                          : at::kBFloat16));
+            r.out_stride = r.num_q_heads * dim;
+        } else {
+            out = tensor(out_, "out");
+            if (out.sizes() != q.sizes())
+                refuse("out must have q's shape");
+            r.out_stride = heads_stride(out, "out", dev, dim);
+        }
+        r.out = out.data_ptr();
+        if (PyObject_IsTrue(lse_) == 1) {
+            const auto lse_options = q.options().dtype(at::kFloat);
+            lse = new_out ? at::empty({r.tokens, r.num_q_heads}, lse_options)
+                          : at::full({r.tokens, r.num_q_heads}, -INFINITY, lse_options);
+            r.lse = static_cast<float*>(lse.data_ptr());
+        }
+        options = (uint32_t)integer(options_) |
+                  (q.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_X_BF16 : 0u) |
+                  (out.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_Y_BF16 : 0u) |
+                  (new_out ? NVFP4_FLAG_ALL_ROWS : 0u);
+    }
+
+    // out, or (out, lse)
+    PyObject* result() const
+    {
+        if (!lse.defined())
+            return THPVariable_Wrap(out);
+        PyObject* pair = PyTuple_New(2);
+        PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
+        PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(lse));
+        return pair;
+    }
+};
+
 // attention(cache, device, q, block_table, seq_len, q_start or None, max_q or None,
-// scale or None, window, out or None, output dtype (0: q's, 1: float32, 2: bfloat16),
-// with lse, options, workspace, workspace bytes, stream) -> out, or (out, lse)
+// scale or None, window, out or None, output dtype, with lse, options, workspace, workspace
+// bytes, stream) -> out, or (out, lse)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     if (n != 16)
         refuse("attention takes 16 arguments");
     const nvfp4_kv_cache* c = cache_of(a[0]);
-    const int64_t dev = integer(a[1]), dim = c->head_dim;
-    const Tensor& q = tensor(a[2], "q");
-    nvfp4_kv_attention_args r = {};
-    r.q_stride = heads_stride(q, "q", dev, dim);
-    r.q = q.data_ptr();
-    r.tokens = q.size(0);
-    r.num_q_heads = q.size(1);
-    const Tensor& seq_len = tensor(a[4], "seq_len");
-    r.seq_len = vector<int32_t>(seq_len, at::kInt, "seq_len", dev);
-    r.reqs = seq_len.size(0);
-    if (a[5] != Py_None)
-        r.q_start = vector<int32_t>(tensor(a[5], "q_start"), at::kInt, "q_start", dev, r.reqs + 1);
-    else if (r.reqs && r.tokens % r.reqs)
-        refuse("without q_start every request has the same number of rows");
-    if (r.num_q_heads % c->num_kv_heads)
-        refuse(std::to_string(r.num_q_heads) + " query heads do not share " +
-               std::to_string(c->num_kv_heads) + " kv heads");
-    const Table t = table(tensor(a[3], "block_table"), r.reqs, dev);
-    r.block_table = t.p;
-    r.table_stride = t.stride;
-    r.max_blocks = t.blocks;
-    r.max_q = a[6] != Py_None ? integer(a[6])
-              : r.q_start     ? r.tokens
-                              : (r.reqs ? r.tokens / r.reqs : 0);
-    r.scale = a[7] != Py_None ? (float)number(a[7]) : 1.0f / std::sqrt((float)dim);
-    r.window = integer(a[8]);
-    Tensor out, lse;
-    // rows of no request are written where the memory is new, left alone in a given output
-    const bool new_out = a[9] == Py_None;
-    if (new_out) {
-        const int64_t type = integer(a[10]);
-        out = at::empty({r.tokens, r.num_q_heads, dim},
-                        q.options().dtype(type == 0   ? q.scalar_type()
-                                          : type == 1 ? at::kFloat
-                                                      : at::kBFloat16));
-        r.out_stride = r.num_q_heads * dim;
-    } else {
-        out = tensor(a[9], "out");
-        if (out.sizes() != q.sizes())
-            refuse("out must have q's shape");
-        r.out_stride = heads_stride(out, "out", dev, dim);
-    }
-    r.out = out.data_ptr();
-    const bool with_lse = PyObject_IsTrue(a[11]) == 1;
-    if (with_lse) {
-        const auto lse_options = q.options().dtype(at::kFloat);
-        lse = new_out ? at::empty({r.tokens, r.num_q_heads}, lse_options)
-                      : at::full({r.tokens, r.num_q_heads}, -INFINITY, lse_options);
-        r.lse = static_cast<float*>(lse.data_ptr());
-    }
-    const uint32_t options = (uint32_t)integer(a[12]) |
-                             (q.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_X_BF16 : 0u) |
-                             (out.scalar_type() == at::kBFloat16 ? NVFP4_FLAG_Y_BF16 : 0u) |
-                             (new_out ? NVFP4_FLAG_ALL_ROWS : 0u);
-    if (failed("nvfp4_kv_attention", fn_attention(c, &r, options, address(a[13]),
+    const Attention t(c, integer(a[1]), a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12]);
+    if (failed("nvfp4_kv_attention", fn_attention(c, &t.r, t.options, address(a[13]),
                                                   (size_t)integer(a[14]), address(a[15]))))
         return nullptr;
-    if (!with_lse)
-        return THPVariable_Wrap(out);
-    PyObject* pair = PyTuple_New(2);
-    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
-    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(lse));
-    return pair;
+    return t.result();
     END_HANDLE_TH_ERRORS
 }
 
-// bind(address of nvfp4_kv_tables, of nvfp4_kv_append, of nvfp4_kv_attention, Nvfp4Error)
+// cross_attention(cache, device, q, block_table, seq_len, q_start or None, max_q or None, scale or
+// None, out or None, output dtype, with lse, options, workspace, workspace bytes, stream)
+PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 15)
+        refuse("cross_attention takes 15 arguments");
+    const nvfp4_kv_cache* c = cache_of(a[0]);
+    const Attention t(c, integer(a[1]), a[2], a[3], a[4], a[5], a[6], a[7], nullptr, a[8], a[9], a[10], a[11]);
+    if (failed("nvfp4_kv_cross_attention", fn_cross(c, &t.r, t.options, address(a[12]),
+                                                    (size_t)integer(a[13]), address(a[14]))))
+        return nullptr;
+    return t.result();
+    END_HANDLE_TH_ERRORS
+}
+
+// attention_shared(cache, device, q, prefix_table, prefix_len, group_start or None, block_table,
+// seq_len, q_start or None, max_q or None, scale or None, out or None, output dtype, with lse,
+// options, workspace, workspace bytes, stream)
+PyObject* attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 18)
+        refuse("attention_shared takes 18 arguments");
+    const nvfp4_kv_cache* c = cache_of(a[0]);
+    const int64_t dev = integer(a[1]);
+    const Attention t(c, dev, a[2], a[6], a[7], a[8], a[9], a[10], nullptr, a[11], a[12], a[13], a[14]);
+    nvfp4_kv_prefixes p = {};
+    const Tensor& prefix_len = tensor(a[4], "prefix_len");
+    p.prefix_len = vector<int32_t>(prefix_len, at::kInt, "prefix_len", dev);
+    p.groups = prefix_len.size(0);
+    if (a[5] != Py_None)
+        p.group_start = vector<int32_t>(tensor(a[5], "group_start"), at::kInt, "group_start", dev, p.groups + 1);
+    else if (p.groups > 1)
+        refuse("without group_start there is one group of all requests");
+    const Table s = table(tensor(a[3], "prefix_table"), p.groups, dev, "prefix_table");
+    p.block_table = s.p;
+    p.table_stride = s.stride;
+    p.max_blocks = s.blocks;
+    Tensor scratch;
+    if (p.groups) {
+        const int64_t size = fn_scratch(t.r.tokens, t.r.num_q_heads, c->head_dim, t.r.reqs);
+        if (size < 0) {
+            failed("nvfp4_kv_shared_scratch_size", (int)-size);
+            return nullptr;
+        }
+        scratch = at::empty({size}, t.out.options().dtype(at::kByte));
+        p.scratch = scratch.data_ptr();
+        p.scratch_bytes = (size_t)size;
+    }
+    if (failed("nvfp4_kv_attention_shared", fn_shared(c, &t.r, &p, t.options, address(a[15]),
+                                                      (size_t)integer(a[16]), address(a[17]))))
+        return nullptr;
+    return t.result();
+    END_HANDLE_TH_ERRORS
+}
+
+// bind(the addresses of nvfp4_kv_tables, _append, _attention, _append_rotary, _cross_attention,
+// _attention_shared and _shared_scratch_size, Nvfp4Error)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 4)
-        refuse("bind takes 4 arguments");
+    if (n != 8)
+        refuse("bind takes 8 arguments");
     fn_tables = reinterpret_cast<decltype(fn_tables)>(address(a[0]));
     fn_append = reinterpret_cast<decltype(fn_append)>(address(a[1]));
     fn_attention = reinterpret_cast<decltype(fn_attention)>(address(a[2]));
-    Py_INCREF(a[3]);
+    fn_rotary = reinterpret_cast<decltype(fn_rotary)>(address(a[3]));
+    fn_cross = reinterpret_cast<decltype(fn_cross)>(address(a[4]));
+    fn_shared = reinterpret_cast<decltype(fn_shared)>(address(a[5]));
+    fn_scratch = reinterpret_cast<decltype(fn_scratch)>(address(a[6]));
+    Py_INCREF(a[7]);
     Py_XDECREF(error_class);
-    error_class = a[3];
+    error_class = a[7];
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -325,6 +476,12 @@ PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&append)), METH_FASTCALL,
      nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&attention)),
+     METH_FASTCALL, nullptr},
+    {"append_rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&append_rotary)),
+     METH_FASTCALL, nullptr},
+    {"cross_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&cross_attention)),
+     METH_FASTCALL, nullptr},
+    {"attention_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&attention_shared)),
      METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

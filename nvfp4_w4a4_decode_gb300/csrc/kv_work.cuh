@@ -97,18 +97,27 @@ struct KvReq {
     int32_t seq;   // tokens in the cache
     int32_t base;  // first query row
     int32_t nq;    // query rows (tokens)
+    int32_t low;   // first key seen (kBehind)
 };
 
+template <KvSees S>
 __device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
 {
     KvReq q;
-    int32_t b, e;
+    int32_t b, e, r0 = r, r1 = r + 1;
+    if constexpr (S == KvSees::kAll) {
+        if (a.shared.rows) {  // r is a group: the rows of its requests
+            const int32_t n = a.shared.reqs;
+            r0 = a.shared.group_start ? min(max(a.shared.group_start[r], 0), n) : 0;
+            r1 = a.shared.group_start ? min(max(a.shared.group_start[r + 1], r0), n) : n;
+        }
+    }
     if (a.q_start) {
-        b = a.q_start[r];
-        e = a.q_start[r + 1];
+        b = a.q_start[r0];
+        e = a.q_start[r1];
     } else {
-        b = r * a.q_per_req;
-        e = b + a.q_per_req;
+        b = r0 * a.q_per_req;
+        e = S == KvSees::kAll ? r1 * a.q_per_req : b + a.q_per_req;
     }
     b = min(max(b, 0), a.tokens);
     e = min(max(e, b), a.tokens);
@@ -116,7 +125,54 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
     q.nq = e - b;
     const int64_t cap = (int64_t)a.max_blocks << a.c.page_shift;
     q.seq = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
+    if constexpr (S == KvSees::kAll) {
+        if (a.shared.rows && q.seq == 0)  // nothing shared: nothing to do
+            q.nq = 0;
+    }
+    if constexpr (S == KvSees::kBehind)
+        q.low = a.shared.first[r];
     return q;
+}
+
+// The position of a request's token among its keys: the last that it sees.
+template <KvSees S>
+__device__ __forceinline__ int32_t kv_position(const KvReq& q, int token)
+{
+    return S == KvSees::kAll ? q.seq - 1 : q.seq - q.nq + token;
+}
+
+// Prefix pass: the first own key of every request, by `threads` threads of every CTA.  A
+// request shares its group's prefix if all of its rows lie behind it (an empty one never does);
+// else it sees all its keys by itself.  A function of its own, like kv_fill_rows.
+static __device__ __noinline__ void kv_find_first(const KvAttnArgs a, int thread, int threads)
+{
+    const KvShared& s = a.shared;
+    const int64_t cap = (int64_t)a.max_blocks << a.c.page_shift;
+    for (int r = blockIdx.x * threads + thread; r < s.reqs; r += gridDim.x * threads) {
+        int g = 0;
+        bool in = true;
+        if (s.group_start) {  // the last group that begins at or before r
+            int hi = a.reqs;
+            while (hi - g > 1) {
+                const int mid = (g + hi) / 2;
+                if (s.group_start[mid] <= r)
+                    g = mid;
+                else
+                    hi = mid;
+            }
+            in = s.group_start[g] <= r && r < s.group_start[g + 1];
+        }
+        int32_t b = r * a.q_per_req, e = b + a.q_per_req;
+        if (a.q_start) {
+            b = a.q_start[r];
+            e = a.q_start[r + 1];
+        }
+        b = min(max(b, 0), a.tokens);
+        e = min(max(e, b), a.tokens);
+        const int32_t seq = (int32_t)min((int64_t)max(s.seq_len[r], 0), s.cap);
+        const int32_t shared = in ? (int32_t)min((int64_t)max(a.seq_len[g], 0), cap) : 0;
+        s.first[r] = e > b && seq - (e - b) >= shared ? shared : 0;
+    }
 }
 
 // Zeros (and lse = -inf) for the call's rows [0, begin) and [end, tokens), by `threads`
@@ -201,16 +257,15 @@ struct KvShare {
 };
 
 // Items of up to WHOLE units, or an eighth of a share, stay whole.
-template <int R, int UT, int COST, int WHOLE>
+template <int R, int UT, int COST, int WHOLE, KvSees S>
 struct KvWork {
     // Units [first, first + n) of the rows [row0, row1) of a request.
     static __device__ __forceinline__ void tile_units(const KvAttnArgs& a, const KvReq& q, int row0,
                                                       int row1, int32_t& first, int32_t& n)
     {
         const int32_t i0 = kv_token(a, row0), i1 = kv_token(a, row1 - 1);
-        const int32_t p0 = q.seq - q.nq;
-        const int32_t hi = p0 + i1 + 1;  // keys [lo, hi)
-        const int32_t lo = a.window > 0 ? max(0, p0 + i0 - a.window + 1) : 0;
+        const int32_t hi = kv_position<S>(q, i1) + 1;  // keys [lo, hi)
+        const int32_t lo = first_key(a, q, i0);
         if (hi <= lo) {
             first = 0;
             n = 1;
@@ -224,7 +279,15 @@ struct KvWork {
     // first unit is not looked at: its page may serve another request by now.
     static __device__ __forceinline__ int32_t first_key(const KvAttnArgs& a, const KvItem& it)
     {
-        return a.window > 0 ? max(0, it.q.seq - it.q.nq + kv_token(a, it.row0) - a.window + 1) : 0;
+        return first_key(a, it.q, S == KvSees::kCausal && a.window > 0 ? kv_token(a, it.row0) : 0);
+    }
+    static __device__ __forceinline__ int32_t first_key(const KvAttnArgs& a, const KvReq& q, int token)
+    {
+        if constexpr (S == KvSees::kAll)
+            return 0;
+        if constexpr (S == KvSees::kBehind)
+            return q.low;
+        return a.window > 0 ? max(0, q.seq - q.nq + token - a.window + 1) : 0;
     }
 
     static __device__ __forceinline__ void units(const KvAttnArgs& a, KvItem& it)
@@ -238,7 +301,7 @@ struct KvWork {
     static __device__ __forceinline__ bool request(const KvAttnArgs& a, KvItem& it, int r)
     {
         for (; r < a.reqs; ++r) {
-            it.q = kv_req(a, r);
+            it.q = kv_req<S>(a, r);
             if (it.q.nq > 0)
                 break;
         }
@@ -389,10 +452,10 @@ struct KvWork {
                                                       KvItem& it)
     {
         const int lane = threadIdx.x & 31;
-        KvReq q = {0, 0, 0};
+        KvReq q = {0, 0, 0, 0};
         int64_t head = 0;
         if (lane < a.reqs) {
-            q = kv_req(a, lane);
+            q = kv_req<S>(a, lane);
             head = head_places(a, q, 0, 1);
             if (blockIdx.x == 0 && kv_too_long(a, lane))
                 atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
@@ -414,6 +477,8 @@ struct KvWork {
         it.q.seq = __shfl_sync(0xFFFFFFFFu, q.seq, it.r);
         it.q.base = __shfl_sync(0xFFFFFFFFu, q.base, it.r);
         it.q.nq = __shfl_sync(0xFFFFFFFFu, q.nq, it.r);
+        if constexpr (S == KvSees::kBehind)
+            it.q.low = __shfl_sync(0xFFFFFFFFu, q.low, it.r);
         it.rows = it.q.nq * a.group;
         return locate(a, sh, it, rem, head);
     }
@@ -435,7 +500,7 @@ struct KvWork {
         int per = (a.reqs + THREADS - 1) / THREADS;
         if (by_warp) {
             for (int r = warp; r < a.reqs; r += THREADS / 32) {
-                const int64_t s = head_places_warp(a, kv_req(a, r));
+                const int64_t s = head_places_warp(a, kv_req<S>(a, r));
                 if (lane == 0)
                     sm.req_sum[r] = a.c.heads * s;
             }
@@ -443,7 +508,7 @@ struct KvWork {
             __syncthreads();
         }
         auto places = [&](int r) {
-            return by_warp ? sm.req_sum[r] : a.c.heads * head_places(a, kv_req(a, r), 0, 1);
+            return by_warp ? sm.req_sum[r] : a.c.heads * head_places(a, kv_req<S>(a, r), 0, 1);
         };
         const int ra = min(tid * per, a.reqs), rb = min(ra + per, a.reqs);
         int64_t mine = 0;

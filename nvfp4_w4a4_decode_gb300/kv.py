@@ -1,5 +1,6 @@
 """Python binding of the paged NVFP4 key/value cache (``include/nvfp4_kv.h``):
-``kv_tables``, ``kv_append`` and ``kv_attention`` over a ``KVCache``.  The checks
+``kv_tables``, ``kv_append``, ``kv_append_rotary``, ``kv_attention``,
+``kv_attention_shared`` and ``kv_cross_attention`` over a ``KVCache``.  The checks
 of their arguments and their output tensors are made in ``csrc/kv_binding.cpp``."""
 from __future__ import annotations
 
@@ -15,7 +16,8 @@ import torch
 __all__ = ["KVCache", "KVTables", "kv_page_bytes", "kv_pool", "kv_tables", "kv_append",
            "kv_attention", "kv_attention_workspace", "nvfp4_kv_tables", "nvfp4_kv_append",
            "nvfp4_kv_attention", "nvfp4_kv_page_bytes", "KERNEL_KV_ROWS", "KERNEL_KV_TILE",
-           "DEVICE_KV_RANGE"]
+           "DEVICE_KV_RANGE", "kv_append_rotary", "kv_attention_shared", "kv_cross_attention",
+           "nvfp4_kv_append_rotary", "nvfp4_kv_attention_shared", "nvfp4_kv_cross_attention"]
 
 KERNEL_KV_ROWS = 1
 KERNEL_KV_TILE = 2
@@ -33,6 +35,10 @@ SIGNATURES = {
     "nvfp4_kv_append": ([_p, _p, _i64, _p, _i64, _i64, _p, _u32, _p], ctypes.c_int),
     "nvfp4_kv_attention": ([_p, _p, _u32, _p, ctypes.c_size_t, _p], ctypes.c_int),
     "nvfp4_kv_attention_workspace_size": ([_i64], _i64),
+    "nvfp4_kv_append_rotary": ([_p, _p, _u32, _p], ctypes.c_int),
+    "nvfp4_kv_cross_attention": ([_p, _p, _u32, _p, ctypes.c_size_t, _p], ctypes.c_int),
+    "nvfp4_kv_attention_shared": ([_p, _p, _p, _u32, _p, ctypes.c_size_t, _p], ctypes.c_int),
+    "nvfp4_kv_shared_scratch_size": ([_i64, _i64, _i64, _i64], _i64),
 }
 
 
@@ -58,7 +64,9 @@ def _binding():
             importlib.util.spec_from_file_location("_kv_binding", _build.BINDING, loader=loader))
         loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.nvfp4_kv_tables, lib.nvfp4_kv_append, lib.nvfp4_kv_attention)), Nvfp4Error)
+            lib.nvfp4_kv_tables, lib.nvfp4_kv_append, lib.nvfp4_kv_attention, lib.nvfp4_kv_append_rotary,
+            lib.nvfp4_kv_cross_attention, lib.nvfp4_kv_attention_shared, lib.nvfp4_kv_shared_scratch_size)),
+            Nvfp4Error)
         _calls = module
     return _calls
 
@@ -201,6 +209,34 @@ def nvfp4_kv_append(cache: KVCache, k, v, slots, pdl: bool = False) -> None:
                                   _stream(_current(cache._dev)))
 
 
+def nvfp4_kv_append_rotary(cache: KVCache, q, k, v, slots, positions, rotary, *, interleaved: bool = False,
+                           out=None, pdl: bool = False):
+    """``kv_append`` with the position rotation on the way: queries and keys are turned by
+    their token's angles, and the keys go from there into the cache without a rounding between.
+
+    q [tokens, num_q_heads, head_dim] (None: no queries), k and v [tokens, num_kv_heads, head_dim],
+    all float32 or all bfloat16; ``positions`` int32 [tokens]; ``rotary`` float32 [positions, n]: the
+    cosines of a position's n / 2 angles, then their sines, n a multiple of 32 up to head_dim.  Angle
+    i turns the elements i and i + n / 2 of a head, or 2 i and 2 i + 1 (``interleaved``); the elements
+    from n on stay.  Returns the turned queries in q's dtype (a new tensor, or ``out``, which may be q
+    itself).  Rows with slot -1 are turned, not appended; positions outside the table give zeros, append
+    nothing and set DEVICE_KV_RANGE in ``device_status()``."""
+    return (_calls or _binding()).append_rotary(
+        cache._desc, cache._dev, q, k, v, slots, positions, rotary, interleaved, out, FLAG_PDL if pdl else 0,
+        _stream(_current(cache._dev)))
+
+
+def _space(cache, workspace, stream):
+    """(address, bytes, what keeps them) of the workspace of an attention call."""
+    if workspace is None:
+        return cache._workspaces.get(stream) or cache._workspace(stream)
+    if workspace is False:
+        return 0, 0, None
+    if workspace.get_device() != cache._dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on CUDA device {cache._dev}")
+    return workspace.data_ptr(), workspace.nbytes, workspace
+
+
 def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
                        max_q: int | None = None, scale: float | None = None, window: int = 0,
                        out=None, out_dtype=None, return_lse: bool = False,
@@ -222,14 +258,7 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
     float32 or bfloat16 (``out_dtype``, by default q's); with ``return_lse``
     also the natural-log sums [tokens, num_q_heads] float32."""
     stream = _stream(_current(cache._dev))
-    if workspace is None:
-        wp, wn, _keep = cache._workspaces.get(stream) or cache._workspace(stream)
-    elif workspace is False:
-        wp = wn = 0
-    else:
-        if workspace.get_device() != cache._dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on CUDA device {cache._dev}")
-        wp, wn = workspace.data_ptr(), workspace.nbytes
+    wp, wn, _keep = _space(cache, workspace, stream)
     if out_dtype not in _OUT:
         raise ValueError(f"the output must be float32 or bfloat16, got {out_dtype}")
     return (_calls or _binding()).attention(
@@ -237,7 +266,52 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
         _OUT[out_dtype], return_lse, kernel | FLAG_PDL if pdl else kernel, wp, wn, stream)
 
 
+def nvfp4_kv_cross_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
+                             max_q: int | None = None, scale: float | None = None, out=None,
+                             out_dtype=None, return_lse: bool = False, kernel: int = KERNEL_AUTO,
+                             workspace=None, pdl: bool = False):
+    """Attention of q [tokens, num_q_heads, head_dim] to all that the cache holds of each
+    request: the states of an encoder, of any length beside the request's rows.
+
+    ``seq_len`` int32 [reqs]: states in the cache (written by ``kv_append``); every row of a
+    request sees all of them, and with 0 gets zeros and lse = -inf.  All else as for
+    ``kv_attention``."""
+    stream = _stream(_current(cache._dev))
+    wp, wn, _keep = _space(cache, workspace, stream)
+    if out_dtype not in _OUT:
+        raise ValueError(f"the output must be float32 or bfloat16, got {out_dtype}")
+    return (_calls or _binding()).cross_attention(
+        cache._desc, cache._dev, q, block_table, seq_len, q_start, max_q, scale, out, _OUT[out_dtype],
+        return_lse, kernel | FLAG_PDL if pdl else kernel, wp, wn, stream)
+
+
+def nvfp4_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len, block_table, seq_len, q_start=None, *,
+                              group_start=None, max_q: int | None = None, scale: float | None = None, out=None,
+                              out_dtype=None, return_lse: bool = False, kernel: int = KERNEL_AUTO,
+                              workspace=None, pdl: bool = False):
+    """``kv_attention`` of requests that share prefixes, each read once for all of its requests.
+
+    ``prefix_len`` int32 [groups]: tokens of each prefix, which need not end with a page;
+    ``prefix_table`` int32 [groups, blocks]: its pages; ``group_start`` int32 [groups + 1],
+    ascending: the first request of each group (None: one group of all requests).  Lengths and
+    positions count the prefix: ``seq_len`` holds whole lengths, and ``block_table`` entry b the
+    tokens from b * page_size on, of which those wholly inside the prefix are not looked up.
+    (Tables, slots and positions of ``kv_tables`` fit as they are.)  A request with a row inside the
+    prefix, or with no tokens, shares nothing: it is attended on its own pages alone.  All else as for
+    ``kv_attention``; ``kernel`` forces the kernel of both passes."""
+    stream = _stream(_current(cache._dev))
+    wp, wn, _keep = _space(cache, workspace, stream)
+    if out_dtype not in _OUT:
+        raise ValueError(f"the output must be float32 or bfloat16, got {out_dtype}")
+    return (_calls or _binding()).attention_shared(
+        cache._desc, cache._dev, q, prefix_table, prefix_len, group_start, block_table, seq_len, q_start,
+        max_q, scale, out, _OUT[out_dtype], return_lse, kernel | FLAG_PDL if pdl else kernel, wp, wn, stream)
+
+
 kv_page_bytes = nvfp4_kv_page_bytes
 kv_tables = nvfp4_kv_tables
 kv_append = nvfp4_kv_append
 kv_attention = nvfp4_kv_attention
+kv_append_rotary = nvfp4_kv_append_rotary
+kv_attention_shared = nvfp4_kv_attention_shared
+kv_cross_attention = nvfp4_kv_cross_attention
