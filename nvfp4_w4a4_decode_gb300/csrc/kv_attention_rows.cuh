@@ -63,22 +63,16 @@ constexpr int kUnit = 32;       // tokens a unit
 constexpr int kGroup = 64;      // tokens a group
 constexpr int kSub = kGroup / kUnit;
 constexpr int kBatch = 3;       // groups the copying warp brings at a time
-constexpr int kWarps = 7;       // compute warps: with the copying warp eight, two
-                                // for each of the SM's four register files
-constexpr int kCompute = 32 * kWarps;
-constexpr int kThreads = kCompute + 32;
-// Groups that an item's start and join cost (us for 24 requests of 1..6000 tokens, FP32
-// queries / three FP32 prompts: 1 25 / 72, 2 21 / 59, 5 20 / 45, 8 18.8 / 42, 12 20 / 44).
-constexpr int kItemCost = 8;
 constexpr int kMaxCtas = 512;   // workspace extent
 constexpr int kMaxRows = 32;
 constexpr float kRaise = 8.0f;  // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;   // p = 2^(s - m + kLift)
 
 // Barrier of the compute warps.
-__device__ __forceinline__ void compute_sync()
+template <int THREADS>
+__device__ __forceinline__ void compute_barrier()
 {
-    asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 __device__ __forceinline__ uint32_t movm_trans(uint32_t v)
@@ -105,20 +99,25 @@ __device__ __forceinline__ int token_of_row(int k)
     return (k & 8) | ((k & 1) ? 4 + (j ^ 1) : j);
 }
 
-template <int D, int NT, bool SPLIT>
+// W compute warps a CTA.  Seven: with the copying warp eight, two for each of the SM's four
+// register files.  Three, with four CTAs an SM: an item's start and join, which wait for
+// memory and for one another, overlap those of three other CTAs.
+template <int D, int NT, bool SPLIT, int W>
 struct Cfg {
+    static constexpr int kCompute = 32 * W;
+    static constexpr int kThreads = kCompute + 32;
     static constexpr int R = 8 * NT;             // query rows a tile
     static constexpr int KS = D / 16;            // k16 steps of Q K, m16 tiles of V
     static constexpr int kStageBytes = kGroup * D * 9 / 8;
     // two CTAs an SM where the registers allow it: the joins and starts of one
     // overlap the other's stream (with FP32 terms that takes the queries out of
     // registers and one half at a time: 24 ragged requests 25.9 -> 20.9 us)
-    static constexpr int kCtas = NT == 1 ? 2 : 1;
-    static constexpr int kStages = 7;
+    static constexpr int kCtas = W == 3 ? 4 : NT == 1 ? 2 : 1;
+    static constexpr int kStages = W == 3 ? (D == 128 ? 3 : 6) : 7;
     static constexpr int kQTerms = SPLIT ? 2 : 1;
     static constexpr int kQBytes = kQTerms * NT * KS * 32 * 8;
     static constexpr int kRingBytes = kStages * kStageBytes;
-    static constexpr int kRedBytes = kWarps * KS * 32 * 16;
+    static constexpr int kRedBytes = W * KS * 32 * 16;
     static constexpr int kSmem = kRingBytes + kRedBytes + kQBytes;
     // queries held in registers while the accumulators leave room (32 rows, or FP32
     // terms, read them from shared memory at each use)
@@ -126,16 +125,24 @@ struct Cfg {
     // A parity tells a phase from its neighbours only: a warp must see every
     // phase of the slots it reads.  Units are dealt by their number in the CTA's
     // whole sequence, so a unit's place in the ring always has the same warp.
-    static_assert(kStages * kSub % kWarps == 0, "a ring holds whole rounds of the warps");
+    static_assert(kStages * kSub % W == 0, "a ring holds whole rounds of the warps");
+    // Groups that an item's start and join cost (seven warps, us for 24 requests of 1..6000
+    // tokens, FP32 queries / three FP32 prompts: 1 25 / 72, 2 21 / 59, 5 20 / 45, 8 18.8 / 42,
+    // 12 20 / 44).
+    static constexpr int kItemCost = W == 3 ? 4 : 8;
+    // Items of up to so many groups stay whole, or of up to twice a share if that is less than kWholeMax
+    static constexpr int kWhole = W == 3 ? 2 : 4, kWholeMax = W == 3 ? 16 : 4;
 };
 
-template <KvSees S, int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
+template <KvSees S, int D, int NT, bool SPLIT, int W>
+__global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPLIT, W>::kCtas)
     kv_rows_kernel(const KvAttnArgs a)
 {
-    using C = Cfg<D, NT, SPLIT>;
+    using C = Cfg<D, NT, SPLIT, W>;
+    constexpr int kWarps = W, kCompute = C::kCompute, kThreads = C::kThreads;
+    auto compute_sync = []() { compute_barrier<C::kCompute>(); };
     constexpr int R = C::R, KS = C::KS, ST = C::kStages;
-    using Work = KvWork<R, kGroup, kItemCost, 4, S>;
+    using Work = KvWork<R, kGroup, C::kItemCost, C::kWhole, C::kWholeMax, S>;
     using Item = KvItem;
     using Share = KvShare;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     // at least as many groups as the warps take in one round
     Share sh;
     Item it;
-    bool more = Work::template start<kThreads>(a, work_sm, kWarps / kSub, sh, it);
+    bool more = Work::template start<kThreads>(a, work_sm, (kWarps + (W == 3)) / kSub, sh, it);
     if (sh.lo >= sh.hi) {
         if (a.all_rows && warp == kWarps)
             kv_write_other_rows(a, lane, 32);
@@ -370,6 +377,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
                 for (int e = 0; e < 4; ++e)
                     acc[nt][i][e] = 0.f;
         }
+        // ---- the prefix's results, a part a warp in turn ------------------------------------
+        // (by the CTA that has the item's first unit, while that is on its way; sums of p: by
+        // the lanes of g = 0)
+        if constexpr (S == KvSees::kBehind) {
+            if (it.q.low > 0 && u0 == 0) {
+#pragma unroll 1
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = it.row0 + nt * 8 + 2 * t + e;
+                        if (row >= it.row1)
+                            continue;
+                        const int tok = kv_token(a, row);
+                        const int64_t at = (int64_t)(it.q.base + tok) * (a.c.heads * a.group) +
+                                           it.h * a.group + row - tok * a.group;
+                        int n;
+                        const int32_t where = kv_where(a.shared, at, n);
+#pragma unroll 1
+                        for (int k = warp; k < n; k += kWarps) {
+                            const int64_t pr = where ? kv_part_row(where, k, a.shared.item_rows) : at;
+                            const float2 ml = (where ? a.shared.part_stats : a.shared.stats)[pr];
+                            const float4* src = reinterpret_cast<const float4*>(
+                                (where ? a.shared.parts : a.shared.rows) + pr * D + D / 8 * g);
+                            float4 x[KS / 2];
+#pragma unroll
+                            for (int i = 0; i < KS / 2; ++i)
+                                x[i] = src[i];
+#pragma unroll
+                            for (int z = 0; z < NT; ++z) {
+                                if (z != nt)  // (registers want fixed indices)
+                                    continue;
+                                const float now = fmaxf(m[z][e], ml.x);
+                                const float by = m[z][e] == now ? 1.f : ex2(m[z][e] - now);
+                                const float add = ml.x == now ? 1.f : ex2(ml.x - now);
+                                m[z][e] = now;
+                                l[z][e] = fmaf(l[z][e], by, g == 0 ? ml.y * add : 0.f);
+#pragma unroll
+                                for (int i = 0; i < KS / 2; ++i) {
+                                    float* o = acc[z][2 * i];
+                                    float* u = acc[z][2 * i + 1];
+                                    o[e] = fmaf(o[e], by, x[i].x * add);
+                                    o[e + 2] = fmaf(o[e + 2], by, x[i].y * add);
+                                    u[e] = fmaf(u[e], by, x[i].z * add);
+                                    u[e + 2] = fmaf(u[e + 2], by, x[i].w * add);
+                                }
+                            }
+                        }
+                    }
+            }
+        }
+
         // positions every row of the tile sees: keys in [all_lo, all_hi]
         const int32_t all_hi = kv_position<S>(it.q, kv_token(a, it.row0));
         const int32_t all_lo = Work::first_key(a, it.q, kv_token(a, it.row1 - 1));
@@ -629,56 +687,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
             }
         }
 
-        // ---- the prefix's results, a part a warp in turn ------------------------------------
-        // (by the CTA that has the item's first unit; sums of p: by the lanes of g = 0)
-        if constexpr (S == KvSees::kBehind) {
-            if (it.q.low > 0 && u0 == 0) {
-#pragma unroll 1
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = it.row0 + nt * 8 + 2 * t + e;
-                        if (row >= it.row1)
-                            continue;
-                        const int tok = kv_token(a, row);
-                        const int64_t at = (int64_t)(it.q.base + tok) * (a.c.heads * a.group) +
-                                           it.h * a.group + row - tok * a.group;
-                        int n;
-                        const int32_t where = kv_where(a.shared, at, n);
-#pragma unroll 1
-                        for (int k = warp; k < n; k += kWarps) {
-                            const int64_t pr = where ? kv_part_row(where, k, a.shared.item_rows) : at;
-                            const float2 ml = (where ? a.shared.part_stats : a.shared.stats)[pr];
-                            const float4* src = reinterpret_cast<const float4*>(
-                                (where ? a.shared.parts : a.shared.rows) + pr * D + D / 8 * g);
-                            float4 x[KS / 2];
-#pragma unroll
-                            for (int i = 0; i < KS / 2; ++i)
-                                x[i] = src[i];
-#pragma unroll
-                            for (int z = 0; z < NT; ++z) {
-                                if (z != nt)  // (registers want fixed indices)
-                                    continue;
-                                const float now = fmaxf(m[z][e], ml.x);
-                                const float by = m[z][e] == now ? 1.f : ex2(m[z][e] - now);
-                                const float add = ml.x == now ? 1.f : ex2(ml.x - now);
-                                m[z][e] = now;
-                                l[z][e] = fmaf(l[z][e], by, g == 0 ? ml.y * add : 0.f);
-#pragma unroll
-                                for (int i = 0; i < KS / 2; ++i) {
-                                    float* o = acc[z][2 * i];
-                                    float* u = acc[z][2 * i + 1];
-                                    o[e] = fmaf(o[e], by, x[i].x * add);
-                                    o[e + 2] = fmaf(o[e + 2], by, x[i].y * add);
-                                    u[e] = fmaf(u[e], by, x[i].z * add);
-                                    u[e + 2] = fmaf(u[e + 2], by, x[i].w * add);
-                                }
-                            }
-                        }
-                    }
-            }
-        }
-
         // ---- join the warps ---------------------------------------------------------------
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -935,17 +943,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, SPLIT>::kCtas)
     }
 }
 
-template <KvSees S, int D, int NT, bool SPLIT>
+template <KvSees S, int D, int NT, bool SPLIT, int W>
 cudaError_t launch(const KvAttnArgs& a, cudaStream_t stream, bool pdl)
 {
-    using C = Cfg<D, NT, SPLIT>;
+    using C = Cfg<D, NT, SPLIT, W>;
     const int dev = current_device();
-    auto* kern = &kv_rows_kernel<S, D, NT, SPLIT>;
+    auto* kern = &kv_rows_kernel<S, D, NT, SPLIT, W>;
     const cudaError_t e = ensure_smem_limit(kern, C::kSmem, dev);
     if (e != cudaSuccess)
         return e;
+    // the workspace holds two partial results of kMaxCtas CTAs with items of kMaxRows rows
+    constexpr int kMost = kMaxCtas * (kMaxRows / C::R) < kKvCountBytes / 4 ? kMaxCtas * (kMaxRows / C::R)
+                                                                           : (int)(kKvCountBytes / 4);
     const int grid = device_sm_count(dev) * C::kCtas;
-    return kv_launch(kern, grid > kMaxCtas ? kMaxCtas : grid, kThreads, C::kSmem, stream, pdl, a);
+    return kv_launch(kern, grid > kMost ? kMost : grid, C::kThreads, C::kSmem, stream, pdl, a);
 }
 
 inline int item_rows(const KvAttnArgs& a)
@@ -959,11 +970,11 @@ cudaError_t launch_rows(const KvAttnArgs& a, cudaStream_t stream, bool pdl)
 {
     switch (item_rows(a)) {
     case 8:
-        return launch<S, D, 1, SPLIT>(a, stream, pdl);
+        return launch<S, D, 1, SPLIT, S == KvSees::kCausal ? 7 : 3>(a, stream, pdl);
     case 16:
-        return launch<S, D, 2, SPLIT>(a, stream, pdl);
+        return launch<S, D, 2, SPLIT, 7>(a, stream, pdl);
     default:
-        return launch<S, D, 4, SPLIT>(a, stream, pdl);
+        return launch<S, D, 4, SPLIT, 7>(a, stream, pdl);
     }
 }
 

@@ -319,7 +319,7 @@ template <KvSees S, int D, bool LOW>
 __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a)
 {
     using C = Cfg<D>;
-    using Work = KvWork<kRows, kKeys, kItemCost, 2, S>;
+    using Work = KvWork<kRows, kKeys, kItemCost, 2, 2, S>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) Barriers bars;
     __shared__ typename Work::Smem work_sm;
@@ -677,17 +677,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                             : (Work::last_cta(sh, it) - Work::first_cta(sh, it) + 1)
                                                       << kKvPartBits | mine_at;
                 }
-                float4* dst = reinterpret_cast<float4*>(whole ? s.rows + at * D : s.parts + (int64_t)mine_at * D);
+                float* dst = whole ? s.rows + at * D : s.parts + (int64_t)mine_at * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
                     tmem_ld32(tO + i, o);
                     if (live)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[i / 4 + j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                         __uint_as_float(o[4 * j + 2]),
-                                                         __uint_as_float(o[4 * j + 3]));
+                        for (int j = 0; j < 32; j += 8)
+                            store8(dst + i + j, o + j);
                 }
                 continue;
             }
@@ -767,16 +765,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
 #pragma unroll 1
                         for (int k = 0; k < parts; ++k) {
                             const float f = part_factor(k) * all_scale;
-                            const float4* y = reinterpret_cast<const float4*>(
-                                (where ? a.shared.parts : a.shared.rows) + part(k) * D + i);
+                            const float* src = (where ? a.shared.parts : a.shared.rows) + part(k) * D + i;
+                            float y[32];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 z = y[j];
-                                x[4 * j] = fmaf(z.x, f, x[4 * j]);
-                                x[4 * j + 1] = fmaf(z.y, f, x[4 * j + 1]);
-                                x[4 * j + 2] = fmaf(z.z, f, x[4 * j + 2]);
-                                x[4 * j + 3] = fmaf(z.w, f, x[4 * j + 3]);
-                            }
+                            for (int j = 0; j < 32; j += 8)
+                                load8(src + j, y + j);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                x[j] = fmaf(y[j], f, x[j]);
                         }
                         write(i, x, 1.f);
                         return;

@@ -78,6 +78,21 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Eight floats, a whole 32-byte sector a thread.
+__device__ __forceinline__ void load8(const float* p, float* v)
+{
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store8(float* p, const uint32_t* v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t d;
@@ -256,8 +271,9 @@ struct KvShare {
     bool cut;  // longer items may be
 };
 
-// Items of up to WHOLE units, or an eighth of a share, stay whole.
-template <int R, int UT, int COST, int WHOLE, KvSees S>
+// Items of up to WHOLE units, or an eighth of a share, stay whole; so do those of up to twice a
+// share and WHOLE_MAX units.
+template <int R, int UT, int COST, int WHOLE, int WHOLE_MAX, KvSees S>
 struct KvWork {
     // Units [first, first + n) of the rows [row0, row1) of a request.
     static __device__ __forceinline__ void tile_units(const KvAttnArgs& a, const KvReq& q, int row0,
@@ -405,7 +421,10 @@ struct KvWork {
         sh.lo = sh.size * blockIdx.x;
         sh.hi = min(sh.lo + sh.size, total);
         sh.cut = a.part != nullptr;
-        sh.least = (int32_t)min(max((int64_t)WHOLE, sh.size >> 3), (int64_t)INT32_MAX);
+        int64_t whole = max((int64_t)WHOLE, sh.size >> 3);
+        if constexpr (WHOLE_MAX > WHOLE)
+            whole = max(whole, min(2 * sh.size, (int64_t)WHOLE_MAX));
+        sh.least = (int32_t)min(whole, (int64_t)INT32_MAX);
         return sh.lo < total;
     }
 
