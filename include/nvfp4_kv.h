@@ -271,14 +271,15 @@ typedef struct {
     size_t scratch_bytes;
 } nvfp4_kv_prefixes;
 
-/* Two kernels: the prefixes, then the requests' own keys and the join. */
+/* Two or three kernels: the prefixes, the requests' own keys, and with few rows a request
+ * the join of the two. */
 int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
                               const nvfp4_kv_prefixes* prefixes, uint32_t options,
                               void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of nvfp4_kv_prefixes.scratch, or minus a status code.  Host only. */
-int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim,
-                                     int64_t reqs);
+/* Bytes of nvfp4_kv_prefixes.scratch on the current device, or minus a status code.  Host
+ * only. */
+int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim);
 
 #ifdef __cplusplus
 }

@@ -94,30 +94,23 @@ enum class KvSees {
     kBehind,  // KvShared::first of its request <= j <= p: a request's own keys
 };
 
-// The two passes of requests that share prefixes.  The first (kAll) takes a group for a
-// request: its rows are those of the group's requests, its table the prefix's.  It leaves
-// every row's sum of p V, its reference (log2) and its sum of p, and which keys each
-// request still has to see.  An item cut between CTAs is not joined there (one SM would
-// read the parts of 256 rows while the others wait): the second pass (kBehind) adds a row's
-// parts to its own sums, in CTA order.
-struct KvShared {
-    float* rows;         // [tokens][query heads][D]: of items that were not cut (null: no such call)
+// What a pass over some of a row's keys leaves of it: the sum of p V, the reference (log2)
+// and the sum of p.  An item cut between CTAs is not joined by the pass (one SM would read the
+// parts of 256 rows while the others wait): whoever reads the row adds up its parts.
+struct KvParts {
+    float* rows;         // [tokens][query heads][D]: of items that were not cut
     float2* stats;       // [tokens][query heads]
-    float* parts;        // [part_total][D]: of the cut ones, two places of an item's rows a CTA
-    float2* part_stats;  // [part_total]
-    int32_t* where;      // [tokens][query heads]: 0, or parts << kKvPartBits | row of the first in `parts`
-    int32_t* first;      // [requests]: the request's first own key, 0 where it shares none
-    int64_t part_total;  // rows of `parts`
-    int32_t item_rows;   // query rows of an item of the first pass
-    // first pass only: the requests
-    const int32_t* group_start;  // first request of each group, or null: one group of all
-    const int32_t* seq_len;
-    int32_t reqs;
-    int64_t cap;       // keys that a request's own table has room for
+    float* parts;        // [total][D]: of the cut ones, two places of an item's rows a CTA
+    float2* part_stats;  // [total]
+    int32_t* where;      // [tokens][query heads]: 0, or parts << kKvPartBits | row of the first in
+                         // `parts`; with kKvSharesBit where the prefix's sums belong to the row
+    int64_t total;       // rows of `parts`
+    int32_t item_rows;   // query rows of an item of the pass
 };
 
-// Rows of KvShared::parts: two items of 256 rows on each SM, or of 32 rows for 512 CTAs.
+// Rows of KvParts::parts: two items of 256 rows on each SM, or of 32 rows for 512 CTAs.
 constexpr int kKvPartBits = 17;
+constexpr int32_t kKvSharesBit = 1 << 30;
 constexpr int64_t kv_part_total(int sms)
 {
     return (int64_t)(sms > 64 ? sms : 64) * 512;
@@ -130,19 +123,30 @@ __device__ __forceinline__ int64_t kv_part_row(int32_t where, int k, int item_ro
     return (where & ((1 << kKvPartBits) - 1)) + (k ? (int64_t)(2 * k - 1) * item_rows : 0);
 }
 
-// What the first pass has written for a row, and the number of its parts.  Starts that go back
+// What a pass has written for a row, and the number of its parts.  Starts that go back
 // (the rows of a request are then not those of its group) may leave anything there: such an
 // entry is not followed.
-__device__ __forceinline__ int32_t kv_where(const KvShared& s, int64_t row, int& parts)
+__device__ __forceinline__ int32_t kv_where(const KvParts& s, int64_t row, int& parts)
 {
-    int32_t w = s.where[row];
+    int32_t w = s.where[row] & ~kKvSharesBit;
     parts = w >> kKvPartBits;
-    if (w < 0 || (parts > 0 && kv_part_row(w, parts - 1, s.item_rows) >= s.part_total))
+    if (w < 0 || (parts > 0 && kv_part_row(w, parts - 1, s.item_rows) >= s.total))
         w = parts = 0;
     if (parts == 0)
         w = 0, parts = 1;
     return w;
 }
+
+// Requests that share prefixes take two passes.  The first (kAll) takes a group for a request:
+// its rows are those of the group's requests, its table the prefix's.  The second (kBehind)
+// takes the requests' own keys; with many rows a request it joins the two itself, else both leave
+// their parts to launch_kv_join.
+struct KvGroups {
+    const int32_t* start;       // first request of each group, or null: one group of all
+    const int32_t* prefix_len;  // tokens of each group's prefix
+    int32_t count, reqs;
+    int64_t cap;                // keys that a row of the prefixes' table has room for
+};
 
 struct KvAttnArgs {
     KvCache c;
@@ -166,7 +170,9 @@ struct KvAttnArgs {
     float* lse;
     int32_t q_bf16, out_bf16;
     int32_t all_rows;  // rows of no request are written too
-    KvShared shared;
+    KvGroups groups;
+    KvParts keep;     // where the pass leaves its rows (rows null: it writes outputs)
+    KvParts prefix;   // what the first pass left
     float* part;      // partial results of items cut between CTAs (null: none is cut)
     unsigned* count;  // arrival counters, zero between calls
     unsigned* status;
@@ -190,6 +196,9 @@ template <KvSees S>
 cudaError_t launch_kv_tile(const KvAttnArgs& a, void* workspace, int64_t workspace_bytes,
                            cudaStream_t stream, bool pdl);
 
+// The outputs of rows whose sums lie in a.prefix and a.keep (the second pass's).
+cudaError_t launch_kv_join(const KvAttnArgs& a, cudaStream_t stream);
+
 // Launch with or without programmatic dependent launch (every kernel of the
 // cache waits for the previous one before its first access).
 template <typename... P, typename... A>
@@ -209,10 +218,33 @@ inline cudaError_t kv_launch(void (*kern)(P...), unsigned grid, unsigned threads
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-__device__ __forceinline__ void kv_pdl_begin()
+__device__ __forceinline__ void kv_pdl_launch()
 {
     asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void kv_pdl_wait()
+{
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void kv_pdl_begin()
+{
+    kv_pdl_launch();
+    kv_pdl_wait();
+}
+// Of the two passes of shared prefixes the first lets the second start only when what came
+// before it is complete; so the second waits for nothing but the first's results, if and when
+// it reads them, and every thread of it before it ends (what follows then waits for both).
+template <KvSees S>
+__device__ __forceinline__ void kv_pdl_begin(const KvParts& keep)
+{
+    if constexpr (S == KvSees::kBehind) {
+        kv_pdl_launch();
+    } else if (S == KvSees::kAll && keep.rows != nullptr) {
+        kv_pdl_wait();
+        kv_pdl_launch();
+    } else {
+        kv_pdl_begin();
+    }
 }
 
 }  // namespace nvfp4

@@ -418,15 +418,14 @@ int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attenti
                : launch_attention<KvSees::kAll>(a, options, workspace, workspace_bytes, stream);
 }
 
-int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim, int64_t reqs)
+int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim)
 {
-    if (tokens < 0 || num_q_heads < 1 || head_dim < 1 || reqs < 0)
+    if (tokens < 0 || num_q_heads < 1 || head_dim < 1)
         return -NVFP4_ERR_INVALID_ARG;
-    if ((head_dim != 64 && head_dim != 128) || tokens >= kMaxTokens || num_q_heads > (1 << 22) ||
-        reqs > nvfp4::kKvMaxReqs)
+    if ((head_dim != 64 && head_dim != 128) || tokens >= kMaxTokens || num_q_heads > (1 << 22))
         return -NVFP4_ERR_UNSUPPORTED;
     const int64_t rows = tokens * num_q_heads, parts = nvfp4::kv_part_total(sm_count());
-    return (rows + parts) * (head_dim * 4 + 8) + (rows + reqs) * 4;
+    return 2 * ((rows + parts) * (head_dim * 4 + 8) + rows * 4);  // of the two passes
 }
 
 int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
@@ -454,21 +453,24 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
     if (p.prefix_len == nullptr || (p.max_blocks > 0 && p.block_table == nullptr) || p.scratch == nullptr ||
         !aligned(p.prefix_len, 4) || !aligned(p.block_table, 4) || !aligned(p.group_start, 4) ||
         !aligned(p.scratch, 16) ||
-        (int64_t)p.scratch_bytes < nvfp4_kv_shared_scratch_size(a.tokens, args->num_q_heads, a.c.dim, a.reqs))
+        (int64_t)p.scratch_bytes < nvfp4_kv_shared_scratch_size(a.tokens, args->num_q_heads, a.c.dim))
         return NVFP4_ERR_INVALID_ARG;
     const int64_t parts = nvfp4::kv_part_total(sm_count());
-    a.shared.rows = static_cast<float*>(p.scratch);
-    a.shared.parts = a.shared.rows + rows * a.c.dim;
-    a.shared.stats = reinterpret_cast<float2*>(a.shared.parts + parts * a.c.dim);
-    a.shared.part_stats = a.shared.stats + rows;
-    a.shared.where = reinterpret_cast<int32_t*>(a.shared.part_stats + parts);
-    a.shared.first = a.shared.where + rows;
-    a.shared.part_total = parts;
+    nvfp4::KvParts of[2];
+    uint8_t* at = static_cast<uint8_t*>(p.scratch);
+    for (nvfp4::KvParts& x : of) {
+        x.rows = reinterpret_cast<float*>(at);
+        x.parts = x.rows + rows * a.c.dim;
+        x.stats = reinterpret_cast<float2*>(x.parts + parts * a.c.dim);
+        x.part_stats = x.stats + rows;
+        x.total = parts;
+        x.item_rows = 0;
+        at = reinterpret_cast<uint8_t*>(x.part_stats + parts);
+    }
+    of[0].where = reinterpret_cast<int32_t*>(at);
+    of[1].where = of[0].where + rows;
+    a.groups = {p.group_start, p.prefix_len, (int32_t)p.groups, a.reqs, p.max_blocks << a.c.page_shift};
     nvfp4::KvAttnArgs g = a;
-    g.shared.group_start = p.group_start;
-    g.shared.seq_len = a.seq_len;
-    g.shared.reqs = a.reqs;
-    g.shared.cap = (int64_t)a.max_blocks << a.c.page_shift;
     g.table = p.block_table;
     g.table_stride = p.table_stride;
     g.max_blocks = (int32_t)p.max_blocks;
@@ -477,12 +479,23 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
     // rows of a group, on the average
     g.max_q = (int32_t)((a.tokens + p.groups - 1) / p.groups);
     g.all_rows = 0;
-    a.shared.item_rows = takes_tile(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
+    g.keep = of[0];
     const int first = launch_attention<KvSees::kAll>(g, options, workspace, workspace_bytes, stream);
     if (first != NVFP4_OK)
         return first;
     a.status = g.status;
-    return launch_attention<KvSees::kBehind>(a, options | NVFP4_FLAG_PDL, workspace, workspace_bytes, stream);
+    a.prefix = of[0];
+    a.prefix.item_rows = takes_tile(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
+    const bool joins = takes_tile(a, options);
+    if (!joins) {
+        a.keep = of[1];
+        a.keep.item_rows = nvfp4::kv_rows_item_rows(a);
+    }
+    const int second =
+        launch_attention<KvSees::kBehind>(a, options | NVFP4_FLAG_PDL, workspace, workspace_bytes, stream);
+    if (second != NVFP4_OK || joins)
+        return second;
+    return from_cuda(nvfp4::launch_kv_join(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
         abort_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    kv_pdl_begin();
+    kv_pdl_begin<S>(a.keep);
 
     // at least as many groups as the warps take in one round
     Share sh;
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
     if (sh.lo >= sh.hi) {
         if (a.all_rows && warp == kWarps)
             kv_write_other_rows(a, lane, 32);
-        if (S == KvSees::kAll && a.shared.rows && warp == kWarps)
-            kv_find_first(a, lane, 32);
+        if (S == KvSees::kBehind)
+            kv_pdl_wait();
         return;
     }
 
@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
         if (a.all_rows)
             kv_write_other_rows(a, lane, 32);
-        if (S == KvSees::kAll && a.shared.rows)
-            kv_find_first(a, lane, 32);
+        if (S == KvSees::kBehind)
+            kv_pdl_wait();
         return;
     }
 
@@ -377,57 +377,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
                 for (int e = 0; e < 4; ++e)
                     acc[nt][i][e] = 0.f;
         }
-        // ---- the prefix's results, a part a warp in turn ------------------------------------
-        // (by the CTA that has the item's first unit, while that is on its way; sums of p: by
-        // the lanes of g = 0)
-        if constexpr (S == KvSees::kBehind) {
-            if (it.q.low > 0 && u0 == 0) {
-#pragma unroll 1
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = it.row0 + nt * 8 + 2 * t + e;
-                        if (row >= it.row1)
-                            continue;
-                        const int tok = kv_token(a, row);
-                        const int64_t at = (int64_t)(it.q.base + tok) * (a.c.heads * a.group) +
-                                           it.h * a.group + row - tok * a.group;
-                        int n;
-                        const int32_t where = kv_where(a.shared, at, n);
-#pragma unroll 1
-                        for (int k = warp; k < n; k += kWarps) {
-                            const int64_t pr = where ? kv_part_row(where, k, a.shared.item_rows) : at;
-                            const float2 ml = (where ? a.shared.part_stats : a.shared.stats)[pr];
-                            const float4* src = reinterpret_cast<const float4*>(
-                                (where ? a.shared.parts : a.shared.rows) + pr * D + D / 8 * g);
-                            float4 x[KS / 2];
-#pragma unroll
-                            for (int i = 0; i < KS / 2; ++i)
-                                x[i] = src[i];
-#pragma unroll
-                            for (int z = 0; z < NT; ++z) {
-                                if (z != nt)  // (registers want fixed indices)
-                                    continue;
-                                const float now = fmaxf(m[z][e], ml.x);
-                                const float by = m[z][e] == now ? 1.f : ex2(m[z][e] - now);
-                                const float add = ml.x == now ? 1.f : ex2(ml.x - now);
-                                m[z][e] = now;
-                                l[z][e] = fmaf(l[z][e], by, g == 0 ? ml.y * add : 0.f);
-#pragma unroll
-                                for (int i = 0; i < KS / 2; ++i) {
-                                    float* o = acc[z][2 * i];
-                                    float* u = acc[z][2 * i + 1];
-                                    o[e] = fmaf(o[e], by, x[i].x * add);
-                                    o[e + 2] = fmaf(o[e + 2], by, x[i].y * add);
-                                    u[e] = fmaf(u[e], by, x[i].z * add);
-                                    u[e + 2] = fmaf(u[e + 2], by, x[i].w * add);
-                                }
-                            }
-                        }
-                    }
-            }
-        }
-
         // positions every row of the tile sees: keys in [all_lo, all_hi]
         const int32_t all_hi = kv_position<S>(it.q, kv_token(a, it.row0));
         const int32_t all_lo = Work::first_key(a, it.q, kv_token(a, it.row1 - 1));
@@ -745,9 +694,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
                   tok * a.group] =
                 ltot == 0.f ? -INFINITY : 0.6931471805599453f * (mtot + log2f(ltot));
         };
-        // First pass of shared prefixes: a row's sums as they are, the row's own place or
-        // this CTA's part of the item
-        const bool prefix = S == KvSees::kAll && a.shared.rows != nullptr;
+        // a row's sums as they are, in the row's own place or in this CTA's part of the item
+        const bool keep = S == KvSees::kBehind || (S == KvSees::kAll && a.keep.rows != nullptr);
         auto keep_stats = [&](int col, float mtot, float ltot) {
             const int row = it.row0 + col;
             if (row >= it.row1)
@@ -755,11 +703,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
             const int tok = kv_token(a, row);
             const int64_t at = (int64_t)(it.q.base + tok) * (a.c.heads * a.group) + it.h * a.group + row -
                                tok * a.group;
-            (whole ? a.shared.stats[at] : a.shared.part_stats[(int64_t)slot * R + col]) = make_float2(mtot, ltot);
+            (whole ? a.keep.stats[at] : a.keep.part_stats[(int64_t)slot * R + col]) = make_float2(mtot, ltot);
             if (u0 == 0)
-                a.shared.where[at] = whole ? 0
-                                           : (Work::last_cta(sh, it) - Work::first_cta(sh, it) + 1) << kKvPartBits |
-                                                 (slot * R + col);
+                a.keep.where[at] = (whole ? 0
+                                          : (Work::last_cta(sh, it) - Work::first_cta(sh, it) + 1) << kKvPartBits |
+                                                (slot * R + col)) |
+                                   (S == KvSees::kBehind && it.q.low > 0 ? kKvSharesBit : 0);
         };
         auto keep2 = [&](int col, int fi, int fl, float v0, float v1) {
             const int row = it.row0 + col;
@@ -768,7 +717,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
             const int tok = kv_token(a, row);
             const int64_t at = (int64_t)(it.q.base + tok) * (a.c.heads * a.group) + it.h * a.group + row -
                                tok * a.group;
-            float* dst = whole ? a.shared.rows + at * D : a.shared.parts + ((int64_t)slot * R + col) * D;
+            float* dst = whole ? a.keep.rows + at * D : a.keep.parts + ((int64_t)slot * R + col) * D;
             *reinterpret_cast<float2*>(dst + (D / 8) * (fl >> 2) + 2 * fi) = make_float2(v0, v1);
         };
         // a column's largest reference of the warps, by which all rescale
@@ -786,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
             for (int w = 0; w < kWarps; ++w)
                 lt += sm_m[w][tid] == mt ? sm_l[w][tid] : sm_l[w][tid] * ex2(sm_m[w][tid] - mt);
             sm_sum[tid] = lt;
-            if (prefix) {
+            if (keep) {
                 keep_stats(tid, mt, lt);
             } else if (whole) {
                 store_lse(tid, mt, lt);
@@ -818,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
                     const float4 o = red[w * kFrag + e];
                     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                 }
-                if (prefix) {
+                if (keep) {
                     const int col = nt * 8 + 2 * (e & 3);
                     keep2(col, e >> 5, e & 31, v.x, v.z);
                     keep2(col + 1, e >> 5, e & 31, v.y, v.w);
@@ -832,7 +781,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
             }
             compute_sync();
         }
-        if (!whole && !prefix) {
+        if (S != KvSees::kBehind && !whole && !keep) {
             // ---- join the CTAs: the last to arrive sums all parts in CTA order ----------------
             const int ca = Work::first_cta(sh, it), cb = Work::last_cta(sh, it);
             if (tid == 0) {
@@ -941,6 +890,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
         compute_sync();  // shared memory is free for the next item
         it = nx;
     }
+    if (S == KvSees::kBehind)
+        kv_pdl_wait();
 }
 
 template <KvSees S, int D, int NT, bool SPLIT, int W>
@@ -988,8 +939,8 @@ cudaError_t launch_kv_rows(const KvAttnArgs& args, void* workspace, int64_t work
     KvAttnArgs a = args;
     a.count = nullptr;
     a.part = nullptr;
-    if (S == KvSees::kAll && a.shared.rows) {
-        a.part = a.shared.parts;  // items may be cut
+    if (a.keep.rows) {
+        a.part = a.keep.parts;  // items may be cut
     } else if (workspace_bytes >= kv_rows_workspace_bytes(a.c.dim)) {
         a.count = static_cast<unsigned*>(workspace);
         a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCountBytes);

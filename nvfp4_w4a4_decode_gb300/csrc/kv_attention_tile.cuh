@@ -62,6 +62,7 @@ constexpr int kKeys = 128;                 // keys of a block
 // heads / six of 32 heads / 16 requests of 3..6 tokens on a window of 1024: 3 704 392 28.8,
 // 4 724 384 27.1, 5 716 401 27.0, 7 753 413 27.8).
 constexpr int kItemCost = 5;
+constexpr int kPrefixLeast = 4;  // blocks that a CTA takes of a shared prefix, at least
 constexpr int kDecodeWarp = 8, kMmaWarp = 12;
 constexpr int kDecodeRows = kKeys / (kMmaWarp - kDecodeWarp);  // tokens a decoding warp
 constexpr int kThreads = 32 * (kMmaWarp + 1);
@@ -132,6 +133,17 @@ __device__ __forceinline__ void fence_after()
 __device__ __forceinline__ void fence_before()
 {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+// All 512 columns of tensor memory, by a whole warp.
+__device__ __forceinline__ void tmem_alloc(uint32_t address_at)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(address_at), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t tmem)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
 // 16 or 32 columns of this warp's 32 rows, a thread a row; complete on return.
@@ -346,26 +358,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         abort_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    kv_pdl_begin();
+    kv_pdl_begin<S>(a.keep);
 
+    // (beside the work list, which waits for memory)
+    constexpr bool kAllocFirst = S != KvSees::kCausal;
+    if (kAllocFirst && warp == kMmaWarp)
+        tmem_alloc(smem_u32(&tmem_base_s));
     KvShare sh;
     KvItem it;
-    bool more = Work::start<kThreads>(a, work_sm, kItemCost + 1, sh, it);
+    // parts of a prefix are not joined here, so that fewer blocks pay a start
+    const int least = S == KvSees::kAll && a.keep.rows ? kPrefixLeast : kItemCost + 1;
+    bool more = Work::template start<kThreads>(a, work_sm, least, sh, it);
     constexpr int kDecodeThreads = 32 * (kMmaWarp - kDecodeWarp);
     const bool decodes = warp >= kDecodeWarp && warp < kMmaWarp;
     if (sh.lo >= sh.hi) {
         if (a.all_rows && decodes)
             kv_write_other_rows(a, tid - 32 * kDecodeWarp, kDecodeThreads);
-        if (S == KvSees::kAll && a.shared.rows && decodes)
-            kv_find_first(a, tid - 32 * kDecodeWarp, kDecodeThreads);
+        if (S == KvSees::kBehind)
+            kv_pdl_wait();
+        if (kAllocFirst && warp == kMmaWarp) {
+            __syncwarp();
+            tmem_free(tmem_base_s);
+        }
         return;
     }
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&tmem_base_s)),
-                     "r"(512u));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    if (!kAllocFirst && warp == kMmaWarp)
+        tmem_alloc(smem_u32(&tmem_base_s));
     fence_before();
     __syncthreads();
     fence_after();
@@ -664,10 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             ++items;
             fence_after();
             const bool whole = it.u0 == 0 && it.u1 == it.n;
-            // First pass of shared prefixes: a row's sums as they are, in the row's own place or
-            // in this CTA's part of the item
-            if (S == KvSees::kAll && a.shared.rows != nullptr) {
-                const KvShared& s = a.shared;
+            // a row's sums as they are, in the row's own place or in this CTA's part of the item
+            if (S == KvSees::kAll && a.keep.rows != nullptr) {
+                const KvParts& s = a.keep;
                 const int32_t mine_at = (2 * blockIdx.x + (it.u0 == 0 ? 1 : 0)) * kRows + st * kRowsTile + r;
                 const int64_t at = row_at();
                 if (live) {
@@ -677,15 +694,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                             : (Work::last_cta(sh, it) - Work::first_cta(sh, it) + 1)
                                                       << kKvPartBits | mine_at;
                 }
-                float* dst = whole ? s.rows + at * D : s.parts + (int64_t)mine_at * D;
+                // 16 sums of each of the warp's rows at a time, over shared memory: a row's lanes write
+                // neighbouring bytes (with a thread a row 4900 cycles a tile of 128)
+                const int64_t to = whole ? at : mine_at;
+                float* dst = whole ? s.rows : s.parts;
 #pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + i, o);
-                    if (live)
+                for (int i = 0; i < D; i += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + i, o);
+                    __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            store8(dst + i + j, o + j);
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4*>(staged + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    __syncwarp();
+                    const int c = lane & 3;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        const int x = j + (lane >> 2);
+                        const int64_t row = __shfl_sync(0xFFFFFFFFu, to, x);
+                        if (x < mine.rows)
+                            *reinterpret_cast<uint4*>(dst + row * D + i + 4 * c) =
+                                *reinterpret_cast<const uint4*>(staged + x * 64 + ((c ^ (x >> 1 & 3)) << 4));
+                    }
                 }
                 continue;
             }
@@ -694,8 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             float scale = 0.f, top = -INFINITY, all_scale = 0.f;
             int32_t where = 0;
             int parts = 0;
-            auto part = [&](int k) { return where ? kv_part_row(where, k, a.shared.item_rows) : row_at(); };
-            auto part_stats = [&](int k) { return (where ? a.shared.part_stats : a.shared.stats)[part(k)]; };
+            auto part = [&](int k) { return where ? kv_part_row(where, k, a.prefix.item_rows) : row_at(); };
+            auto part_stats = [&](int k) { return (where ? a.prefix.part_stats : a.prefix.stats)[part(k)]; };
             auto part_factor = [&](int k) {
                 const float mk = part_stats(k).x;
                 return mk == top ? 1.f : ex2(mk - top);
@@ -705,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 float by = 1.f;
                 if constexpr (S == KvSees::kBehind) {
                     if (it.q.low > 0) {
-                        where = kv_where(a.shared, row_at(), parts);
+                        kv_pdl_wait();
+                        where = kv_where(a.prefix, row_at(), parts);
                         for (int k = 0; k < parts; ++k)
                             top = fmaxf(top, part_stats(k).x);
                         by = mt == top ? 1.f : ex2(mt - top);
@@ -765,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
 #pragma unroll 1
                         for (int k = 0; k < parts; ++k) {
                             const float f = part_factor(k) * all_scale;
-                            const float* src = (where ? a.shared.parts : a.shared.rows) + part(k) * D + i;
+                            const float* src = (where ? a.prefix.parts : a.prefix.rows) + part(k) * D + i;
                             float y[32];
 #pragma unroll
                             for (int j = 0; j < 32; j += 8)
@@ -918,8 +950,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
         if (a.all_rows)
             kv_write_other_rows(a, tid - 32 * kDecodeWarp, kDecodeThreads);
-        if (S == KvSees::kAll && a.shared.rows)
-            kv_find_first(a, tid - 32 * kDecodeWarp, kDecodeThreads);
     } else {
         // ---- warp 12: the MMAs --------------------------------------------------------------------
         uint32_t one;
@@ -1002,7 +1032,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     __syncthreads();
     fence_after();
     if (warp == kMmaWarp)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+        tmem_free(tmem);
+    if (S == KvSees::kBehind)
+        kv_pdl_wait();
 }
 
 template <KvSees S, int D, bool LOW>
@@ -1024,8 +1056,8 @@ cudaError_t launch_kv_tile(const KvAttnArgs& args, void* workspace, int64_t work
     KvAttnArgs a = args;
     a.count = nullptr;
     a.part = nullptr;
-    if (S == KvSees::kAll && a.shared.rows) {
-        a.part = a.shared.parts;  // items may be cut
+    if (S == KvSees::kAll && a.keep.rows) {
+        a.part = a.keep.parts;  // items may be cut
     } else if (workspace_bytes >= kv_tile_workspace_bytes(a.c.dim)) {
         a.count = static_cast<unsigned*>(workspace);
         a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCountBytes);

@@ -432,7 +432,7 @@ PyObject* attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n)
     p.max_blocks = s.blocks;
     Tensor scratch;
     if (p.groups) {
-        const int64_t size = fn_scratch(t.r.tokens, t.r.num_q_heads, c->head_dim, t.r.reqs);
+        const int64_t size = fn_scratch(t.r.tokens, t.r.num_q_heads, c->head_dim);
         if (size < 0) {
             failed("nvfp4_kv_shared_scratch_size", (int)-size);
             return nullptr;

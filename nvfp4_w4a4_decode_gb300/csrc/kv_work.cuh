@@ -115,16 +115,35 @@ struct KvReq {
     int32_t low;   // first key seen (kBehind)
 };
 
+// Tokens of the prefix of request r's group, 0 if it is in none.
+__device__ __forceinline__ int32_t kv_prefix(const KvGroups& s, int r)
+{
+    int g = 0;
+    if (s.start) {  // the last group that begins at or before r
+        int hi = s.count;
+        while (hi - g > 1) {
+            const int mid = (g + hi) / 2;
+            if (s.start[mid] <= r)
+                g = mid;
+            else
+                hi = mid;
+        }
+        if (s.start[g] > r || r >= s.start[g + 1])
+            return 0;
+    }
+    return (int32_t)min((int64_t)max(s.prefix_len[g], 0), s.cap);
+}
+
 template <KvSees S>
 __device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
 {
     KvReq q;
     int32_t b, e, r0 = r, r1 = r + 1;
     if constexpr (S == KvSees::kAll) {
-        if (a.shared.rows) {  // r is a group: the rows of its requests
-            const int32_t n = a.shared.reqs;
-            r0 = a.shared.group_start ? min(max(a.shared.group_start[r], 0), n) : 0;
-            r1 = a.shared.group_start ? min(max(a.shared.group_start[r + 1], r0), n) : n;
+        if (a.keep.rows) {  // r is a group: the rows of its requests
+            const int32_t n = a.groups.reqs;
+            r0 = a.groups.start ? min(max(a.groups.start[r], 0), n) : 0;
+            r1 = a.groups.start ? min(max(a.groups.start[r + 1], r0), n) : n;
         }
     }
     if (a.q_start) {
@@ -141,11 +160,14 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs& a, int r)
     const int64_t cap = (int64_t)a.max_blocks << a.c.page_shift;
     q.seq = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
     if constexpr (S == KvSees::kAll) {
-        if (a.shared.rows && q.seq == 0)  // nothing shared: nothing to do
+        if (a.keep.rows && q.seq == 0)  // nothing shared: nothing to do
             q.nq = 0;
     }
-    if constexpr (S == KvSees::kBehind)
-        q.low = a.shared.first[r];
+    if constexpr (S == KvSees::kBehind) {
+        // the group's prefix if all rows lie behind it (an empty request never shares)
+        const int32_t shared = kv_prefix(a.groups, r);
+        q.low = q.nq > 0 && q.seq - q.nq >= shared ? shared : 0;
+    }
     return q;
 }
 
@@ -154,40 +176,6 @@ template <KvSees S>
 __device__ __forceinline__ int32_t kv_position(const KvReq& q, int token)
 {
     return S == KvSees::kAll ? q.seq - 1 : q.seq - q.nq + token;
-}
-
-// Prefix pass: the first own key of every request, by `threads` threads of every CTA.  A
-// request shares its group's prefix if all of its rows lie behind it (an empty one never does);
-// else it sees all its keys by itself.  A function of its own, like kv_fill_rows.
-static __device__ __noinline__ void kv_find_first(const KvAttnArgs a, int thread, int threads)
-{
-    const KvShared& s = a.shared;
-    const int64_t cap = (int64_t)a.max_blocks << a.c.page_shift;
-    for (int r = blockIdx.x * threads + thread; r < s.reqs; r += gridDim.x * threads) {
-        int g = 0;
-        bool in = true;
-        if (s.group_start) {  // the last group that begins at or before r
-            int hi = a.reqs;
-            while (hi - g > 1) {
-                const int mid = (g + hi) / 2;
-                if (s.group_start[mid] <= r)
-                    g = mid;
-                else
-                    hi = mid;
-            }
-            in = s.group_start[g] <= r && r < s.group_start[g + 1];
-        }
-        int32_t b = r * a.q_per_req, e = b + a.q_per_req;
-        if (a.q_start) {
-            b = a.q_start[r];
-            e = a.q_start[r + 1];
-        }
-        b = min(max(b, 0), a.tokens);
-        e = min(max(e, b), a.tokens);
-        const int32_t seq = (int32_t)min((int64_t)max(s.seq_len[r], 0), s.cap);
-        const int32_t shared = in ? (int32_t)min((int64_t)max(a.seq_len[g], 0), cap) : 0;
-        s.first[r] = e > b && seq - (e - b) >= shared ? shared : 0;
-    }
 }
 
 // Zeros (and lse = -inf) for the call's rows [0, begin) and [end, tokens), by `threads`
@@ -371,6 +359,9 @@ struct KvWork {
 
     static __device__ __forceinline__ bool next(const KvAttnArgs& a, const KvShare& s, KvItem& it)
     {
+        // where the next one's first unit would lie behind the share no request is looked at
+        if (S != KvSees::kCausal && it.begin + 2 * COST + it.n >= s.hi)
+            return false;
         return settle(a, s, it, after(a, it));
     }
 
@@ -502,6 +493,43 @@ struct KvWork {
         return locate(a, sh, it, rem, head);
     }
 
+    // The same with a run of requests a lane (up to kLaneReqs of them).
+    static constexpr int kLaneReqs = 8;
+    static __device__ __forceinline__ bool start_lanes(const KvAttnArgs& a, int64_t least, KvShare& sh,
+                                                       KvItem& it)
+    {
+        const int lane = threadIdx.x & 31, per = (a.reqs + 31) / 32;
+        const int ra = min(lane * per, a.reqs), rb = min(ra + per, a.reqs);
+        int64_t mine = 0;
+        for (int r = ra; r < rb; ++r) {
+            mine += a.c.heads * head_places(a, kv_req<S>(a, r), 0, 1);
+            if (blockIdx.x == 0 && kv_too_long(a, r))
+                atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
+        }
+        int64_t inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            if (lane >= d)
+                inc += o;
+        }
+        if (!cut_share(a, __shfl_sync(0xFFFFFFFFu, inc, 31), least, sh))
+            return false;
+        // the lane whose run holds sh.lo; there, the request
+        const int at = __ffs(__ballot_sync(0xFFFFFFFFu, inc > sh.lo)) - 1;
+        const int r0 = __shfl_sync(0xFFFFFFFFu, ra, at), r1 = __shfl_sync(0xFFFFFFFFu, rb, at);
+        int64_t rem = sh.lo - __shfl_sync(0xFFFFFFFFu, inc - mine, at), head = 0;
+        for (it.r = r0;; ++it.r) {
+            it.q = kv_req<S>(a, it.r);
+            head = head_places(a, it.q, 0, 1);
+            if (rem < a.c.heads * head || it.r + 1 >= r1)
+                break;
+            rem -= a.c.heads * head;
+        }
+        it.rows = it.q.nq * a.group;
+        return locate(a, sh, it, rem, head);
+    }
+
     // The whole CTA (THREADS threads) computes its share of the list and the
     // first item with a unit in it; false when there is none.
     template <int THREADS>
@@ -511,6 +539,12 @@ struct KvWork {
         if (a.reqs <= 32 && (int64_t)a.tokens * a.group <= 4 * R * (int64_t)a.reqs) {
             const bool more = start_warp(a, least, sh, it);
             __syncthreads();  // what the caller initialised
+            return more;
+        }
+        if (S != KvSees::kCausal && a.reqs <= 32 * kLaneReqs &&
+            (int64_t)a.tokens * a.group <= 4 * R * (int64_t)a.reqs) {
+            const bool more = start_lanes(a, least, sh, it);
+            __syncthreads();
             return more;
         }
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

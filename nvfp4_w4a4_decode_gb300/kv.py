@@ -38,7 +38,7 @@ SIGNATURES = {
     "nvfp4_kv_append_rotary": ([_p, _p, _u32, _p], ctypes.c_int),
     "nvfp4_kv_cross_attention": ([_p, _p, _u32, _p, ctypes.c_size_t, _p], ctypes.c_int),
     "nvfp4_kv_attention_shared": ([_p, _p, _p, _u32, _p, ctypes.c_size_t, _p], ctypes.c_int),
-    "nvfp4_kv_shared_scratch_size": ([_i64, _i64, _i64, _i64], _i64),
+    "nvfp4_kv_shared_scratch_size": ([_i64, _i64, _i64], _i64),
 }
 
 

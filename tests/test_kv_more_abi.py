@@ -153,11 +153,11 @@ def test_shared_refusals_of_the_attention(lib):
 def test_scratch_size(lib):
     f = lib.nvfp4_kv_shared_scratch_size
     for dim in (64, 128):
-        none = f(0, 1, dim, 0)  # the cut items' parts alone
-        assert none >= 64 * 512 * (4 * dim + 8) and none % 16 == 0
-        assert f(3, 32, dim, 5) == none + 3 * 32 * (4 * dim + 8 + 4) + 5 * 4
-    assert f(-1, 32, 128, 5) == f(3, 0, 128, 5) == f(3, 32, 0, 5) == f(3, 32, 128, -1) == -INVALID
-    assert f(3, 32, 96, 5) == f(1 << 30, 32, 128, 5) == f(3, 32, 128, 16385) == -UNSUPPORTED
+        none = f(0, 1, dim)  # the cut items' parts alone
+        assert none >= 2 * 64 * 512 * (4 * dim + 8) and none % 16 == 0
+        assert f(3, 32, dim) == none + 2 * 3 * 32 * (4 * dim + 8 + 4)
+    assert f(-1, 32, 128) == f(3, 0, 128) == f(3, 32, 0) == -INVALID
+    assert f(3, 32, 96) == f(1 << 30, 32, 128) == -UNSUPPORTED
 
 
 def test_calls_want_the_current_device(lib, monkeypatch):
