@@ -14,6 +14,9 @@
 // 16-element blocks of one head of K or V: the two that the rotation pairs (neighbours
 // where the pairs are interleaved, or nothing is turned).  Its units are neighbouring
 // pieces of a head, so that a warp's loads and stores are runs of whole sectors.
+//
+// What bounds it: memory (16103 tokens of 32/8 heads of 128 in BF16: 357 MB in 60.6 us, 5.9 TB/s,
+// 88 % of the copy rate) once enough loads are on their way; few tokens the launch (8 tokens: 2.5 us).
 #include "../../include/nvfp4_kv.h"
 #include "kv.cuh"
 #include "kv_quantise.cuh"
@@ -24,7 +27,14 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kManyHeads = 4;
+// With many tokens a thread turns four query heads by the angles it has loaded (two in FP32, whose
+// elements take twice the registers).  16103 tokens of 32/8 heads of 128 in BF16: 60.6 us; with
+// eight heads 88, two 69, one 114.  CTAs an SM, which the registers make room for: seven 60.6 us,
+// six 64, eight 63, nine 80, as many as come of themselves (five) 71.
+template <bool BF16>
+constexpr int kManyHeads = BF16 ? 4 : 2;
+template <bool BF16, int U>
+constexpr int kCtas = U == 1 ? 1 : BF16 ? 7 : 6;
 
 // (a, b) turned by (c, s), each operation rounded.
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s)
@@ -113,7 +123,7 @@ __device__ __forceinline__ Eight<BF16> pack(const float (&v)[8])
 // Units of a token: U query heads' pieces of 8 pairs (q_units), then pairs of blocks of K
 // and of V.
 template <bool BF16, bool WIDE, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas<BF16, U>)
     kv_rotary_kernel(const KvRotaryArgs a, uint32_t per, uint32_t q_units, int q_groups)
 {
     kv_pdl_begin();
@@ -251,10 +261,11 @@ template <bool BF16, bool WIDE>
 cudaError_t launch(const KvRotaryArgs& a, cudaStream_t stream, bool pdl)
 {
     // several heads a thread once that still leaves every SM a few CTAs
-    const int64_t units = a.tokens * ((int64_t)(a.q_heads + kManyHeads - 1) / kManyHeads * (a.c.dim / 16) +
+    constexpr int kMany = kManyHeads<BF16>;
+    const int64_t units = a.tokens * ((int64_t)(a.q_heads + kMany - 1) / kMany * (a.c.dim / 16) +
                                       a.c.heads * (a.c.dim / 16));
     return units >= (int64_t)8 * kThreads * device_sm_count(current_device())
-               ? launch_units<BF16, WIDE, kManyHeads>(a, stream, pdl)
+               ? launch_units<BF16, WIDE, kMany>(a, stream, pdl)
                : launch_units<BF16, WIDE, 1>(a, stream, pdl);
 }
 
