@@ -126,12 +126,19 @@ struct Cfg {
     // phase of the slots it reads.  Units are dealt by their number in the CTA's
     // whole sequence, so a unit's place in the ring always has the same warp.
     static_assert(kStages * kSub % W == 0, "a ring holds whole rounds of the warps");
-    // Groups that an item's start and join cost (seven warps, us for 24 requests of 1..6000
-    // tokens, FP32 queries / three FP32 prompts: 1 25 / 72, 2 21 / 59, 5 20 / 45, 8 18.8 / 42,
-    // 12 20 / 44).
-    static constexpr int kItemCost = W == 3 ? 4 : 8;
-    // Items of up to so many groups stay whole, or of up to twice a share if that is less than kWholeMax
-    static constexpr int kWhole = W == 3 ? 2 : 4, kWholeMax = W == 3 ? 16 : 4;
+};
+
+// How the list is cut.  Groups that an item's start and join cost: seven warps, us for 24 requests
+// of 1..6000 tokens, FP32 queries / three FP32 prompts: 1 25 / 72, 2 21 / 59, 5 20 / 45, 8 18.8 / 42,
+// 12 20 / 44; three warps, 20 requests of 300..1500 states: 2 15.3, 4 15.0, 6 14.5, 8 14.5, and where
+// parts are left to kv_join.cu, 64 requests of 30..900 tokens behind a prefix: 2 43.8, 4 41.4, 6 43.9.
+// Items of up to kWhole groups, or of two shares and up to kWholeMax, stay whole: 20 requests of
+// states 2 15.9, 8 16.3, 12 15.1, 16 15.0 (at a cost of 4); behind a prefix 2 41.2, 8 41.4, 16 45.1.
+template <KvSees S, int W>
+struct Cut {
+    static constexpr int kItemCost = W != 3 ? 8 : S == KvSees::kBehind ? 4 : 6;
+    static constexpr int kWhole = W != 3 ? 4 : 2;
+    static constexpr int kWholeMax = W != 3 ? 4 : S == KvSees::kBehind ? 8 : 12;
 };
 
 template <KvSees S, int D, int NT, bool SPLIT, int W>
@@ -142,7 +149,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
     constexpr int kWarps = W, kCompute = C::kCompute, kThreads = C::kThreads;
     auto compute_sync = []() { compute_barrier<C::kCompute>(); };
     constexpr int R = C::R, KS = C::KS, ST = C::kStages;
-    using Work = KvWork<R, kGroup, C::kItemCost, C::kWhole, C::kWholeMax, S>;
+    using Work = KvWork<R, kGroup, Cut<S, W>::kItemCost, Cut<S, W>::kWhole, Cut<S, W>::kWholeMax, S>;
     using Item = KvItem;
     using Share = KvShare;
     extern __shared__ __align__(128) uint8_t smem[];
