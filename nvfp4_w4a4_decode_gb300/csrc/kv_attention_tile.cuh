@@ -69,6 +69,9 @@ constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kSpan = 64;                  // keys between two looks at the reference
 constexpr float kRaise = 8.0f;             // log2 a score may pass the reference by
 constexpr float kLift = 7.0f;              // p = 2^(s - m + kLift)
+// Where rows see keys from their first block on, or none at all, the sum of kSpan probabilities tells
+// whether one of them may have passed 2^(kLift + kRaise), and their maximum is only taken then.
+constexpr float kMostSum = 0x1p15f;
 constexpr uint32_t kColS = 0, kColO = 256;  // scores and outputs, 128 columns a tile
 
 
@@ -332,6 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
 {
     using C = Cfg<D>;
     using Work = KvWork<kRows, kKeys, kItemCost, 2, 2, S>;
+    // short loops in place of straight runs of them: a first block takes 5700 cycles, most of them
+    // for its instructions (attention to 8 x 4000..6000 states 186 -> 182 us, drafted tokens behind
+    // three prefixes 64.8 -> 62.6)
+    constexpr bool kSmall = S != KvSees::kCausal;
+    constexpr bool kBySum = S != KvSees::kCausal;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) Barriers bars;
     __shared__ typename Work::Smem work_sm;
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
         auto fetch = [&](const KvItem& x) {
             const Row y = row_of(x);
             const int64_t at = (x.q.base + y.tok) * a.q_stride + (int64_t)y.head * D;
-#pragma unroll 2
+#pragma unroll kSmall ? 4 : 2
             for (int i = 0; i < 32; i += 32 / kPieces) {
                 const int z = i + lane / kPieces, c = lane % kPieces;
                 const int64_t from = __shfl_sync(0xFFFFFFFFu, at, z);
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 };
                 if (mine.rows > 0 && u == it.u0) {  // the first reference: the block's largest score
                     float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll kSmall ? 1 : 4
                     for (int c = 0; c < kKeys; c += 32) {
                         uint32_t s[32];
                         tmem_ld32(tS + c, s);
@@ -573,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 // 2048 rows on 30000 keys took 858 us, every 64 776, every 128 784);
                 // blocks that every row of the warp sees whole skip the masks
                 auto exponentials = [&](auto masked) {
-#pragma unroll
+#pragma unroll kSmall ? 1 : 2
                     for (int h = 0; h < kKeys; h += kSpan) {
                         uint32_t p16[kSpan / 2];
                         float sum;
@@ -597,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                                                  __uint_as_float(s[i + 1])), f2, neg);
                                     float p0, p1;
                                     unpair(x, p0, p1);
-                                    top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(p0, p1));
+                                    if constexpr (!kBySum)
+                                        top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(p0, p1));
                                     p0 = ex2(p0);
                                     p1 = ex2(p1);
                                     sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], pair(p0, p1));
@@ -607,12 +616,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                             float x0, x1;
                             unpair(add2(sums[0], sums[1]), x0, x1);
                             sum = x0 + x1;
-                            const float best = fmaxf(top[0], top[1]);  // against ref
+                            float best = fmaxf(top[0], top[1]);  // against ref
                             // (a row that has seen no key takes its first reference too)
-                            const bool raise =
-                                best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
+                            bool raise = best > kLift + kRaise || (m == -INFINITY && best > -INFINITY);
+                            if constexpr (kBySum)
+                                raise = !(sum <= kMostSum);
                             if (pass == 1 || !__any_sync(0xFFFFFFFFu, raise))
                                 break;
+                            if constexpr (kBySum) {
+#pragma unroll 1
+                                for (int c = 0; c < kSpan; c += 32) {
+                                    uint32_t s[32];
+                                    tmem_ld32(tS + h + c, s);
+                                    if constexpr (masked)
+                                        hide(h + c, s);
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        best = fmaxf(best, __uint_as_float(s[i]));
+                                }
+                                best = best == -INFINITY ? best : fmaf(best, f, -ref);
+                            }
                             // The first reference as it comes; then a whole number of powers of
                             // two at a time, which takes nothing from probabilities already f16.
                             float by = 0.f;
@@ -694,29 +717,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                             : (Work::last_cta(sh, it) - Work::first_cta(sh, it) + 1)
                                                       << kKvPartBits | mine_at;
                 }
-                // 16 sums of each of the warp's rows at a time, over shared memory: a row's lanes write
-                // neighbouring bytes (with a thread a row 4900 cycles a tile of 128)
-                const int64_t to = whole ? at : mine_at;
-                float* dst = whole ? s.rows : s.parts;
+                // a thread a row, a whole sector a store (over shared memory, so that lanes wrote
+                // neighbouring bytes, a tile took 6300 cycles instead of 4900)
+                float* dst = (whole ? s.rows + at * D : s.parts + (int64_t)mine_at * D);
 #pragma unroll 1
-                for (int i = 0; i < D; i += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + i, o);
-                    __syncwarp();
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + i, o);
+                    if (live)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4*>(staged + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
-                            make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    __syncwarp();
-                    const int c = lane & 3;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        const int x = j + (lane >> 2);
-                        const int64_t row = __shfl_sync(0xFFFFFFFFu, to, x);
-                        if (x < mine.rows)
-                            *reinterpret_cast<uint4*>(dst + row * D + i + 4 * c) =
-                                *reinterpret_cast<const uint4*>(staged + x * 64 + ((c ^ (x >> 1 & 3)) << 4));
-                    }
+                        for (int j = 0; j < 32; j += 8)
+                            store8(dst + i + j, o + j);
                 }
                 continue;
             }
