@@ -266,7 +266,7 @@ typedef struct {
     const int32_t* group_start; /* int32 [groups + 1], ascending, or NULL: one group of all
                                    requests (groups is 1 then) */
     int64_t groups;             /* at most 16384; 0: nothing is shared */
-    void* scratch;              /* nvfp4_kv_shared_scratch_size() bytes, 16-byte aligned, any contents,
+    void* scratch;              /* nvfp4_kv_shared_scratch_size() bytes, 32-byte aligned, any contents,
                                    not used by another call at the same time */
     size_t scratch_bytes;
 } nvfp4_kv_prefixes;

@@ -14,6 +14,18 @@ using nvfp4::KvSees;
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
+int sm_count()
+{
+    return nvfp4::device_sm_count(nvfp4::current_device());
+}
+
+// Bytes of what one of two passes over `rows` rows leaves, but for KvParts::where; its sums begin
+// on a sector's boundary.
+int64_t pass_bytes(int64_t rows, int64_t dim)
+{
+    return ((rows + nvfp4::kv_part_total(sm_count())) * (dim * 4 + 8) + 31) / 32 * 32;
+}
+
 // Whether the tcgen05 kernel takes an attention call: its tiles of 128 rows and
 // its start of some microseconds an item want many rows a request, and enough of
 // them in all.  Measured both ways on GB300 (rows kernel / tile kernel, us): 64
@@ -26,11 +38,6 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
 {
     return rows > 32 && reqs * heads * rows >= 2048;
-}
-
-int sm_count()
-{
-    return nvfp4::device_sm_count(nvfp4::current_device());
 }
 
 bool aligned(const void* p, uintptr_t a)
@@ -424,8 +431,8 @@ int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_
         return -NVFP4_ERR_INVALID_ARG;
     if ((head_dim != 64 && head_dim != 128) || tokens >= kMaxTokens || num_q_heads > (1 << 22))
         return -NVFP4_ERR_UNSUPPORTED;
-    const int64_t rows = tokens * num_q_heads, parts = nvfp4::kv_part_total(sm_count());
-    return 2 * ((rows + parts) * (head_dim * 4 + 8) + rows * 4);  // of the two passes
+    const int64_t rows = tokens * num_q_heads;
+    return 2 * (pass_bytes(rows, head_dim) + rows * 4);
 }
 
 int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
@@ -452,23 +459,23 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
     const int64_t rows = (int64_t)a.tokens * args->num_q_heads;
     if (p.prefix_len == nullptr || (p.max_blocks > 0 && p.block_table == nullptr) || p.scratch == nullptr ||
         !aligned(p.prefix_len, 4) || !aligned(p.block_table, 4) || !aligned(p.group_start, 4) ||
-        !aligned(p.scratch, 16) ||
+        !aligned(p.scratch, 32) ||
         (int64_t)p.scratch_bytes < nvfp4_kv_shared_scratch_size(a.tokens, args->num_q_heads, a.c.dim))
         return NVFP4_ERR_INVALID_ARG;
     const int64_t parts = nvfp4::kv_part_total(sm_count());
     nvfp4::KvParts of[2];
-    uint8_t* at = static_cast<uint8_t*>(p.scratch);
-    for (nvfp4::KvParts& x : of) {
+    for (int i = 0; i < 2; ++i) {
+        nvfp4::KvParts& x = of[i];
+        uint8_t* at = static_cast<uint8_t*>(p.scratch) + i * pass_bytes(rows, a.c.dim);
         x.rows = reinterpret_cast<float*>(at);
         x.parts = x.rows + rows * a.c.dim;
         x.stats = reinterpret_cast<float2*>(x.parts + parts * a.c.dim);
         x.part_stats = x.stats + rows;
         x.total = parts;
         x.item_rows = 0;
-        at = reinterpret_cast<uint8_t*>(x.part_stats + parts);
+        x.where = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(p.scratch) + 2 * pass_bytes(rows, a.c.dim)) +
+                  i * rows;
     }
-    of[0].where = reinterpret_cast<int32_t*>(at);
-    of[1].where = of[0].where + rows;
     a.groups = {p.group_start, p.prefix_len, (int32_t)p.groups, a.reqs, p.max_blocks << a.c.page_shift};
     nvfp4::KvAttnArgs g = a;
     g.table = p.block_table;

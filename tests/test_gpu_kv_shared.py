@@ -136,6 +136,17 @@ def test_head_groups(nv, kernel, dtype, hq, hkv):
     run_shared(nv, [(77, [(5, 1), (130, 2), (1, 1)])], hq, hkv, 128, 32, dtype, kernel=kernel, seed=hq)
 
 
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+@pytest.mark.parametrize("hq,hkv", [(7, 1), (5, 1), (1, 1), (9, 3)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_odd_numbers_of_rows(nv, kernel, dtype, hq, hkv, dim):
+    """Rows times heads of every remainder, cut items and whole ones: what the passes leave each other
+    lies on its boundaries."""
+    for counts in ([1], [1, 1], [2, 1], [1, 1, 2], [3, 2], [5, 6]):
+        run_shared(nv, [(300, [(9 + c, c) for c in counts])], hq, hkv, dim, 16, dtype, kernel=kernel)
+    run_shared(nv, [(20000, [(9, 5), (700, 6)])], hq, hkv, dim, 64, dtype, kernel=kernel)
+
+
 GROUPS = [
     # groups of different sizes, one empty, one without a prefix
     [(300, [(5, 1), (40, 1)]), (0, [(7, 1), (100, 2)]), (50, []), (16, [(1, 1)]), (129, [(3, 2), (20, 20), (64, 1)])],
@@ -613,3 +624,116 @@ def test_a_decode_step(nv, dtype):
     assert nv.device_status() == 0
     kk, _ = page_values(cache.pool[states[0, 0].long()][None], page, dim)
     assert (kk[0].transpose(0, 1) * cache.k_g.double() - kv[:page, :hkv].double()).abs().max() < 1.0
+
+
+# ---- references that rise --------------------------------------------------------------------
+
+def rising(nv, cache, table, lo, hi, gen, step=1 / 100, down=False):
+    """Keys whose scores grow along the tokens [lo, hi) of a table's row; returns the direction."""
+    page, heads, dim = cache.page_size, cache.num_kv_heads, cache.head_dim
+    base = torch.randn((dim,), generator=gen, device="cuda")
+    i = torch.arange(hi - lo, device="cuda")
+    k = ((hi - lo - 1 - i if down else i)[:, None, None] * (base * step)).expand(-1, heads, -1).contiguous()
+    v = torch.randn((hi - lo, heads, dim), generator=gen, device="cuda")
+    at = lo + i
+    slots = table[at // page].long() * page + at % page
+    nv.kv_append(cache, k, v, slots)
+    return base, k
+
+
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_cross_growing_scores(nv, kernel, dtype, dim):
+    """Scores of hundreds that rise (or fall) along the states, whole requests and cut ones: what was summed
+    is rescaled again and again, also inside a block and where only a few of a warp's rows rise."""
+    n = 1900
+    for down in (False, True):
+        cache, table, gen = make(nv, [(0, n)], 1, dim, 16)
+        table = table.cuda()
+        base, k = rising(nv, cache, table[0], 0, n, gen, 1 / 300, down)
+        cache.k_g.copy_(nv.global_scale(k))
+        nv.kv_append(cache, k, torch.randn((n, 1, dim), generator=gen, device="cuda"),
+                     table[0, torch.arange(n, device="cuda") // 16].long() * 16 + torch.arange(n, device="cuda") % 16)
+        q = torch.randn((70, 4, dim), generator=gen, device="cuda")
+        q[::3] += base * 10
+        q[1::7] -= base * 5
+        q = q.to(dtype)
+        for ws in (None, False):
+            out, lse = nv.kv_cross_attention(cache, q, table, ints([n]), return_lse=True, kernel=getattr(nv, kernel),
+                                             workspace=ws)
+            ref = attend(q, [table_values(cache, table[0], 0, n)], [70], causal=False)
+            check_attention(out, lse, ref, dtype)
+
+
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+def test_shared_growing_scores(nv, kernel, dtype):
+    """The same through a prefix into the own keys of prompts behind it."""
+    s = Shared(nv, [(1000, [(300, 200), (90, 3)])], 4, 1, 64, 16, dtype)
+    s.cache.k_g.fill_(5.0 / 300 * 1000 / 2688)
+    base, _ = rising(nv, s.cache, s.prefix_table[0], 0, 1000, s.gen, 1 / 300)
+    for r in range(2):
+        rising(nv, s.cache, s.table[r], 1000, s.seqs[r], s.gen, 1 / 100, down=bool(r))
+    q = s.q.float()
+    q[::3] += base * 8
+    q = q.to(dtype)
+    out, lse = s.call(nv, q, kernel=getattr(nv, kernel))
+    check_attention(out, lse, s.ref(q=q), dtype)
+
+
+@pytest.mark.parametrize("name", ["KERNEL_KV_ROWS", "KERNEL_KV_TILE"])
+def test_cross_probabilities_are_rounded_once(nv, name):
+    """One f16 rounding of each probability (the bound's 2^-11), also where the reference rises inside a
+    block: 128 keys of score 0, 64 about 2^7 times as probable with values of +1, then 16 about 2^9
+    times with values of -1, so that the rest of the two sums is what roundings leave."""
+    n, rows, group = 320, 64, 64
+    unit = 1.4426950408889634  # scores below are in powers of two
+    cache, table, gen = make(nv, [(0, n)], 1, 64, 16)
+    table = table.cuda()
+    k = torch.zeros((n, 1, 64), device="cuda")
+    k[128:192, 0, 0] = 6.0
+    k[192:208, 0, 16] = 6.0
+    k[128:192, 0, 1] = k[192:208, 0, 17] = 0.5  # a twelfth, for scores between those of BF16 queries
+    k[208:, 0, 32] = -6.0                     # as good as unseen
+    v = torch.zeros((n, 1, 64), device="cuda")
+    v[128:192], v[192:208] = 1.0, -1.0
+    cache.k_g.fill_(1.0)
+    cache.v_g.fill_(1.0)
+    slots = table[0, :n // 16].long().repeat_interleave(16) * 16 + torch.arange(n, device="cuda") % 16
+    nv.kv_append(cache, k, v, slots)
+    q = torch.zeros((rows, group, 64), device="cuda")
+    rand = lambda: torch.rand((rows, group), generator=gen, device="cuda")  # noqa: E731
+    q[..., 1], q[..., 17] = rand(), rand()
+    q[..., 0] = (7.0 + 0.08 * rand() - 0.5 * q[..., 1]) / 6.0
+    q[..., 16] = (8.93 + 0.069 * rand() - 0.5 * q[..., 17]) / 6.0
+    q[..., 32] = 10.0
+    q = q.to(BF16)
+    out, lse = nv.kv_cross_attention(cache, q, table, ints([n]), scale=1.0 / unit, return_lse=True,
+                                     kernel=getattr(nv, name), workspace=False)
+    ref = attend(q, [table_values(cache, table[0], 0, n)], [rows], 1.0 / unit, causal=False)
+    check_attention(out, lse, ref, BF16)
+
+
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+def test_pages_and_layers(nv, kernel, dtype):
+    """Strided pages (one pool for several layers), every page size, prefixes that end inside a page."""
+    for page in (16, 32, 64, 128, 256):
+        run_shared(nv, [(page + 5, [(page * 2, 1), (3, 3)]), (page, [(1, 1)])], 8, 4, 128, page, dtype, kernel=kernel,
+                   layers=3)
+
+
+def test_starts_that_go_back_lead_nowhere(nv):
+    """A request's rows reach over those of its group: what the first pass has not written is not followed
+    (results mean nothing there); the next call is right."""
+    s = Shared(nv, [(300, [(5, 1), (20, 3)]), (40, [(9, 2)])], 8, 2, 64, 16, BF16)
+    want, _ = s.call(nv)
+    for fill in (math.nan, 1e30, 2.0, 0.0):
+        old = [torch.full((1 << 22,), fill, device="cuda") for _ in range(8)]  # memory that the call may take
+        old += [torch.full((1 << 22,), 2 ** 31 - 1, dtype=torch.int32, device="cuda") for _ in range(4)]
+        del old
+        for start in ([0, 5, 2, 6], [0, 6, 1, 4], [2, 6, 0, 6], [0, 1, 0, 6]):
+            for kernel in (nv.KERNEL_KV_ROWS, nv.KERNEL_KV_TILE):
+                s.call(nv, q_start=ints(start), kernel=kernel)
+    torch.cuda.synchronize()
+    nv.device_status(clear=True)
+    out, _ = s.call(nv)
+    assert torch.equal(out, want) and nv.device_status() == 0

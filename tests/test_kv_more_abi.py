@@ -130,7 +130,7 @@ def prefixes(**change):
     (dict(groups=16385), UNSUPPORTED), (dict(blocks=1 << 27, stride=1 << 27), UNSUPPORTED),
     (dict(lens=None), INVALID), (dict(table=None), INVALID), (dict(scratch=None), INVALID),
     (dict(lens=FAKE + 2), INVALID), (dict(table=FAKE + 2), INVALID), (dict(start=FAKE + 1), INVALID),
-    (dict(scratch=FAKE + 8), INVALID), (dict(size=2 * 32 * (512 + 8)), INVALID), (dict(size=None), INVALID)])
+    (dict(scratch=FAKE + 16), INVALID), (dict(size=2 * 32 * (512 + 8)), INVALID), (dict(size=None), INVALID)])
 def test_shared_refusals(lib, change, status):
     assert lib.nvfp4_kv_attention_shared(cache(), attention(), prefixes(**change), 0, None, 0, None) == status
 
@@ -156,6 +156,9 @@ def test_scratch_size(lib):
         none = f(0, 1, dim)  # the cut items' parts alone
         assert none >= 2 * 64 * 512 * (4 * dim + 8) and none % 16 == 0
         assert f(3, 32, dim) == none + 2 * 3 * 32 * (4 * dim + 8 + 4)
+        for tokens in range(1, 9):  # the second pass's half begins on a boundary, whatever the rows
+            half = (f(tokens, 7, dim) - 2 * tokens * 7 * 4) // 2
+            assert half % 32 == 0 and 0 <= half - none // 2 - tokens * 7 * (4 * dim + 8) < 32
     assert f(-1, 32, 128) == f(3, 0, 128) == f(3, 32, 0) == -INVALID
     assert f(3, 32, 96) == f(1 << 30, 32, 128) == -UNSUPPORTED
 
