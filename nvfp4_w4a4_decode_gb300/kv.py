@@ -210,7 +210,7 @@ def nvfp4_kv_append(cache: KVCache, k, v, slots, pdl: bool = False) -> None:
 
 
 def nvfp4_kv_append_rotary(cache: KVCache, q, k, v, slots, positions, rotary, *, interleaved: bool = False,
-                           out=None, pdl: bool = False):
+                           out=None, pdl: bool = True):
     """``kv_append`` with the position rotation on the way: queries and keys are turned by
     their token's angles, and the keys go from there into the cache without a rounding between.
 
@@ -220,7 +220,8 @@ def nvfp4_kv_append_rotary(cache: KVCache, q, k, v, slots, positions, rotary, *,
     i turns the elements i and i + n / 2 of a head, or 2 i and 2 i + 1 (``interleaved``); the elements
     from n on stay.  Returns the turned queries in q's dtype (a new tensor, or ``out``, which may be q
     itself).  Rows with slot -1 are turned, not appended; positions outside the table give zeros, append
-    nothing and set DEVICE_KV_RANGE in ``device_status()``."""
+    nothing and set DEVICE_KV_RANGE in ``device_status()``.  ``pdl``: the launch may begin while the
+    kernel in front of it ends, which it waits for before its first access."""
     return (_calls or _binding()).append_rotary(
         cache._desc, cache._dev, q, k, v, slots, positions, rotary, interleaved, out, FLAG_PDL if pdl else 0,
         _stream(_current(cache._dev)))
@@ -269,13 +270,14 @@ def nvfp4_kv_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
 def nvfp4_kv_cross_attention(cache: KVCache, q, block_table, seq_len, q_start=None, *,
                              max_q: int | None = None, scale: float | None = None, out=None,
                              out_dtype=None, return_lse: bool = False, kernel: int = KERNEL_AUTO,
-                             workspace=None, pdl: bool = False):
+                             workspace=None, pdl: bool = True):
     """Attention of q [tokens, num_q_heads, head_dim] to all that the cache holds of each
     request: the states of an encoder, of any length beside the request's rows.
 
     ``seq_len`` int32 [reqs]: states in the cache (written by ``kv_append``); every row of a
-    request sees all of them, and with 0 gets zeros and lse = -inf.  All else as for
-    ``kv_attention``."""
+    request sees all of them, and with 0 gets zeros and lse = -inf.  ``pdl``: the launch may begin
+    while the kernel in front of it ends, which it waits for before its first access.  All else as
+    for ``kv_attention``."""
     stream = _stream(_current(cache._dev))
     wp, wn, _keep = _space(cache, workspace, stream)
     if out_dtype not in _OUT:
@@ -288,7 +290,7 @@ def nvfp4_kv_cross_attention(cache: KVCache, q, block_table, seq_len, q_start=No
 def nvfp4_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len, block_table, seq_len, q_start=None, *,
                               group_start=None, max_q: int | None = None, scale: float | None = None, out=None,
                               out_dtype=None, return_lse: bool = False, kernel: int = KERNEL_AUTO,
-                              workspace=None, pdl: bool = False):
+                              workspace=None, pdl: bool = True):
     """``kv_attention`` of requests that share prefixes, each read once for all of its requests.
 
     ``prefix_len`` int32 [groups]: tokens of each prefix, which need not end with a page;
@@ -297,8 +299,10 @@ def nvfp4_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len, block
     positions count the prefix: ``seq_len`` holds whole lengths, and ``block_table`` entry b the
     tokens from b * page_size on, of which those wholly inside the prefix are not looked up.
     (Tables, slots and positions of ``kv_tables`` fit as they are.)  A request with a row inside the
-    prefix, or with no tokens, shares nothing: it is attended on its own pages alone.  All else as for
-    ``kv_attention``; ``kernel`` forces the kernel of both passes."""
+    prefix, or with no tokens, shares nothing: it is attended on its own pages alone.  ``kernel``
+    forces the kernel of both passes; ``pdl``: the first launch may begin while the kernel in front
+    of it ends, which it waits for before its first access.  A call takes scratch memory of about 1 KB
+    a row and query head (at head_dim 128), and 81 MB.  All else as for ``kv_attention``."""
     stream = _stream(_current(cache._dev))
     wp, wn, _keep = _space(cache, workspace, stream)
     if out_dtype not in _OUT:
