@@ -40,6 +40,27 @@ bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
     return rows > 32 && reqs * heads * rows >= 2048;
 }
 
+// The same for a prefix that requests share: its parts are joined by another kernel, so that items
+// cut between all SMs cost little.  Measured both ways (rows kernel / tile kernel for the prefix, us
+// a call; one group of single tokens, heads of 128, a prefix of 500 / 8000 / 60000 tokens): 16 rows of 8
+// kv heads 14.4 22 39 / 19.2 23 58; 24 rows 18.0 28 55 / 19.6 26 60; 48 rows 18.3 29 83 / 19.6 27 61; 264 rows
+// of 4 kv heads (500, 4000, 30000) 28 34 91 / 24 27 48.
+bool use_tile_for_prefix(int64_t rows)
+{
+    return rows > 16;
+}
+
+// The same for the keys behind a prefix, which the rows kernel takes beside the prefix's pass and
+// leaves to the kernel that joins, while the tile kernel waits for the prefix and joins itself.
+// Measured both ways (rows / tile for these keys, us a call; a prefix of 2000, 0 / 300 / 3000 tokens
+// and the new ones behind it, by requests x kv heads x rows): 4 x 8 x 80 34 36 58 / 42 48 72; 4 x 8 x 160 46 50
+// 77 / 45 57 76; 32 x 2 x 84 46 51 86 / 47 61 83; 32 x 4 x 48 37 43 69 / 33 50 67; 32 x 2 x 140 62 67 122 / 47 61 85;
+// 32 x 8 x 80 100 115 258 / 72 92 168.
+bool use_tile_behind(int64_t reqs, int64_t heads, int64_t rows)
+{
+    return rows > 32 && reqs * heads * rows >= 6144;
+}
+
 bool aligned(const void* p, uintptr_t a)
 {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
@@ -200,11 +221,16 @@ int check_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* 
     return NVFP4_OK;
 }
 
+template <KvSees S>
 bool takes_tile(const nvfp4::KvAttnArgs& a, uint32_t options)
 {
     const uint32_t kern = options & NVFP4_KERNEL_MASK;
-    return kern == NVFP4_KERNEL_KV_TILE || (kern == NVFP4_KERNEL_AUTO && a.q_bf16 && a.out_bf16 &&
-                                            use_tile(a.reqs, a.c.heads, (int64_t)a.max_q * a.group));
+    if (kern != NVFP4_KERNEL_AUTO || !a.q_bf16 || !a.out_bf16)
+        return kern == NVFP4_KERNEL_KV_TILE;
+    const int64_t rows = (int64_t)a.max_q * a.group;
+    if (S == KvSees::kBehind)
+        return use_tile_behind(a.reqs, a.c.heads, rows);
+    return S == KvSees::kAll && a.keep.rows ? use_tile_for_prefix(rows) : use_tile(a.reqs, a.c.heads, rows);
 }
 
 template <KvSees S>
@@ -213,7 +239,7 @@ int launch_attention(nvfp4::KvAttnArgs& a, uint32_t options, void* workspace, si
 {
     if (a.status == nullptr && nvfp4::device_status_address(&a.status) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-    const auto launch = takes_tile(a, options) ? nvfp4::launch_kv_tile<S> : nvfp4::launch_kv_rows<S>;
+    const auto launch = takes_tile<S>(a, options) ? nvfp4::launch_kv_tile<S> : nvfp4::launch_kv_rows<S>;
     return from_cuda(launch(a, workspace, (int64_t)workspace_bytes, static_cast<cudaStream_t>(stream),
                             (options & NVFP4_FLAG_PDL) != 0));
 }
@@ -492,8 +518,8 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
         return first;
     a.status = g.status;
     a.prefix = of[0];
-    a.prefix.item_rows = takes_tile(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
-    const bool joins = takes_tile(a, options);
+    a.prefix.item_rows = takes_tile<KvSees::kAll>(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
+    const bool joins = takes_tile<KvSees::kBehind>(a, options);
     if (!joins) {
         a.keep = of[1];
         a.keep.item_rows = nvfp4::kv_rows_item_rows(a);
