@@ -1,5 +1,7 @@
 // kv_attention_rows.cuh -- attention over the paged NVFP4 cache with few query
-// rows a request: single tokens, drafted tokens, short prompts.
+// rows a request: single tokens, drafted tokens, short prompts.  Which keys a row sees is a
+// template's matter (KvSees): causal attention, all keys (cross attention; a prefix that a group of
+// requests shares, whose rows are then one request's), the keys behind such a prefix.
 //
 // Mathematics.  With K = k_g sK cK (codes cK, block scales sK), a score is
 // scale k_g sum_d q_d (sK cK)_d.  sK cK has at most 6 significant bits and
@@ -30,12 +32,13 @@
 //
 // Work.  One list of 64-token groups for all requests (kv_work.cuh), equal shares a
 // CTA; the 32-token units of an item's groups are dealt to the CTA's seven
-// compute warps in turn.  An eighth warp runs ahead through the list, across
+// compute warps (three behind a prefix) in turn.  One more warp runs ahead through the list, across
 // items: it looks up the pages and fills a ring of groups with bulk copies --
 // a page of up to 64 tokens holds all four pieces of a kv head in one run of
 // bytes, so a group is one to four copies.  Compute warps join through shared
 // memory at an item's end; items cut between CTAs are joined by the last of
-// them to arrive, in CTA order.  Each item counts kItemCost groups more than it
+// them to arrive, in CTA order, or where two passes share a row's keys are left to
+// kv_join.cu as they are.  Each item counts kItemCost groups more than it
 // has: its start and join cost about that, so that shares of many short
 // requests take equal time.  Every wait has a clock budget: one that runs out
 // sets NVFP4_DEVICE_WAIT_TIMEOUT and all waits after it are passed over.
@@ -47,7 +50,10 @@
 // 6000..8191 tokens, 8 kv heads, a token each: 110 us, 4.6 TB/s of codes and scales; two of
 // 100000..131071: 59.5 us, 4.3 TB/s).  For few tokens the chain list - queries - units -
 // join, about 9.5 us (one request of 1000); a launch's fixed parts measured in cycles: list 2300, queries
-// 1700, first units 2800, warps' join 1400, part and counter 2000, CTAs' join 5000.
+// 1700, first units 2800, warps' join 1400, part and counter 2000, CTAs' join 5000.  Where every SM has one or
+// two short items each of these runs once, and a third to a half of a warp's time goes into fetching its
+// instructions (20 requests of 300..1500 states, 16 heads of 64: 14.6 us, no instruction 4.4 of 9.7 stalls
+// an issue; 16 tokens at a time instead of two times 16, half the code: 14.7 instead of 14.0).
 #pragma once
 
 #include "formats.cuh"
@@ -100,8 +106,11 @@ __device__ __forceinline__ int token_of_row(int k)
 }
 
 // W compute warps a CTA.  Seven: with the copying warp eight, two for each of the SM's four
-// register files.  Three, with four CTAs an SM: an item's start and join, which wait for
-// memory and for one another, overlap those of three other CTAs.
+// register files.  Three, with four CTAs an SM, for the few keys that requests mostly have behind a
+// shared prefix: an item's start and end, which wait for memory and for instructions, overlap
+// those of three other CTAs (seven / three warps, us: four requests of 300 tokens behind 2000 19.7 / 15.9, 64
+// of 30..900 41.0 / 38.3, 64 of 3000 83.8 / 87.3, eight of 20000 66.8 / 72.6; without a prefix, 64 of 100
+// 12.0 / 8.7, 20 of 300..1500 14.7 / 14.0, eight of 1500 12.0 / 13.8, 64 of 6000..8191 108.7 / 124.8).
 template <int D, int NT, bool SPLIT, int W>
 struct Cfg {
     static constexpr int kCompute = 32 * W;
@@ -130,15 +139,14 @@ struct Cfg {
 
 // How the list is cut.  Groups that an item's start and join cost: seven warps, us for 24 requests
 // of 1..6000 tokens, FP32 queries / three FP32 prompts: 1 25 / 72, 2 21 / 59, 5 20 / 45, 8 18.8 / 42,
-// 12 20 / 44; three warps, 20 requests of 300..1500 states: 2 15.3, 4 15.0, 6 14.5, 8 14.5, and where
-// parts are left to kv_join.cu, 64 requests of 30..900 tokens behind a prefix: 2 43.8, 4 41.4, 6 43.9.
-// Items of up to kWhole groups, or of two shares and up to kWholeMax, stay whole: 20 requests of
-// states 2 15.9, 8 16.3, 12 15.1, 16 15.0 (at a cost of 4); behind a prefix 2 41.2, 8 41.4, 16 45.1.
-template <KvSees S, int W>
+// 12 20 / 44; three warps, whose parts are left to kv_join.cu, 64 requests of 30..900 tokens behind a
+// prefix: 2 43.8, 4 41.4, 6 43.9.  Items of up to kWhole groups, or of two shares and up to kWholeMax,
+// stay whole (the same requests: 2 41.2, 8 41.4, 16 45.1).
+template <int W>
 struct Cut {
-    static constexpr int kItemCost = W != 3 ? 8 : S == KvSees::kBehind ? 4 : 6;
-    static constexpr int kWhole = W != 3 ? 4 : 2;
-    static constexpr int kWholeMax = W != 3 ? 4 : S == KvSees::kBehind ? 8 : 12;
+    static constexpr int kItemCost = W == 3 ? 4 : 8;
+    static constexpr int kWhole = W == 3 ? 2 : 4;
+    static constexpr int kWholeMax = W == 3 ? 8 : 4;
 };
 
 template <KvSees S, int D, int NT, bool SPLIT, int W>
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
     constexpr int kWarps = W, kCompute = C::kCompute, kThreads = C::kThreads;
     auto compute_sync = []() { compute_barrier<C::kCompute>(); };
     constexpr int R = C::R, KS = C::KS, ST = C::kStages;
-    using Work = KvWork<R, kGroup, Cut<S, W>::kItemCost, Cut<S, W>::kWhole, Cut<S, W>::kWholeMax, S>;
+    using Work = KvWork<R, kGroup, Cut<W>::kItemCost, Cut<W>::kWhole, Cut<W>::kWholeMax, S>;
     using Item = KvItem;
     using Share = KvShare;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -180,8 +188,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
     if (sh.lo >= sh.hi) {
         if (a.all_rows && warp == kWarps)
             kv_write_other_rows(a, lane, 32);
-        if (S == KvSees::kBehind)
-            kv_pdl_wait();
+        kv_pdl_end<S>();
         return;
     }
 
@@ -281,8 +288,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
             atomicOr(a.status, NVFP4_DEVICE_KV_RANGE);
         if (a.all_rows)
             kv_write_other_rows(a, lane, 32);
-        if (S == KvSees::kBehind)
-            kv_pdl_wait();
+        kv_pdl_end<S>();
         return;
     }
 
@@ -897,8 +903,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, SPLIT, W>::kThreads, Cfg<D, NT, SPL
         compute_sync();  // shared memory is free for the next item
         it = nx;
     }
-    if (S == KvSees::kBehind)
-        kv_pdl_wait();
+    kv_pdl_end<S>();
 }
 
 template <KvSees S, int D, int NT, bool SPLIT, int W>
@@ -928,7 +933,7 @@ cudaError_t launch_rows(const KvAttnArgs& a, cudaStream_t stream, bool pdl)
 {
     switch (item_rows(a)) {
     case 8:
-        return launch<S, D, 1, SPLIT, S == KvSees::kCausal ? 7 : 3>(a, stream, pdl);
+        return launch<S, D, 1, SPLIT, S == KvSees::kBehind ? 3 : 7>(a, stream, pdl);
     case 16:
         return launch<S, D, 2, SPLIT, 7>(a, stream, pdl);
     default:

@@ -5,7 +5,9 @@
 // exact f16, BF16 query rows scaled by powers of two as (practically) exact f16,
 // scores and outputs accumulate in FP32 in tensor memory, the softmax runs online
 // against a reference per row that is raised lazily, probabilities enter the
-// second product as f16 (scaled by 2^7), row sums are FP32.
+// second product as f16 (scaled by 2^7), row sums are FP32.  Which keys a row sees is a
+// template's matter (KvSees): causal attention, all keys (cross attention; a prefix that a group of
+// requests shares), the keys behind such a prefix, whose outputs take the prefix's parts in.
 //
 // One CTA an SM, 256 query rows (token, head of the group) of one kv head as two
 // 128-row tiles, 128 keys at a time:
@@ -35,7 +37,15 @@
 // decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
 // cycles.  2048 queries of 32 heads on 32049 keys: 768 us, 1.36 PFLOP/s; four prompts of
 // 2185..3879 tokens and 64 heads: 723 us, 0.94 PFLOP/s (an item's queries, first
-// block, masked last block and output add about 9 us to its keys).
+// block, masked last block and output add about 9 us to its keys).  5065 rows of 64 heads on a shared
+// prefix of 12001 keys: 1500 us, 1.33 PFLOP/s; 2183 rows of 32 heads on 4000..6000 states: 177 us, 1.02
+// PFLOP/s.  There a tile's block takes 3490 cycles, 1790 from scores to probabilities and 1700 until the next
+// scores are there (1024 of its own products).  Exponentials are not what bounds it: with an eighth of them
+// on the FMA pipe (a polynomial) the prefix took 7 % longer.  Neither are the loads of scores: 64 columns at
+// once instead of twice 32 cost registers that are not there (6 % longer).
+// A prefix for few rows (64 tokens of 32 heads on 8003 keys: 21 us, 136 CTAs of four blocks) pays a start of
+// 18000 cycles a CTA: list 3600, queries 6900, the first block's scores 1200, its softmax 5400 (most of it
+// for instructions).
 //
 // Waits have clock budgets; when one runs out NVFP4_DEVICE_WAIT_TIMEOUT is set,
 // later waits are passed over, MMAs in flight are drained and tensor memory is
@@ -382,8 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     if (sh.lo >= sh.hi) {
         if (a.all_rows && decodes)
             kv_write_other_rows(a, tid - 32 * kDecodeWarp, kDecodeThreads);
-        if (S == KvSees::kBehind)
-            kv_pdl_wait();
+        kv_pdl_end<S>();
         if (kAllocFirst && warp == kMmaWarp) {
             __syncwarp();
             tmem_free(tmem_base_s);
@@ -1044,8 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
     fence_after();
     if (warp == kMmaWarp)
         tmem_free(tmem);
-    if (S == KvSees::kBehind)
-        kv_pdl_wait();
+    kv_pdl_end<S>();
 }
 
 template <KvSees S, int D, bool LOW>

@@ -5,7 +5,10 @@
 //
 // A warp a row: its lanes take the parts' references and sums, 32 at a time, then four elements
 // each of all parts, eight loads on their way at once.  What bounds it: two loads that wait for
-// one another (where the parts lie, the parts) and the launch, which the passes hide.
+// one another (where the parts lie, the parts); its launch is hidden by the passes (64 tokens of 32
+// heads, 17 parts of a prefix each: 11 us alone with nothing cached, 3 us behind the passes; with the
+// parts added up by the second pass at its items' starts the call took 46.2 us instead of 45.5, a call
+// of two tokens 17.7 instead of 14.5).
 #include <cuda_bf16.h>
 
 #include "kv.cuh"
