@@ -254,9 +254,9 @@ int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attenti
  * pages, as by nvfp4_kv_attention.  Requests of no group share nothing.  A prefix need not
  * end with a page (the rest of its last page is a request's own page then), and may be
  * empty (0 or less).
- * args->window is 0 (else NVFP4_ERR_INVALID_ARG).  Options, workspace, statuses and what is
- * done about bad entries as for nvfp4_kv_attention, for both tables; the kernel choice
- * of the options is that of both passes.
+ * args->window is 0 (else NVFP4_ERR_INVALID_ARG), tokens * num_q_heads below 2^31 (else
+ * NVFP4_ERR_UNSUPPORTED).  Options, workspace, statuses and what is done about bad entries as for
+ * nvfp4_kv_attention, for both tables; the kernel choice of the options is that of both passes.
  */
 typedef struct {
     const int32_t* block_table; /* int32 [groups][table_stride] */
@@ -271,8 +271,8 @@ typedef struct {
     size_t scratch_bytes;
 } nvfp4_kv_prefixes;
 
-/* Two or three kernels: the prefixes, the requests' own keys, and with few rows a request
- * the join of the two. */
+/* Two kernels, the prefixes and the requests' own keys, which join the two; with few rows a
+ * request three: the own keys are taken beside the prefixes, and a third kernel joins. */
 int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
                               const nvfp4_kv_prefixes* prefixes, uint32_t options,
                               void* workspace, size_t workspace_bytes, void* stream);

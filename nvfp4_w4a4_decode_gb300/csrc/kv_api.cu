@@ -476,7 +476,8 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
     if (p.groups < 0 || p.max_blocks < 0 || p.table_stride < p.max_blocks ||
         (p.group_start == nullptr && p.groups > 1))
         return NVFP4_ERR_INVALID_ARG;
-    if (p.groups > nvfp4::kKvMaxReqs || p.max_blocks >= (kMaxTokens >> a.c.page_shift))
+    if (p.groups > nvfp4::kKvMaxReqs || p.max_blocks >= (kMaxTokens >> a.c.page_shift) ||
+        args->tokens * args->num_q_heads > INT32_MAX)
         return NVFP4_ERR_UNSUPPORTED;
     if (!any)
         return NVFP4_OK;

@@ -3,12 +3,14 @@
 //     L = sum l_k 2^(m_k - M),  out = v_g / L sum o_k 2^(m_k - M),  lse = ln L + M ln 2,
 // added up in one order, first the prefix's parts, then the own ones.
 //
-// A warp a row: its lanes take the parts' references and sums, 32 at a time, then four elements
-// each of all parts, eight loads on their way at once.  What bounds it: two loads that wait for
-// one another (where the parts lie, the parts); its launch is hidden by the passes (64 tokens of 32
-// heads, 17 parts of a prefix each: 11 us alone with nothing cached, 3 us behind the passes; with the
-// parts added up by the second pass at its items' starts the call took 46.2 us instead of 45.5, a call
-// of two tokens 17.7 instead of 14.5).
+// A warp a row, and a CTA: its lanes take the parts' references and sums, 32 at a time, then four
+// elements each of all parts, sixteen loads on their way at once.  What bounds it: three loads that
+// wait for one another (where the parts lie, their statistics, the parts), and L2 (64 tokens of 32
+// heads, 17 parts each of a prefix and one or two of the own keys: 20 MB, 4 us behind the passes); its
+// launch is hidden by them.  The call took 41.6 us with eight loads and four warps a CTA, 40.6 with
+// sixteen loads, and two requests on 60000 tokens 29.9, 28.9 and with a warp a CTA 27.4.  (With the prefix's
+// parts added up by the other pass at its items' starts a call of two tokens behind 1030 took 17.7 us
+// instead of 14.5.)
 #include <cuda_bf16.h>
 
 #include "kv.cuh"
@@ -18,14 +20,12 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWarps = 4;
-
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) kv_join_kernel(const KvAttnArgs a)
+__global__ void __launch_bounds__(32) kv_join_kernel(const KvAttnArgs a)
 {
     kv_pdl_begin();
-    const int lane = threadIdx.x & 31, heads = a.c.heads * a.group;
-    const int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x, heads = a.c.heads * a.group;
+    const int64_t at = blockIdx.x;
     const int64_t t = kv_divide(at, heads);
     // rows of no request are the second pass's to write
     int32_t begin = 0, end = a.tokens;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_join_kernel(const KvAttnArgs a
         float2 ml = make_float2(-INFINITY, 0.f);
         if (lane < n)
             ml = __ldcg((w ? s.part_stats : s.stats) + row);
-        constexpr int kAhead = 8;
+        constexpr int kAhead = 16 / kAbreast;
         float4 x[kAhead];
         auto load = [&](int z0) {
 #pragma unroll
@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_join_kernel(const KvAttnArgs a
 cudaError_t launch_kv_join(const KvAttnArgs& a, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)a.tokens * a.c.heads * a.group;
-    const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
-    return kv_launch(a.c.dim == 128 ? kv_join_kernel<128> : kv_join_kernel<64>, grid, 32 * kWarps, 0, stream, true,
+    return kv_launch(a.c.dim == 128 ? kv_join_kernel<128> : kv_join_kernel<64>, (unsigned)rows, 32, 0, stream, true,
                      a);
 }
 

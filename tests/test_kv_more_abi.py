@@ -139,6 +139,7 @@ def test_shared_refusals_of_the_attention(lib):
     f = lib.nvfp4_kv_attention_shared
     for change, status in ((dict(window=4), INVALID), (dict(reqs=-1), INVALID), (dict(max_q=-1), INVALID),
                            (dict(num_q_heads=8 * 65, q_stride=1 << 20, out_stride=1 << 20), UNSUPPORTED),
+                           (dict(num_q_heads=512, tokens=1 << 22, q_stride=1 << 20, out_stride=1 << 20), UNSUPPORTED),
                            (dict(out=None), INVALID), (dict(tokens=0), OK), (dict(reqs=0), OK)):
         assert f(cache(), attention(**change), prefixes(), 0, None, 0, None) == status
     assert f(cache(), attention(), None, 0, None, 0, None) == INVALID
