@@ -233,7 +233,9 @@ int64_t nvfp4_kv_attention_workspace_size(int64_t head_dim);
  * Cross attention: every query row of request r sees all seq_len[r] tokens that the
  * cache holds for it (the states of an encoder, say), however many rows it has; with
  * seq_len[r] = 0 they get zeros and lse = -inf.  All else, the workspace too, as for
- * nvfp4_kv_attention; args->window is 0 (else NVFP4_ERR_INVALID_ARG).  One kernel.
+ * nvfp4_kv_attention; args->window is 0 (else NVFP4_ERR_INVALID_ARG).  out may be q itself (the
+ * same address, type and stride); any other overlap of out or lse with q, the pool or each other
+ * is refused.  One kernel.
  */
 int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* args,
                              uint32_t options, void* workspace, size_t workspace_bytes,
@@ -255,7 +257,7 @@ int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attenti
  * end with a page (the rest of its last page is a request's own page then), and may be
  * empty (0 or less).
  * args->window is 0 (else NVFP4_ERR_INVALID_ARG), tokens * num_q_heads below 2^31 (else
- * NVFP4_ERR_UNSUPPORTED).  Options, workspace, statuses and what is done about bad entries as for
+ * NVFP4_ERR_UNSUPPORTED); out as for nvfp4_kv_cross_attention.  Options, workspace, statuses and what is done about bad entries as for
  * nvfp4_kv_attention, for both tables; the kernel choice of the options is that of both passes.
  */
 typedef struct {

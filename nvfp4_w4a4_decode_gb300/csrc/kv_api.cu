@@ -221,6 +221,22 @@ int check_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* 
     return NVFP4_OK;
 }
 
+// Whether an attention call writes over what it, or another of its CTAs, reads.  In place is fine: a
+// row's output is written once all CTAs that take a part of its keys have read the row (but for the
+// prefix's pass over a row that shares nothing, whose results nothing reads).
+bool writes_over(const nvfp4::KvAttnArgs& a)
+{
+    const int64_t heads = (int64_t)a.c.heads * a.group, row = heads * a.c.dim;
+    const Span q = token_rows(a.q, a.tokens, a.q_stride, row, a.q_bf16 ? 2 : 4, false);
+    const Span out = token_rows(a.out, a.tokens, a.out_stride, row, a.out_bf16 ? 2 : 4, true);
+    const Span pool = {reinterpret_cast<uintptr_t>(a.c.pool), a.c.num_pages, a.c.page_stride,
+                       nvfp4_kv_page_bytes((int64_t)1 << a.c.page_shift, a.c.heads, a.c.dim), false};
+    const Span lse = vec(a.lse, a.lse ? a.tokens * heads : 0, true);
+    const bool in_place = a.out == a.q && a.out_bf16 == a.q_bf16 && (a.out_stride == a.q_stride || a.tokens == 1);
+    return (!in_place && rows_meet(out, q)) || rows_meet(out, pool) || meets(lse, q) || meets(lse, out) ||
+           meets(lse, pool);
+}
+
 template <KvSees S>
 bool takes_tile(const nvfp4::KvAttnArgs& a, uint32_t options)
 {
@@ -446,6 +462,8 @@ int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attenti
     if (args != nullptr && args->window != 0)
         return NVFP4_ERR_INVALID_ARG;
     const int st = check_attention(cache, args, options, workspace, workspace_bytes, &a, &any);
+    if (st == NVFP4_OK && any && writes_over(a))
+        return NVFP4_ERR_INVALID_ARG;
     return st != NVFP4_OK || !any
                ? st
                : launch_attention<KvSees::kAll>(a, options, workspace, workspace_bytes, stream);
@@ -481,6 +499,8 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
         return NVFP4_ERR_UNSUPPORTED;
     if (!any)
         return NVFP4_OK;
+    if (writes_over(a))
+        return NVFP4_ERR_INVALID_ARG;
     if (p.groups == 0 || a.reqs == 0)
         return launch_attention<KvSees::kCausal>(a, options, workspace, workspace_bytes, stream);
     const int64_t rows = (int64_t)a.tokens * args->num_q_heads;
@@ -519,7 +539,8 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
         return first;
     a.status = g.status;
     a.prefix = of[0];
-    a.prefix.item_rows = takes_tile<KvSees::kAll>(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
+    a.prefix.item_rows =
+        takes_tile<KvSees::kAll>(g, options) ? nvfp4::kv_tile_item_rows() : nvfp4::kv_rows_item_rows(g);
     const bool joins = takes_tile<KvSees::kBehind>(a, options);
     if (!joins) {
         a.keep = of[1];

@@ -275,7 +275,7 @@ def nvfp4_kv_cross_attention(cache: KVCache, q, block_table, seq_len, q_start=No
     request: the states of an encoder, of any length beside the request's rows.
 
     ``seq_len`` int32 [reqs]: states in the cache (written by ``kv_append``); every row of a
-    request sees all of them, and with 0 gets zeros and lse = -inf.  ``pdl``: the launch may begin
+    request sees all of them, and with 0 gets zeros and lse = -inf.  ``out`` may be q itself.  ``pdl``: the launch may begin
     while the kernel in front of it ends, which it waits for before its first access.  All else as
     for ``kv_attention``."""
     stream = _stream(_current(cache._dev))
@@ -300,7 +300,7 @@ def nvfp4_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len, block
     tokens from b * page_size on, of which those wholly inside the prefix are not looked up.
     (Tables, slots and positions of ``kv_tables`` fit as they are.)  A request with a row inside the
     prefix, or with no tokens, shares nothing: it is attended on its own pages alone.  ``kernel``
-    forces the kernel of both passes; ``pdl``: the first launch may begin while the kernel in front
+    forces the kernel of both passes; ``out`` may be q itself; ``pdl``: the first launch may begin while the kernel in front
     of it ends, which it waits for before its first access.  A call takes scratch memory of about 1 KB
     a row and query head (at head_dim 128), and 81 MB.  All else as for ``kv_attention``."""
     stream = _stream(_current(cache._dev))

@@ -737,3 +737,89 @@ def test_starts_that_go_back_lead_nowhere(nv):
     nv.device_status(clear=True)
     out, _ = s.call(nv)
     assert torch.equal(out, want) and nv.device_status() == 0
+
+
+# ---- calls beside one another -----------------------------------------------------------------
+
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+def test_two_streams_and_two_graphs(nv, kernel, dtype):
+    """Calls of one cache on two streams at once, and two graphs replayed beside them, with the default
+    workspaces and scratch: the bits of calls that run alone."""
+    s = Shared(nv, [(3000, [(50 + i, 1) for i in range(6)] + [(70, 40)]), (500, [(9, 2)])], 8, 2, 64, 16, dtype)
+    args = dict(kernel=getattr(nv, kernel))
+    table, lens, start = s.args["prefix_table"], ints([3000, 500]), ints([0, 46, 48])
+
+    def both():
+        a, al = s.call(nv, **args)
+        b, bl = nv.kv_cross_attention(s.cache, s.q, table, lens, start, max_q=46, return_lse=True, **args)
+        return a, al, b, bl
+
+    want = [x.clone() for x in both()]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, results = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            results.append(both())
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for x in itertools.chain(*results):
+            x.fill_(math.nan)
+        torch.cuda.synchronize()
+        for i in range(4):
+            with torch.cuda.stream(streams[i % 2]):
+                got.append(both())
+                if i < 2:
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        for r in got + results:
+            for x, w in zip(r, want):
+                assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+def test_tables_with_strides(nv, kernel, dtype):
+    """Tables that are parts of wider ones, with more columns than are used."""
+    s = Shared(nv, [(100, [(5, 1), (60, 9)]), (33, [(9, 2)])], 8, 2, 64, 16, dtype)
+    args = dict(kernel=getattr(nv, kernel))
+    want, want_lse = s.call(nv, **args)
+    wide = []
+    for t in (s.prefix_table, s.table):
+        w = torch.full((t.shape[0], t.shape[1] + 13), -5, dtype=torch.int32, device="cuda")
+        w[:, 4:4 + t.shape[1]] = t
+        wide.append(w[:, 4:4 + t.shape[1]])
+    out, lse = s.call(nv, prefix_table=wide[0], block_table=wide[1], **args)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    one, one_lse = nv.kv_cross_attention(s.cache, s.q[:2], wide[0], ints(s.prefix), max_q=1, return_lse=True, **args)
+    two, two_lse = nv.kv_cross_attention(s.cache, s.q[:2], s.prefix_table, ints(s.prefix), max_q=1, return_lse=True,
+                                         **args)
+    assert torch.equal(one, two) and torch.equal(one_lse, two_lse)
+
+
+def test_more_groups_than_a_warp_takes(nv):
+    """More than 32 groups with long prefixes: shares of one list, cut anywhere."""
+    for kernel, dtype in KERNELS:
+        run_shared(nv, [(700 + 13 * g, [(5 + g, 1), (9, 2)]) for g in range(40)], 8, 2, 64, 16, dtype, kernel=kernel)
+        run_shared(nv, [(9000, [(5, 1)])] + [(g, [(5 + g, 3)]) for g in range(1, 33)], 8, 2, 64, 64, dtype, kernel=kernel)
+
+
+@pytest.mark.parametrize("kernel,dtype", KERNELS)
+@pytest.mark.parametrize("rows", [1, 40])
+def test_in_place(nv, kernel, dtype, rows):
+    """The output over the queries (heads of a wider row), with and without cut items: the same bits."""
+    s = Shared(nv, [(9000, [(50, rows), (700, rows)]), (300, [((200,), rows), (1 + rows, rows)])], 8, 2, 128, 16, dtype)
+    args = dict(kernel=getattr(nv, kernel))
+    table, lens, start = s.args["prefix_table"], ints([9000, 300]), ints([0, 2 * rows, 4 * rows])
+    for call in (lambda q, **more: s.call(nv, q, **args, **more),
+                 lambda q, **more: nv.kv_cross_attention(s.cache, q, table, lens, start, return_lse=True, **args, **more)):
+        want, want_lse = call(s.q)
+        wide = torch.cat((s.q, s.q, s.q), 1)
+        q, rest = wide[:, 8:16], wide[:, 16:].clone()
+        out, lse = call(q, out=q)
+        assert out.data_ptr() == q.data_ptr()
+        assert torch.equal(q, want) and torch.equal(lse, want_lse)
+        assert torch.equal(wide[:, :8], s.q) and torch.equal(wide[:, 16:], rest)
+        with pytest.raises(nv.Nvfp4Error):
+            call(q, out=wide[:, 9:17])

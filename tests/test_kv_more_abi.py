@@ -151,6 +151,28 @@ def test_shared_refusals_of_the_attention(lib):
     assert f(cache(), attention(tokens=0), prefixes(groups=-1), 0, None, 0, None) == INVALID
 
 
+APART = dict(q=FAKE, out=FAKE + MB, lse=FAKE + 2 * MB)
+
+
+@pytest.mark.parametrize("change,options", [
+    (dict(out=FAKE + 16), 0), (dict(out=FAKE - 16), 0), (dict(out=FAKE + 16), 0xC00), (dict(out=FAKE), 0x400),
+    (dict(out=FAKE, out_stride=8192), 0), (dict(out=FAKE + 16 * MB), 0), (dict(out=FAKE + 16 * MB - 16), 0),
+    (dict(lse=FAKE + 4), 0), (dict(lse=FAKE + MB + 4), 0), (dict(lse=FAKE + 16 * MB), 0), (dict(lse=FAKE - 4), 0)])
+def test_attention_does_not_write_over_what_it_reads(lib, change, options):
+    a = attention(**{**APART, **change})
+    assert lib.nvfp4_kv_cross_attention(far_cache(), a, options, None, 0, None) == INVALID
+    assert lib.nvfp4_kv_attention_shared(far_cache(), a, prefixes(), options, None, 0, None) == INVALID
+    assert lib.nvfp4_kv_attention_shared(far_cache(), a, prefixes(groups=0), options, None, 0, None) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls go on to the device's status word")
+@pytest.mark.parametrize("change", [dict(), dict(out=FAKE), dict(lse=None), dict(out=FAKE + 48 * 16384),
+                                    dict(out=FAKE + 16384, q_stride=8192, out_stride=8192)])
+def test_attention_takes_operands_that_do_not_meet(lib, change):
+    a = attention(**{**APART, **change})
+    assert lib.nvfp4_kv_cross_attention(far_cache(), a, 0, None, 0, None) == CUDA
+
+
 def test_scratch_size(lib):
     f = lib.nvfp4_kv_shared_scratch_size
     for dim in (64, 128):
