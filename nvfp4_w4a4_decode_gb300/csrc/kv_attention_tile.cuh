@@ -42,7 +42,11 @@
 // PFLOP/s.  There a tile's block takes 3490 cycles, 1790 from scores to probabilities and 1700 until the next
 // scores are there (1024 of its own products).  Exponentials are not what bounds it: with an eighth of them
 // on the FMA pipe (a polynomial) the prefix took 7 % longer.  Neither are the loads of scores: 64 columns at
-// once instead of twice 32 cost registers that are not there (6 % longer).
+// once instead of twice 32 cost registers that are not there (6 % longer), 16 on their way while 16 are used
+// gained nothing.  Probabilities handed over by halves of a block (their products with V under the other
+// half's exponentials) took 4 % longer, scores by halves too (two 64-key buffers a tile) 26 %: twice the
+// products with half the columns take nearly twice the time.  Runs with work left out, of 1700 us: half of
+// all products 1541, no decoded stores 1540, no exponentials 1619; no single one of them bounds it.
 // A prefix for few rows (64 tokens of 32 heads on 8003 keys: 21 us, 136 CTAs of four blocks) pays a start of
 // 18000 cycles a CTA: list 3600, queries 6900, the first block's scores 1200, its softmax 5400 (most of it
 // for instructions).
