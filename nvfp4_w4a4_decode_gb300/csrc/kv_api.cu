@@ -222,8 +222,8 @@ int check_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attention_args* 
 }
 
 // Whether an attention call writes over what it, or another of its CTAs, reads.  In place is fine: a
-// row's output is written once all CTAs that take a part of its keys have read the row (but for the
-// prefix's pass over a row that shares nothing, whose results nothing reads).
+// row's output is written once all CTAs that take a part of its keys have read the row, those of the
+// prefix's pass, which takes all rows of a group, among them.
 bool writes_over(const nvfp4::KvAttnArgs& a)
 {
     const int64_t heads = (int64_t)a.c.heads * a.group, row = heads * a.c.dim;

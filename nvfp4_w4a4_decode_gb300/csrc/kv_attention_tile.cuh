@@ -759,8 +759,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                 top = mt;
                 float by = 1.f;
                 if constexpr (S == KvSees::kBehind) {
-                    if (it.q.low > 0) {
+                    // The prefix's pass takes every row of its groups, those that share nothing too:
+                    // outputs over the queries are written once it has read them (a row changed under
+                    // it would raise its neighbours' references by chance).
+                    if (it.q.low > 0 || a.out == a.q)
                         kv_pdl_wait();
+                    if (it.q.low > 0) {
                         where = kv_where(a.prefix, row_at(), parts);
                         for (int k = 0; k < parts; ++k)
                             top = fmaxf(top, part_stats(k).x);

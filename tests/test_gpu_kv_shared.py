@@ -823,3 +823,28 @@ def test_in_place(nv, kernel, dtype, rows):
         assert torch.equal(wide[:, :8], s.q) and torch.equal(wide[:, 16:], rest)
         with pytest.raises(nv.Nvfp4Error):
             call(q, out=wide[:, 9:17])
+
+
+@pytest.mark.parametrize("kernel", ["KERNEL_AUTO", "KERNEL_KV_TILE"])
+@pytest.mark.parametrize("rows,reqs", [(7, 40), (40, 60)])
+def test_in_place_beside_rows_inside_the_prefix(nv, kernel, rows, reqs):
+    """Requests with rows inside their prefix between such that share it, the output over the queries: the
+    prefix's pass takes rows of both side by side, and the first ones' outputs must not come under it.
+    Their queries are large, so that a row read half old and half new would move its neighbours'
+    references and with them their last bits.  (40 rows of 60 requests: the own keys on the tcgen05 kernel by
+    the library's choice too.)"""
+    group = [((50 + 9 * r,), rows) if r % 2 else (rows + 3 * r, rows) for r in range(reqs)]
+    s = Shared(nv, [(9000, group), (5000, group[::-1])], 8, 2, 128, 16, BF16)
+    q = s.q.clone().view(-1, rows, 8, 128)
+    q[1:reqs:2] *= 40.0
+    q[reqs::2] *= 40.0  # the second group begins with one of them (reqs is even)
+    q = q.flatten(0, 1)
+    args = dict(kernel=getattr(nv, kernel))
+    want, want_lse = s.call(nv, q, **args)
+    assert not torch.equal(want, q)
+    check_attention(want, want_lse, s.ref(q=q), BF16)
+    for _ in range(30):
+        mine = q.clone()
+        out, lse = s.call(nv, mine, out=mine, **args)
+        assert out.data_ptr() == mine.data_ptr()
+        assert torch.equal(mine, want) and torch.equal(lse, want_lse)
