@@ -713,6 +713,44 @@ def test_cross_probabilities_are_rounded_once(nv, name):
     check_attention(out, lse, ref, BF16)
 
 
+@pytest.mark.parametrize("name", ["KERNEL_KV_ROWS", "KERNEL_KV_TILE"])
+@pytest.mark.parametrize("form", ["causal", "cross", "prefix", "behind"])
+def test_small_probabilities_stay_where_the_reference_rises(nv, form, name):
+    """A probability is held to 2^-32 of its row's largest (the bound's reach) also where the reference rises
+    far inside a block: 64 keys with values of 1, then 16 keys that are 2^18 to 2^36 times as probable, with
+    values of 0, so that the output is what is left of the first ones."""
+    n, rows, group = 384, 64, 64
+    unit = 1.4426950408889634  # scores below are in powers of two
+    cache, table, gen = make(nv, [(0, n)], 1, 64, 16)
+    table = table.cuda()
+    k = torch.zeros((n, 1, 64), device="cuda")
+    k[128:192, 0, 0] = 6.0
+    k[192:208, 0, 16] = 6.0
+    k[208:, 0, 32] = -6.0  # as good as unseen
+    v = torch.zeros((n, 1, 64), device="cuda")
+    v[128:192] = 1.0
+    cache.k_g.fill_(1.0)
+    cache.v_g.fill_(1.0)
+    slots = table[0, :n // 16].long().repeat_interleave(16) * 16 + torch.arange(n, device="cuda") % 16
+    nv.kv_append(cache, k, v, slots)
+    q = torch.zeros((rows, group, 64), device="cuda")
+    q[..., 0] = 30.0 / 6.0
+    q[..., 16] = (48.0 + 18.0 * torch.rand((rows, group), generator=gen, device="cuda")) / 6.0
+    q[..., 32] = 10.0
+    q = q.to(BF16)
+    # (no workspace: a request's keys stay with one SM, in order)
+    args = dict(scale=1.0 / unit, return_lse=True, kernel=getattr(nv, name), workspace=False)
+    if form == "causal":
+        out, lse = nv.kv_attention(cache, q, table, ints([n]), **args)
+    elif form == "cross":
+        out, lse = nv.kv_cross_attention(cache, q, table, ints([n]), **args)
+    else:
+        out, lse = nv.kv_attention_shared(cache, q, table, ints([320 if form == "prefix" else 16]), table, ints([n]),
+                                          **args)
+    ref = attend(q, [table_values(cache, table[0], 0, n)], [rows], 1.0 / unit, causal=form != "cross")
+    check_attention(out, lse, ref, BF16)
+
+
 @pytest.mark.parametrize("kernel,dtype", KERNELS)
 def test_pages_and_layers(nv, kernel, dtype):
     """Strided pages (one pool for several layers), every page size, prefixes that end inside a page."""
