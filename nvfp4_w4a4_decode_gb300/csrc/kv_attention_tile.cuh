@@ -652,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                             // The first reference as it comes; then a whole number of powers of
                             // two at a time, which takes nothing from probabilities already f16.
                             float by = 0.f;
-                            int down = 48;  // as far as f16 goes: 2^16 to 2^-25, which is 0
                             if (m == -INFINITY) {
                                 m = best - kLift;
                             } else {
@@ -660,27 +659,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                 m += steps;
                                 if (steps < 127.f)
                                     by = __int_as_float((127 - (int)steps) << 23);
-                                if (steps < 48.f)
-                                    down = (int)steps;
                             }
                             l *= by;
-                            // The output so far (its products are complete: this block's scores
-                            // were issued after them, and their commit covers both) and the
-                            // probabilities of the first half, over scores already used.
+                            // The probabilities of the first half, over scores already used, and the
+                            // output so far (its products are complete: this block's scores
+                            // were issued after them, and their commit covers both).
                             tmem_wait_st();
-                            if (u > it.u0) {
-#pragma unroll 1
-                                for (int i = 0; i < D; i += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tO + i, o);
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j)
-                                        o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-                                    tmem_st16(tO + i, o);
-                                }
-                            }
-                            // by two factors: one of 2^-25 or less would be 0 in f16, and a probability
-                            // of 2^7 is lost only with 2^-32
+                            // (f16 has no factor below 2^-24, so two of them: one of 2^15 at most, a
+                            // probability stays down to f16's 2^-24)
+                            const int down = 127 - (__float_as_int(by) >> 23);
                             const float by_a = __int_as_float((127 - (down >> 1)) << 23);
                             const float by_b = __int_as_float((127 - ((down + 1) >> 1)) << 23);
                             const uint32_t a16 = pack_f16(by_a, by_a), b16 = pack_f16(by_b, by_b);
@@ -692,6 +679,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const KvAttnArgs a
                                 for (int j = 0; j < 16; ++j)
                                     o[j] = f16x2_mul(f16x2_mul(o[j], a16), b16);
                                 tmem_st16(tS + i, o);
+                            }
+                            if (u > it.u0) {
+#pragma unroll 1
+                                for (int i = 0; i < D; i += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + i, o);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j)
+                                        o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+                                    tmem_st16(tO + i, o);
+                                }
                             }
                         }
                         l += sum;
