@@ -279,8 +279,8 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
                               const nvfp4_kv_prefixes* prefixes, uint32_t options,
                               void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of nvfp4_kv_prefixes.scratch on the current device, or minus a status code.  Host
- * only. */
+/* Bytes of nvfp4_kv_prefixes.scratch on the current device, or minus a status code (devices of
+ * more than 256 SMs: NVFP4_ERR_UNSUPPORTED).  Host only. */
 int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_t head_dim);
 
 #ifdef __cplusplus

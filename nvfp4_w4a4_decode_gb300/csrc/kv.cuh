@@ -116,6 +116,10 @@ constexpr int64_t kv_part_total(int sms)
     return (int64_t)(sms > 64 ? sms : 64) * 512;
 }
 
+// Devices of more SMs, whose rows `where` has no bits for, are refused.
+constexpr int kKvMostSms = 256;
+static_assert(kv_part_total(kKvMostSms) <= (int64_t)1 << kKvPartBits);
+
 // Part k's row of the parts that `where` names: the first lies in its CTA's second place, the
 // others in the first places of the CTAs behind.
 __device__ __forceinline__ int64_t kv_part_row(int32_t where, int k, int item_rows)

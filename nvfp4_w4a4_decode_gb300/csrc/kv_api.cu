@@ -473,7 +473,8 @@ int64_t nvfp4_kv_shared_scratch_size(int64_t tokens, int64_t num_q_heads, int64_
 {
     if (tokens < 0 || num_q_heads < 1 || head_dim < 1)
         return -NVFP4_ERR_INVALID_ARG;
-    if ((head_dim != 64 && head_dim != 128) || tokens >= kMaxTokens || num_q_heads > (1 << 22))
+    if ((head_dim != 64 && head_dim != 128) || tokens >= kMaxTokens || num_q_heads > (1 << 22) ||
+        sm_count() > nvfp4::kKvMostSms)
         return -NVFP4_ERR_UNSUPPORTED;
     const int64_t rows = tokens * num_q_heads;
     return 2 * (pass_bytes(rows, head_dim) + rows * 4);
@@ -504,10 +505,12 @@ int nvfp4_kv_attention_shared(const nvfp4_kv_cache* cache, const nvfp4_kv_attent
     if (p.groups == 0 || a.reqs == 0)
         return launch_attention<KvSees::kCausal>(a, options, workspace, workspace_bytes, stream);
     const int64_t rows = (int64_t)a.tokens * args->num_q_heads;
+    const int64_t scratch = nvfp4_kv_shared_scratch_size(a.tokens, args->num_q_heads, a.c.dim);
+    if (scratch < 0)
+        return (int)-scratch;
     if (p.prefix_len == nullptr || (p.max_blocks > 0 && p.block_table == nullptr) || p.scratch == nullptr ||
         !aligned(p.prefix_len, 4) || !aligned(p.block_table, 4) || !aligned(p.group_start, 4) ||
-        !aligned(p.scratch, 32) ||
-        (int64_t)p.scratch_bytes < nvfp4_kv_shared_scratch_size(a.tokens, args->num_q_heads, a.c.dim))
+        !aligned(p.scratch, 32) || (int64_t)p.scratch_bytes < scratch)
         return NVFP4_ERR_INVALID_ARG;
     const int64_t parts = nvfp4::kv_part_total(sm_count());
     nvfp4::KvParts of[2];
