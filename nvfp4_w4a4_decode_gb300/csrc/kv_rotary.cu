@@ -15,7 +15,7 @@
 // where the pairs are interleaved, or nothing is turned).  Its units are neighbouring
 // pieces of a head, so that a warp's loads and stores are runs of whole sectors.
 //
-// What bounds it: memory (16103 tokens of 32/8 heads of 128 in BF16: 357 MB in 60.6 us, 5.9 TB/s,
+// What bounds it: memory (16103 tokens of 32/8 heads of 128 in BF16: 357 MB in 60.2 us, 5.9 TB/s,
 // 88 % of the copy rate) once enough loads are on their way; few tokens the launch (8 tokens: 2.5 us).
 #include "../../include/nvfp4_kv.h"
 #include "kv.cuh"
@@ -28,13 +28,14 @@ namespace {
 
 constexpr int kThreads = 128;
 // With many tokens a thread turns four query heads by the angles it has loaded (two in FP32, whose
-// elements take twice the registers).  16103 tokens of 32/8 heads of 128 in BF16: 60.6 us; with
-// eight heads 88, two 69, one 114.  CTAs an SM, which the registers make room for: seven 60.6 us,
-// six 64, eight 63, nine 80, as many as come of themselves (five) 71.
+// elements take twice the registers), seven CTAs an SM.  Measured, 32/8 heads of 128: 16103 tokens in
+// BF16, 60.2 us; with eight heads 88, two 69, one 114; six CTAs an SM 64, eight 63, nine 80, as many as come
+// of themselves (five) 71.  19583 tokens in FP32, 124.7 us, 6.7 TB/s; with four heads 178, one 166; six, five
+// or as many as come of themselves 129.4, eight 128.5.
 template <bool BF16>
 constexpr int kManyHeads = BF16 ? 4 : 2;
-template <bool BF16, int U>
-constexpr int kCtas = U == 1 ? 1 : BF16 ? 7 : 6;
+template <int U>
+constexpr int kCtas = U == 1 ? 1 : 7;
 
 // (a, b) turned by (c, s), each operation rounded.
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s)
@@ -123,7 +124,7 @@ __device__ __forceinline__ Eight<BF16> pack(const float (&v)[8])
 // Units of a token: U query heads' pieces of 8 pairs (q_units), then pairs of blocks of K
 // and of V.
 template <bool BF16, bool WIDE, int U>
-__global__ void __launch_bounds__(kThreads, kCtas<BF16, U>)
+__global__ void __launch_bounds__(kThreads, kCtas<U>)
     kv_rotary_kernel(const KvRotaryArgs a, uint32_t per, uint32_t q_units, int q_groups)
 {
     kv_pdl_begin();
