@@ -242,8 +242,13 @@ int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attenti
                              void* stream);
 
 /*
- * Causal attention of requests that share prefixes, each prefix read and multiplied
- * once for all rows of its requests.  Group g is the requests group_start[g] up to
+ * Causal attention of requests that share prefixes, each prefix read not for every request
+ * but once a kv head for 256 rows (tokens times query heads of the kv head) of its requests on the
+ * tcgen05 kernel, for 8, 16 or 32 of them on the rows kernel, which takes FP32 always and short groups:
+ * the library chooses by the average rows of a group.  For few requests or a short prefix
+ * nvfp4_kv_attention with tables that spell the prefix out is faster (single tokens, 32 query heads of 128
+ * on 8 kv heads in BF16: 2 requests up to 8000 tokens, 8 up to 4000, 16 up to 2000, 64 up to 250; 14 query
+ * heads of 64 on 2 in FP32: 8 requests up to 30000, 64 up to 8000).  Group g is the requests group_start[g] up to
  * group_start[g + 1]; their first prefix_len[g] tokens are the same and lie on the pages of
  * row g of the prefixes' table.  Lengths and positions count them: in args, seq_len[r] is the
  * whole length, and entry b of a request's own row of args->block_table holds the tokens
@@ -257,8 +262,9 @@ int nvfp4_kv_cross_attention(const nvfp4_kv_cache* cache, const nvfp4_kv_attenti
  * end with a page (the rest of its last page is a request's own page then), and may be
  * empty (0 or less).
  * args->window is 0 (else NVFP4_ERR_INVALID_ARG), tokens * num_q_heads below 2^31 (else
- * NVFP4_ERR_UNSUPPORTED); out as for nvfp4_kv_cross_attention.  Options, workspace, statuses and what is done about bad entries as for
- * nvfp4_kv_attention, for both tables; the kernel choice of the options is that of both passes.
+ * NVFP4_ERR_UNSUPPORTED); out as for nvfp4_kv_cross_attention.  Options, workspace, statuses and what
+ * is done about bad entries as for nvfp4_kv_attention, for both tables; the kernel choice of the options is that
+ * of both passes.
  */
 typedef struct {
     const int32_t* block_table; /* int32 [groups][table_stride] */

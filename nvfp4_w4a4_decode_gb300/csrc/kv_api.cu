@@ -35,16 +35,26 @@ int64_t pass_bytes(int64_t rows, int64_t dim)
 // 142 / 91; one of 2000, 256 rows 30 / 36.  (The last lies on the rule's border and goes to
 // the slower one: neither lengths nor windows enter the rule, and one answer holds for
 // all requests of a call, so that single tokens beside a prompt go with the prompt.)
+// All keys (cross attention), requests x kv heads x rows on 100 / 1500 / 8000 states: of 128, 1 x 8 x 160 12 21
+// 39 / 11 30 58; 4 x 8 x 48 11 25 49 / 10 30 54; 8 x 8 x 24 10 25 50 / 10 34 70; 8 x 8 x 36 11 32 84 / 10 34 69;
+// 1 x 8 x 400 12 31 71 / 11 32 56; 32 x 8 x 36 35 83 295 / 16 60 204; of 64, 8 x 16 x 40 14 34 95 / 8 29 84; 64 x 4 x 40
+// 27 56 189 / 13 43 153.
 bool use_tile(int64_t reqs, int64_t heads, int64_t rows)
 {
     return rows > 32 && reqs * heads * rows >= 2048;
 }
 
 // The same for a prefix that requests share: its parts are joined by another kernel, so that items
-// cut between all SMs cost little.  Measured both ways (rows kernel / tile kernel for the prefix, us
-// a call; one group of single tokens, heads of 128, a prefix of 500 / 8000 / 60000 tokens): 16 rows of 8
-// kv heads 14.4 22 39 / 19.2 23 58; 24 rows 18.0 28 55 / 19.6 26 60; 48 rows 18.3 29 83 / 19.6 27 61; 264 rows
-// of 4 kv heads (500, 4000, 30000) 28 34 91 / 24 27 48.
+// cut between all SMs cost little.  `rows` is the average of the groups.  Measured both ways (rows kernel /
+// tile kernel for the prefix, us a call; single tokens of 8 kv heads of 128, a prefix of 500 / 2000 / 8000 / 60000
+// tokens).  One group of 16 rows 13.5 14 21 33 / 18 19 21 60, of 20 17 18 22 49 / 19 19 21 61, of 32 17 18 27 50 /
+// 19 19 21 63, of 64 18 24 31 80 / 20 20 26 67; four of 16 rows 17 24 35 139 / 20 26 43 205, of 20 24 25 40 208 /
+// 21 27 45 204, of 64 23 35 90 574 / 23 29 47 204; sixteen (up to 8000) of 16 rows 30 40 88 / 30 48 119, of 20 43 56
+// 121 / 36 52 137, of 32 49 69 154 / 40 57 148, of 64 80 108 228 / 60 77 152.  4 kv heads of 64, one group: of 32
+// rows 14 15 17 26 / 16 16 17 29, of 128 15 16 25 51 / 16 17 18 32.  264 rows of 4 kv heads (500, 4000, 30000) 28 34 91 /
+// 24 27 48.  From 17 to 48 rows neither wins by much; the rows kernel's items grow from 16 to 32 rows there.  Uneven
+// groups, 64 single tokens behind 8000 and 30 behind as many prefixes (13 rows on the average: the rows
+// kernel): prefixes of 8000 154 / 202, of 500 89 / 63.
 bool use_tile_for_prefix(int64_t rows)
 {
     return rows > 16;

@@ -52,8 +52,8 @@
 // join, about 9.5 us (one request of 1000); a launch's fixed parts measured in cycles: list 2300, queries
 // 1700, first units 2800, warps' join 1400, part and counter 2000, CTAs' join 5000.  Where every SM has one or
 // two short items each of these runs once, and a third to a half of a warp's time goes into fetching its
-// instructions (20 requests of 300..1500 states, 16 heads of 64: 14.6 us, no instruction 4.4 of 9.7 stalls
-// an issue; 16 tokens at a time instead of two times 16, half the code: 14.7 instead of 14.0).
+// instructions (20 requests of 300..1500 states, 16 heads of 64: 15.0 us, no instruction 4.4 of 9.7 stalls
+// an issue; 16 tokens at a time instead of two times 16, half the code, gained nothing).
 #pragma once
 
 #include "formats.cuh"
@@ -109,8 +109,9 @@ __device__ __forceinline__ int token_of_row(int k)
 // register files.  Three, with four CTAs an SM, for the few keys that requests mostly have behind a
 // shared prefix: an item's start and end, which wait for memory and for instructions, overlap
 // those of three other CTAs (seven / three warps, us: four requests of 300 tokens behind 2000 19.7 / 15.9, 64
-// of 30..900 41.0 / 38.3, 64 of 3000 83.8 / 87.3, eight of 20000 66.8 / 72.6; without a prefix, 64 of 100
-// 12.0 / 8.7, 20 of 300..1500 14.7 / 14.0, eight of 1500 12.0 / 13.8, 64 of 6000..8191 108.7 / 124.8).
+// of 30..900 41.0 / 38.3, but 64 of 3000 83.8 / 87.3, eight of 20000 66.8 / 72.6).  All keys are left to seven,
+// as their number is not known on the host (64 of 100 12.0 / 8.8, but 20 of 300..1500 15.0 / 16.0, eight of
+// 1500 12.1 / 13.4, 64 of 6000..8191 108.5 / 124.3).
 template <int D, int NT, bool SPLIT, int W>
 struct Cfg {
     static constexpr int kCompute = 32 * W;

@@ -35,10 +35,10 @@
 // (about 2600 cycles a block beside the 1024 of its products, of which the other
 // tile's run meanwhile) and shared memory, which the products of both tiles and the
 // decode's stores read and write 192 KB of a block, 1536 of its 2048 tensor
-// cycles.  2048 queries of 32 heads on 32049 keys: 768 us, 1.36 PFLOP/s; four prompts of
-// 2185..3879 tokens and 64 heads: 723 us, 0.94 PFLOP/s (an item's queries, first
+// cycles.  2048 queries of 32 heads on 32049 keys: 764 us, 1.37 PFLOP/s; four prompts of
+// 2185..3879 tokens and 64 heads: 735 us, 0.92 PFLOP/s (an item's queries, first
 // block, masked last block and output add about 9 us to its keys).  5065 rows of 64 heads on a shared
-// prefix of 12001 keys: 1500 us, 1.33 PFLOP/s; 2183 rows of 32 heads on 4000..6000 states: 177 us, 1.02
+// prefix of 12001 keys: 1500 us, 1.33 PFLOP/s; 2183 rows of 32 heads on 4000..6000 states: 180 us, 1.01
 // PFLOP/s.  There a tile's block takes 3490 cycles, 1790 from scores to probabilities and 1700 until the next
 // scores are there (1024 of its own products).  Exponentials are not what bounds it: with an eighth of them
 // on the FMA pipe (a polynomial) the prefix took 7 % longer.  Neither are the loads of scores: 64 columns at
